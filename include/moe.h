@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 7
+#define MOE_ABI_VERSION 8
 
 typedef enum {
   MOE_OK = 0,
@@ -367,6 +367,38 @@ int32_t moe_prenorm(int32_t T, int32_t H, const void* x, void* out, void* stream
 int32_t moe_residual_add(int32_t T, int32_t H, void* x, const float* y, void* stream);
 int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void* out,
                              void* stream);
+
+/* The norms around a block, fused with its gate, the residual scale and the
+ * residual add (one pass; for the step between the layers of a decoder that
+ * normalises before and after a block):
+ *   n_t   = post_norm ? y_t / sqrt(mean(y_t^2) + eps) * post_weight : y_t
+ *   x'_t  = bf16(x_t + scale * gate * n_t)
+ *   out_t = bf16(x'_t / sqrt(mean(x'_t^2) + eps) * pre_weight)
+ * in fp32 between the loads and the two roundings.
+ *   x     [dev] bf16 [T, H]
+ *   y     [dev] the block's output [T, H], y_dtype bf16 or fp32; NULL: there is
+ *         no block, out is the pre-norm of x (x_out, gate and post_weight must
+ *         be NULL)
+ *   gate  [dev] fp32, by gate_kind [T], [H] or [T, H]; not read with
+ *         MOE_GATE_NONE
+ *   post_weight, pre_weight  [dev] fp32 [H], NULL: no weight
+ *   x_out [dev] bf16 [T, H]: x', may be x itself (in place)
+ *   out   [dev] bf16 [T, H], or NULL: no pre-norm (after the last block); must
+ *         not be x, x_out or y
+ *   scale any float; eps >= 0 and finite; post_norm 0 or 1
+ * Any H from 1 to 49152 (MOE_EUNSUPPORTED above), and pointers aligned to
+ * their elements only.  A row depends on nothing but itself: rows with
+ * infinities or NaN leave the others as they are. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_TOKEN = 1,   /* one value for each token */
+  MOE_GATE_CHANNEL = 2, /* one for each of the H channels */
+  MOE_GATE_ELEMENT = 3
+} moe_gate;
+int32_t moe_residual_norm(int32_t T, int32_t H, const void* x, const void* y, int32_t y_dtype,
+                          const float* gate, int32_t gate_kind, const float* post_weight,
+                          const float* pre_weight, float scale, float eps, int32_t post_norm,
+                          void* x_out, void* out, void* stream);
 
 #ifdef __cplusplus
 }

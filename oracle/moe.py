@@ -228,3 +228,23 @@ def prenorm(x, eps: float = 1e-6) -> np.ndarray:
 def residual_add(x, y) -> np.ndarray:
     """x <- bf16(x + y)."""
     return codecs.bf16_rne(np.asarray(x, dtype=np.float64) + np.asarray(y, dtype=np.float64))
+
+
+def residual_norm(x, y, gate=None, post_weight=None, pre_weight=None, scale=1.0, eps=1e-6,
+                  post_norm=True):
+    """The norms around a block with its gate, residual scale and residual
+    add: (x' before its rounding to bf16, out of the rounded x' before its own
+    rounding).  gate broadcasts against [T, H]; y None: out of x alone."""
+    x = np.asarray(x, dtype=np.float64)
+    if y is not None:
+        n = np.asarray(y, dtype=np.float64)
+        if post_norm:
+            n = n / np.sqrt(np.mean(n * n, axis=1, keepdims=True) + eps)
+            if post_weight is not None:
+                n = n * np.asarray(post_weight, dtype=np.float64)
+        x = x + scale * (1.0 if gate is None else np.asarray(gate, dtype=np.float64)) * n
+    r = codecs.bf16_rne(x)
+    out = r / np.sqrt(np.mean(r * r, axis=1, keepdims=True) + eps)
+    if pre_weight is not None:
+        out = out * np.asarray(pre_weight, dtype=np.float64)
+    return x, out

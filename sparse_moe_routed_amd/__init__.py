@@ -119,10 +119,15 @@ _SIGS = {
                                           ctypes.c_void_p, ctypes.c_void_p]),
     "moe_residual_prenorm": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_residual_norm": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                           ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_float, ctypes.c_float, ctypes.c_int32,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
 }
 
 _lib = None
-ABI_VERSION = 7  # MOE_ABI_VERSION of include/moe.h this binding describes
+ABI_VERSION = 8  # MOE_ABI_VERSION of include/moe.h this binding describes
 
 
 def lib():
@@ -537,3 +542,84 @@ def residual_prenorm(x: torch.Tensor, y: torch.Tensor,
     _check("moe_residual_prenorm",
            lib().moe_residual_prenorm(T, H, _ptr(x), _ptr(y), _ptr(out), _stream()))
     return out
+
+
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ELEMENT = 0, 1, 2, 3
+
+
+def _raw_stream(device: torch.device):
+    """The current stream of `device` (the tensors' device, which is made the
+    current one by the caller when it is not)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on(device: torch.device):
+    """Makes `device` current for the launches below it; free when it is."""
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _NO_SWITCH
+
+
+class _NoSwitch:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _same_device(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, x is on {device}")
+
+
+def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torch.Tensor] = None,
+                  x_out: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  post_weight: Optional[torch.Tensor] = None,
+                  pre_weight: Optional[torch.Tensor] = None, scale: float = 1.0,
+                  eps: float = 1e-6, post_norm: bool = True, pre_norm: bool = True):
+    """moe_residual_norm: (x', out).  x' goes into x_out, or into x itself when
+    it is None; with pre_norm=False there is no out (None).  The gate's shape
+    says its kind: [T, 1], [H] or [T, H].  Without a block output (y=None) x
+    stays and out is its pre-norm."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected a [T, H] tensor")
+    T, H = x.shape
+    _dev(x, torch.bfloat16, "x")
+    _same_device(x.device, y=y, out=out, x_out=x_out, gate=gate, post_weight=post_weight,
+                 pre_weight=pre_weight)
+    kind, yd = GATE_NONE, Y_F32
+    if y is not None:
+        yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}.get(y.dtype)
+        if yd is None:
+            raise ValueError(f"y: expected float32 or bfloat16, got {y.dtype}")
+        _dev(y, y.dtype, "y", (T, H))
+        if x_out is None:
+            x_out = x
+        _dev(x_out, torch.bfloat16, "x_out", (T, H))
+    elif x_out is not None or gate is not None or post_weight is not None:
+        raise ValueError("x_out, gate and post_weight need a block output y")
+    if gate is not None:
+        kinds = {(T, 1): GATE_TOKEN, (H,): GATE_CHANNEL, (T, H): GATE_ELEMENT}
+        kind = kinds.get(tuple(gate.shape))
+        if kind is None:
+            raise ValueError(f"gate: expected shape ({T}, 1), ({H},) or ({T}, {H}), got {tuple(gate.shape)}")
+        _dev(gate, torch.float32, "gate")
+    if post_weight is not None:
+        _dev(post_weight, torch.float32, "post_weight", (H,))
+    if pre_weight is not None:
+        _dev(pre_weight, torch.float32, "pre_weight", (H,))
+    if pre_norm and out is None:
+        out = torch.empty_like(x)
+    if out is not None:
+        if not pre_norm:
+            raise ValueError("out: given with pre_norm=False")
+        _dev(out, torch.bfloat16, "out", (T, H))
+    p = lambda t: None if t is None else t.data_ptr()
+    with _on(x.device):
+        _check("moe_residual_norm", lib().moe_residual_norm(
+            T, H, x.data_ptr(), p(y), yd, p(gate), kind, p(post_weight), p(pre_weight), scale, eps,
+            int(bool(post_norm)), p(x_out), p(out), _raw_stream(x.device)))
+    return (x if y is None else x_out), out

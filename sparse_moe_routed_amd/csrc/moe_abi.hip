@@ -705,4 +705,46 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
                                                  static_cast<hipStream_t>(stream)));
 }
 
+int32_t moe_residual_norm(int32_t T, int32_t H, const void* x, const void* y, int32_t y_dtype,
+                          const float* gate, int32_t gate_kind, const float* post_weight,
+                          const float* pre_weight, float scale, float eps, int32_t post_norm,
+                          void* x_out, void* out, void* stream) {
+  if (T < 0 || T > kMaxTokens || H <= 0) return MOE_EINVAL;
+  if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
+  if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_ELEMENT) return MOE_EINVAL;
+  if (post_norm != 0 && post_norm != 1) return MOE_EINVAL;
+  if (!(eps >= 0.f) || eps > std::numeric_limits<float>::max()) return MOE_EINVAL;
+  if (H > moe::residual_norm_max_width()) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;  // nothing is read or written; pointers may be null
+  if (!x) return MOE_EINVAL;
+  if (y) {
+    if (!x_out || (gate_kind != MOE_GATE_NONE && !gate)) return MOE_EINVAL;
+    if (x_out == y) return MOE_EINVAL;
+  } else {
+    if (!out || x_out || gate || gate_kind != MOE_GATE_NONE || post_weight) return MOE_EINVAL;
+  }
+  if (out && (out == x || out == x_out || out == y)) return MOE_EINVAL;
+  if (post_weight && !post_norm) return MOE_EINVAL;
+  if (pre_weight && !out) return MOE_EINVAL;
+  if (!aligned(x, 2) || !aligned(y, y_dtype == MOE_Y_F32 ? 4 : 2) || !aligned(gate, 4) ||
+      !aligned(post_weight, 4) || !aligned(pre_weight, 4) || !aligned(x_out, 2) || !aligned(out, 2))
+    return MOE_EINVAL;
+  moe::ResidualNormArgs a{};
+  a.T = T;
+  a.H = H;
+  a.x = static_cast<const uint16_t*>(x);
+  a.y = y;
+  a.y_bf16 = y_dtype == MOE_Y_BF16;
+  a.gate = gate;
+  a.gate_kind = gate_kind;
+  a.post_w = post_weight;
+  a.pre_w = pre_weight;
+  a.scale = scale;
+  a.eps = eps;
+  a.post_norm = post_norm;
+  a.x_out = static_cast<uint16_t*>(x_out);
+  a.out = static_cast<uint16_t*>(out);
+  return hip_status(moe::launch_residual_norm(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -143,4 +143,21 @@ hipError_t launch_residual(uint16_t* x, const float* y, int T, int H, hipStream_
 hipError_t launch_residual_prenorm(uint16_t* x, const float* y, int T, int H, uint16_t* out,
                                    hipStream_t stream);
 
+// norms around a block with its gate and residual scale (moe_residual_norm)
+enum GateKind { kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateElement = 3 };
+struct ResidualNormArgs {
+  int T, H;
+  const uint16_t* x;
+  const void* y;  // fp32 or bf16, or null: the pre-norm alone
+  int y_bf16;
+  const float* gate;
+  int gate_kind;
+  const float *post_w, *pre_w;
+  float scale, eps;
+  int post_norm;
+  uint16_t *x_out, *out;
+};
+int residual_norm_max_width();
+hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream);
+
 }  // namespace moe
