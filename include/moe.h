@@ -368,6 +368,26 @@ int32_t moe_residual_add(int32_t T, int32_t H, void* x, const float* y, void* st
 int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void* out,
                              void* stream);
 
+/* The whole layer for a few tokens: moe_route and moe_forward of at most
+ * MOE_FEW_TOKENS tokens in two kernels (decode, where the six to nine launches
+ * of the two calls cost more than the weights of one token).  Formulas, routing
+ * order and quantisation are those of the two calls; sums run in another fixed
+ * order (a token's experts by index instead of by slot), so y agrees with
+ * moe_forward's to fp32 summation order and repeats bit for bit.
+ *   x [dev] bf16 [T, H]; router, experts as moe_route and moe_forward
+ *   ids [dev] int32 [T, k], gates [dev] fp32 [T, k], y [dev] [T, H]: written
+ *   ws [dev] workspace of ws_bytes >= moe_layer_few_workspace_size(dims, fmt, T),
+ *      256-byte aligned; its contents need no initialisation
+ * MOE_EUNSUPPORTED for T > MOE_FEW_TOKENS, and where T rows of max(H, F + 8)
+ * bf16 values exceed the GPU's shared memory (144 KiB: H up to 4608 at 16
+ * tokens) or an expert matrix exceeds 2^30 values.  Errors otherwise as
+ * moe_route and moe_forward.  Capturable in a HIP graph. */
+#define MOE_FEW_TOKENS 16
+size_t moe_layer_few_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens);
+int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_router* router,
+                      const moe_experts* experts, int32_t* ids, float* gates, void* y,
+                      int32_t y_dtype, void* ws, size_t ws_bytes, void* stream);
+
 /* The norms around a block, fused with its gate, the residual scale and the
  * residual add (one pass; for the step between the layers of a decoder that
  * normalises before and after a block):

@@ -119,6 +119,13 @@ _SIGS = {
                                           ctypes.c_void_p, ctypes.c_void_p]),
     "moe_residual_prenorm": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_layer_few_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims), ctypes.c_int32,
+                                                       ctypes.c_int32]),
+    "moe_layer_few": (ctypes.c_int32, [ctypes.POINTER(Dims), ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.POINTER(Router), ctypes.POINTER(Experts),
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                                       ctypes.c_void_p]),
     "moe_residual_norm": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                            ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                            ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
@@ -623,3 +630,57 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torc
             T, H, x.data_ptr(), p(y), yd, p(gate), kind, p(post_weight), p(pre_weight), scale, eps,
             int(bool(post_norm)), p(x_out), p(out), _raw_stream(x.device)))
     return (x if y is None else x_out), out
+
+
+FEW_TOKENS = 16  # MOE_FEW_TOKENS of include/moe.h
+
+
+def layer_few_workspace(dims: LayerDims, fmt: str, max_tokens: int = FEW_TOKENS,
+                        device="cuda") -> torch.Tensor:
+    d = dims.c()
+    n = int(lib().moe_layer_few_workspace_size(ctypes.byref(d), WFMT[fmt], int(max_tokens)))
+    if n == 0:
+        raise ValueError(f"moe_layer_few_workspace_size: invalid dims {dims}, format {fmt} or "
+                         f"max_tokens {max_tokens} (at most {FEW_TOKENS})")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
+              dims: LayerDims = LayerDims(), y_dtype: torch.dtype = torch.float32,
+              ids: Optional[torch.Tensor] = None, gates: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """moe_layer_few: route and forward of at most FEW_TOKENS tokens in two
+    kernels; (y [T, H], ids int32 [T, k], gates fp32 [T, k])."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected a [T, H] tensor")
+    T, dev = x.shape[0], x.device
+    _dev(x, torch.bfloat16, "x", (T, dims.hidden))
+    _dev(router.w_packed, torch.bfloat16, "w_packed", (3, dims.n_experts, dims.hidden))
+    if ids is None:
+        ids = torch.empty((T, dims.top_k), dtype=torch.int32, device=dev)
+    else:
+        _dev(ids, torch.int32, "ids", (T, dims.top_k))
+    if gates is None:
+        gates = torch.empty((T, dims.top_k), dtype=torch.float32, device=dev)
+    else:
+        _dev(gates, torch.float32, "gates", (T, dims.top_k))
+    if y is None:
+        y = torch.empty((T, dims.hidden), dtype=y_dtype, device=dev)
+    else:
+        _dev(y, y_dtype, "y", (T, dims.hidden))
+    if ws is None:
+        ws = layer_few_workspace(dims, experts.fmt, min(T, FEW_TOKENS), dev)
+    else:
+        _dev(ws, torch.uint8, "ws")
+    _same_device(dev, w_packed=router.w_packed, bias=router.bias, up=experts.up, down=experts.down,
+                 ids=ids, gates=gates, y=y, ws=ws)
+    yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}[y_dtype]
+    d = dims.c()
+    r = Router(router.w_packed.data_ptr(),
+               router.bias.data_ptr() if router.bias is not None else None)
+    e = experts.c()
+    with _on(dev):
+        _check("moe_layer_few", lib().moe_layer_few(
+            ctypes.byref(d), T, x.data_ptr(), ctypes.byref(r), ctypes.byref(e), ids.data_ptr(),
+            gates.data_ptr(), y.data_ptr(), yd, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
+    return y, ids, gates

@@ -111,6 +111,22 @@ Layout make_layout(const moe_dims* d, int32_t fmt, int32_t T) {
   return L;
 }
 
+// workspace of moe_layer_few: counters, partial logits, the intermediate
+struct FewLayout {
+  size_t ctr, part, act, total;
+};
+
+FewLayout few_layout(const moe_dims* d, int32_t T) {
+  const auto up = [](size_t n) { return (n + kAlign - 1) / kAlign * kAlign; };
+  const size_t rows = static_cast<size_t>(T);
+  FewLayout L{};
+  L.ctr = 0;
+  L.part = up(moe::kFewCounters * 4);
+  L.act = L.part + up(moe::kFewSlices * rows * d->n_experts * 4);
+  L.total = L.act + up(rows * d->top_k * d->ffn * 2);
+  return L;
+}
+
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
@@ -745,6 +761,55 @@ int32_t moe_residual_norm(int32_t T, int32_t H, const void* x, const void* y, in
   a.x_out = static_cast<uint16_t*>(x_out);
   a.out = static_cast<uint16_t*>(out);
   return hip_status(moe::launch_residual_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_layer_few_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens) {
+  if (!dims_ok(dims) || !fmt_ok(fmt) || max_tokens < 0 || max_tokens > moe::kFewTokens) return 0;
+  return few_layout(dims, max_tokens).total;
+}
+
+int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_router* router,
+                      const moe_experts* experts, int32_t* ids, float* gates, void* y,
+                      int32_t y_dtype, void* ws, size_t ws_bytes, void* stream) {
+  if (const moe_status ds = dims_check(dims)) return ds;
+  if (!experts || T < 0 || T > kMaxTokens) return MOE_EINVAL;
+  if (!fmt_ok(experts->fmt)) return MOE_EINVAL;
+  if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
+  if (T > moe::kFewTokens) return MOE_EUNSUPPORTED;
+  if (!moe::few_fits(T, dims->hidden, dims->ffn)) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;  // nothing is read or written; pointers may be null
+  if (!router || !router->w_packed || !x || !ids || !gates || !y) return MOE_EINVAL;
+  if (!experts->up || !experts->down) return MOE_EINVAL;
+  if (experts->fmt != kBF16 && (!experts->up_s || !experts->down_s)) return MOE_EINVAL;
+  if (experts->fmt == kNVFP4 && (!experts->up_bs || !experts->down_bs)) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(router->w_packed, 16) || !aligned(router->bias, 4) ||
+      !aligned(ids, 4) || !aligned(gates, 4) || !aligned(y, 16) || !bank_aligned(experts))
+    return MOE_EINVAL;
+  const FewLayout L = few_layout(dims, T);
+  if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
+  moe::FewArgs g{};
+  g.T = T;
+  g.H = dims->hidden;
+  g.F = dims->ffn;
+  g.E = dims->n_experts;
+  g.k = dims->top_k;
+  g.x = static_cast<const uint16_t*>(x);
+  g.w_router = static_cast<const uint16_t*>(router->w_packed);
+  g.bias = router->bias;
+  g.up = experts->up;
+  g.down = experts->down;
+  g.up_bs = experts->up_bs;
+  g.down_bs = experts->down_bs;
+  g.up_s = experts->up_s;
+  g.down_s = experts->down_s;
+  g.ctr = at<uint32_t>(ws, L.ctr);
+  g.part = at<float>(ws, L.part);
+  g.act = at<uint16_t>(ws, L.act);
+  g.ids = ids;
+  g.gates = gates;
+  g.y = y;
+  g.y_bf16 = y_dtype == MOE_Y_BF16;
+  return hip_status(moe::launch_few(experts->fmt, g, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -160,4 +160,30 @@ struct ResidualNormArgs {
 int residual_norm_max_width();
 hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream);
 
+// the whole layer for at most kFewTokens tokens (moe_layer_few)
+constexpr int kFewTokens = 16;
+constexpr int kFewSlices = 4;  // K slices of the partial logits
+// counters: [0] tickets, [1] up rounds done, then kAmaxSlots maxima of a
+constexpr int kFewAmax = 64;
+constexpr int kFewCounters = 128;
+struct FewArgs {
+  int T, H, F, E, k;
+  const uint16_t* x;
+  const uint16_t* w_router;  // packed [3, E, H]
+  const float* bias;
+  const void *up, *down;
+  const uint8_t *up_bs, *down_bs;
+  const float *up_s, *down_s;
+  float* part;     // [kFewSlices, T, E]
+  uint32_t* ctr;   // [kFewCounters]
+  uint16_t* act;   // [T * k, F]
+  int32_t* ids;
+  float* gates;
+  void* y;
+  int y_bf16;
+  int stage_rows;  // rows of a that the LDS stage holds (set by the launch)
+};
+bool few_fits(int T, int H, int F);
+hipError_t launch_few(int fmt, const FewArgs& g, hipStream_t stream);
+
 }  // namespace moe
