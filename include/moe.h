@@ -378,9 +378,10 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  *   ids [dev] int32 [T, k], gates [dev] fp32 [T, k], y [dev] [T, H]: written
  *   ws [dev] workspace of ws_bytes >= moe_layer_few_workspace_size(dims, fmt, T),
  *      256-byte aligned; its contents need no initialisation
- * MOE_EUNSUPPORTED for T > MOE_FEW_TOKENS, and where T rows of max(H, F + 8)
- * bf16 values exceed the GPU's shared memory (144 KiB: H up to 4608 at 16
- * tokens) or an expert matrix exceeds 2^30 values.  Errors otherwise as
+ * MOE_EUNSUPPORTED for T > MOE_FEW_TOKENS, and where T rows of H or F + 8
+ * bf16 values, H and F rounded up to 128, exceed 120 KiB of the GPU's shared
+ * memory (H up to 3840 and F up to 3712 at 16
+ * tokens), or an expert matrix exceeds 2^30 values.  Errors otherwise as
  * moe_route and moe_forward.  Capturable in a HIP graph. */
 #define MOE_FEW_TOKENS 16
 size_t moe_layer_few_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens);

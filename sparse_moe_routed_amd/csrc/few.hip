@@ -31,31 +31,139 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 16;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kTok = kFewTokens;        // MFMA columns
 constexpr int kMaxRows = kTok * 8;      // (token, slot) pairs
 constexpr int kRouterThreads = 256;
 
-// ---- partial logits: grid (E / 16, kFewSlices), 4 waves; the K steps are
-// dealt to slices and waves in contiguous ranges, the waves' sums added in
-// wave order.  Also clears the counters of the second kernel.
-__global__ __launch_bounds__(kRouterThreads) void few_router_kernel(
-    const uint16_t* __restrict__ x, const uint16_t* __restrict__ wp, int T, int H, int E,
-    float* __restrict__ part, uint32_t* __restrict__ ctr) {
+__device__ __forceinline__ bf16x8 fp8_frag(uint32_t w0, uint32_t w1) {
+  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+  return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// ---- activation quantisers, 8 values of one lane (the recipes of quant.hip)
+template <int FMT>
+struct TensorScale {
+  float s = 1.f;  // value = stored * s
+  float a = 0.f;  // FP8: 448 / amax; NVFP4: 6 s
+  __device__ explicit TensorScale(float amax) {
+    if constexpr (FMT == kFP8) {
+      s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
+      a = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
+    } else if constexpr (FMT == kNVFP4) {
+      s = amax > 0.f ? __fdiv_rn(amax, 2688.f) : 0.f;
+      a = 6.f * s;
+    }
+  }
+};
+
+__device__ __forceinline__ float amax8(u32x4 v) {
+  float m = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    m = fmaxf(m, fabsf(__uint_as_float(v[w] << 16)));
+    m = fmaxf(m, fabsf(__uint_as_float(v[w] & 0xffff0000u)));
+  }
+  return m;
+}
+
+// 8 bf16 values as the GEMM operand: dec(code) in bf16 (FP8), dec(code) *
+// dec(block scale) in fp16 (NVFP4; the other half of the 16-value block is on
+// the neighbouring lane, which must be active).  The values are those of the
+// encoders of moe_common.h; a code's sign may be that of -0, whose products
+// add nothing.
+template <int FMT>
+__device__ __forceinline__ u32x4 quantise8(u32x4 v, const TensorScale<FMT>& ts) {
+  if constexpr (FMT == kBF16) {
+    return v;
+  } else {
+    float f[8];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f[2 * w] = __uint_as_float(v[w] << 16);
+      f[2 * w + 1] = __uint_as_float(v[w] & 0xffff0000u);
+    }
+    if constexpr (FMT == kFP8) {
+      const uint32_t c0 = e4m3_encode4(f[0] * ts.a, f[1] * ts.a, f[2] * ts.a, f[3] * ts.a);
+      const uint32_t c1 = e4m3_encode4(f[4] * ts.a, f[5] * ts.a, f[6] * ts.a, f[7] * ts.a);
+      return __builtin_bit_cast(u32x4, fp8_frag(c0, c1));
+    } else {
+      float m = fabsf(f[0]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+      // quad_perm [1, 0, 3, 2]: the value of the neighbouring lane
+      const float mo = __builtin_bit_cast(
+          float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, m), 0xb1, 0xf, 0xf, false));
+      const uint32_t sb = ts.s > 0.f ? e4m3_encode(__fdiv_rn(fmaxf(m, mo), ts.a)) : 0u;
+      const f16x2 s2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb | (sb << 8), 1.0f, false);
+      const float sbf = static_cast<float>(s2[0]);
+      const float r = sbf > 0.f ? __fdiv_rn(1.f, sbf * ts.s) : 0.f;
+      // |f r| is at most 6 * (1 + 2^-4) / (1 - 2^-4) (0 for a zero scale): the
+      // hardware conversion saturates it to 6
+      uint32_t q = 0u;
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[0] * r, f[1] * r, 1.0f, 0);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[2] * r, f[3] * r, 1.0f, 1);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[4] * r, f[5] * r, 1.0f, 2);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[6] * r, f[7] * r, 1.0f, 3);
+      const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 0) * s2;
+      const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 1) * s2;
+      const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 2) * s2;
+      const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 3) * s2;
+      return u32x4{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
+                   __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
+    }
+  }
+}
+
+// ---- first kernel.  Workgroups [0, E / 16 * kFewSlices) write partial logits:
+// 16 experts over one K slice each, its K steps dealt to the 4 waves in
+// contiguous ranges, the waves' sums added in wave order.  The others (FP8,
+// NVFP4) quantise a part of the tokens each, the tensor's amax taken by every
+// one of them.  Workgroup 0 clears the counters of the second kernel.
+constexpr int kQuantGroups = 16;
+
+template <int FMT>
+__global__ __launch_bounds__(kRouterThreads) void few_router_kernel(FewArgs g) {
   constexpr int U = 6;  // K steps of loads in flight
   __shared__ f32x4 red[4][kWave];
+  const int T = g.T, H = g.H, E = g.E;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int eb = blockIdx.x, s = blockIdx.y;
-  if (eb == 0 && s == 0 && threadIdx.x < kFewCounters) ctr[threadIdx.x] = 0u;
+  const int n_router = E / 16 * kFewSlices;
+  if (blockIdx.x == 0)
+    for (int j = threadIdx.x; j < kFewCounters; j += kRouterThreads) g.ctr[j] = 0u;
+  if constexpr (FMT != kBF16) {
+    if (static_cast<int>(blockIdx.x) >= n_router) {
+      float* part = reinterpret_cast<float*>(red);
+      const u32x4* x = reinterpret_cast<const u32x4*>(g.x);
+      const int n8 = T * H / 8;
+      float m = 0.f;
+#pragma unroll 8
+      for (int i = threadIdx.x; i < n8; i += kRouterThreads) m = fmaxf(m, amax8(x[i]));
+      m = wave_max(m);
+      if (lane == 0) part[wave] = m;
+      __syncthreads();
+      const TensorScale<FMT> ts(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
+      const int b = static_cast<int>(blockIdx.x) - n_router;
+      if (b == 0 && threadIdx.x == 0) *g.x_scale = ts.s;
+      // pairs of chunks (a block's halves) stay together: the stride is even
+      for (int i = b * kRouterThreads + threadIdx.x; i < n8; i += kQuantGroups * kRouterThreads)
+        reinterpret_cast<u32x4*>(g.x_q)[i] = quantise8<FMT>(x[i], ts);
+      return;
+    }
+  }
+  const int eb = blockIdx.x / kFewSlices, s = blockIdx.x % kFewSlices;
   const int row = lane & 15;
   const int kq = (lane >> 4) * 8;
   const int steps = H / 32;
   const int i = s * 4 + wave;
   const int k0 = steps * i / (4 * kFewSlices), k1 = steps * (i + 1) / (4 * kFewSlices);
   const size_t n = static_cast<size_t>(E) * H;
-  const uint16_t* xr = x + static_cast<size_t>(min(row, T - 1)) * H + kq;
-  const uint16_t* hi = wp + static_cast<size_t>(eb * 16 + row) * H + kq;
+  const uint16_t* xr = g.x + static_cast<size_t>(min(row, T - 1)) * H + kq;
+  const uint16_t* hi = g.w_router + static_cast<size_t>(eb * 16 + row) * H + kq;
   const uint16_t* mid = hi + n;
   const uint16_t* lo = mid + n;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -88,27 +196,30 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = (lane >> 4) * 4 + r;
-      if (t < T) part[(static_cast<size_t>(s) * T + t) * E + eb * 16 + row] = v[r];
+      if (t < T) g.part[(static_cast<size_t>(s) * T + t) * E + eb * 16 + row] = v[r];
     }
   }
 }
 
-// ---- weight units.  A unit is what one wave loads of 16 weight rows with one
-// 16-byte load a lane (NVFP4: and one 2-byte load of block scales): lane l
-// holds row l % 16 and, with q = l / 16, the K values
-//   BF16   32 per unit:  8 at 32 u + 8 q                      (1 MFMA)
-//   FP8    64 per unit: 16 at 64 u + 16 q                     (2 MFMAs)
-//   NVFP4 128 per unit: 32 at 128 u + 32 q, two scale blocks  (4 MFMAs)
-// MFMA i of a unit multiplies values 8 i .. 8 i + 7 of each lane; the tokens'
-// operand is read at the same K values.  Loads go through a buffer descriptor
-// of one expert's matrix, so a unit past the end reads nothing and is zero.
+// ---- weight units.  A unit is what a wave takes of 16 weight rows at a time:
+//   BF16, FP8  one 128-byte line of each row (64 / 128 K values): two 16-byte
+//              loads a lane, 8 lanes to a row, so that every load instruction
+//              reads whole lines; the wave turns them into MFMA operand order
+//              through 2 KB of LDS of its own.  (Loading in operand order
+//              puts 16 rows on neighbouring lanes: every 16 lanes touch 16
+//              lines, and four tokens BF16 ran at 2.5 TB/s that way.)
+//   NVFP4      two 64-value steps of the panel layout (128 K values), which is
+//              operand order as it stands: one 16-byte load of codes and one
+//              2-byte load of block scales a lane
+// Loads go through a buffer descriptor of one expert's matrix, so a unit past
+// the end, or the part of a last unit past K, reads nothing and is zero.
 template <int FMT>
 struct Unit {
-  u32x4 v;
+  u32x4 v[FMT == kNVFP4 ? 1 : 2];
   uint32_t sb;
 };
 template <int FMT>
-constexpr int kUnitK = FMT == kBF16 ? 32 : (FMT == kFP8 ? 64 : 128);
+constexpr int kUnitK = FMT == kBF16 ? 64 : 128;
 
 template <int FMT>
 __host__ __device__ constexpr int units_of(int K) {
@@ -119,188 +230,169 @@ constexpr uint32_t kPastEnd = 0xffffff00u;  // beyond every matrix: reads as zer
 constexpr int kRawBuffer = 0x00027000;      // descriptor word 3: raw 32-bit data
 constexpr int kStreamOnce = 2;              // cache policy: non-temporal
 
-struct Matrix {
-  __amdgpu_buffer_rsrc_t codes, scales;
+// One expert's matrix for the 16 rows of a tile: descriptors, and this lane's
+// byte offsets in unit 0 (a unit further on adds a scalar).  DOWN selects the
+// FP8 code layout: row-major (up) or panels (down).
+template <int FMT, bool DOWN>
+struct Tile {
+  const uint8_t *codes, *scales;
+  uint32_t bytes;          // of the codes; a block scale for every 8 of them (NVFP4)
+  uint32_t at, at_last;    // codes; of the last unit (past K: kPastEnd)
+  uint32_t step, row8;     // from unit to unit, from rows 0..7 to 8..15
+  uint32_t row8_last;
+  uint32_t sat, sat_last;  // scales
+  int last;                // index of the last unit
+
+  // e: expert (matrix index), n0: first row, uniform over the wave
+  __device__ __forceinline__ void point(const void* w, const uint8_t* bs, int e, int n0, int N, int K) {
+    const int lane = threadIdx.x & 63;
+    const size_t n = static_cast<size_t>(N) * K;
+    const size_t size = FMT == kBF16 ? 2 * n : (FMT == kFP8 ? n : n / 2);
+    bytes = static_cast<uint32_t>(size);
+    codes = static_cast<const uint8_t*>(w) + size * e;
+    last = units_of<FMT>(K) - 1;
+    if constexpr (FMT == kNVFP4) {
+      scales = bs + n / 16 * e;
+      const int q = lane >> 4, p = n0 / kNvPanel, rows = nv_panel_rows(N, p);
+      const uint32_t pr = n0 + (lane & 15) - p * kNvPanel;
+      at = static_cast<uint32_t>(p) * kNvPanel * (K / 2) + (q >> 1) * rows * 32 + pr * 32 + (q & 1) * 16;
+      sat = static_cast<uint32_t>(p) * kNvPanel * (K / 16) + (q >> 1) * rows * 4 + pr * 4 + (q & 1) * 2;
+      step = 2 * rows * 32;
+      const bool in = (2 * last + (q >> 1)) * kNvStepK < K;
+      at_last = in ? at : kPastEnd;
+      sat_last = in ? sat : kPastEnd;
+    } else {
+      const int row = lane >> 3, ch = lane & 7;
+      const uint32_t width = FMT == kBF16 ? 2 * K : K;  // row bytes
+      const bool in = last * 128 + ch * 16 < static_cast<int>(width);
+      if constexpr (FMT == kFP8 && DOWN) {
+        const int p = n0 / kNvPanel, rows = nv_panel_rows(N, p), pr = n0 + row - p * kNvPanel;
+        const int sb = min(kFp8StepK, K - last * kFp8StepK);  // row bytes of the last step
+        const uint32_t base = static_cast<uint32_t>(p) * kNvPanel * K + ch * 16;
+        at = base + pr * kFp8StepK;
+        at_last = in ? base + pr * sb : kPastEnd;
+        step = rows * kFp8StepK;
+        row8 = 8 * kFp8StepK;
+        row8_last = in ? 8 * sb : 0;
+      } else {
+        at = static_cast<uint32_t>(n0 + row) * width + ch * 16;
+        at_last = in ? at : kPastEnd;
+        step = 128;
+        row8 = 8 * width;
+        row8_last = in ? row8 : 0;
+      }
+    }
+  }
+
+  // loads of unit u; none (zeros) unless `in`.  The scheduling fence keeps the
+  // loads of a stream in order, so that a wait for the oldest unit waits for no
+  // later one.
+  __device__ __forceinline__ Unit<FMT> load(int u, bool in) const {
+    const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(codes), 0, in ? static_cast<int>(bytes) : 0, kRawBuffer);
+    Unit<FMT> r{};
+    const bool tail = u == last;
+    if constexpr (FMT == kNVFP4) {
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(scales), 0, in ? static_cast<int>(bytes / 8) : 0, kRawBuffer);
+      r.sb = __builtin_amdgcn_raw_buffer_load_b16(rs, tail ? sat_last : sat, u * (step / 8), kStreamOnce);
+      r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, tail ? at_last : at, u * step, kStreamOnce);
+    } else {
+      const uint32_t o = tail ? at_last : at;
+      r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, o, u * step, kStreamOnce);
+      r.v[1] = __builtin_amdgcn_raw_buffer_load_b128(rc, o + (tail ? row8_last : row8), u * step, kStreamOnce);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    return r;
+  }
 };
 
+// acc += 16 weight rows of a unit times the tokens' values: lane l has weight
+// row and token column l % 16 and, of each MFMA, the K values of one 16-byte
+// chunk of the tokens.  x points at the unit's first chunk of this lane's
+// column, chunks lie dx bytes apart.  `turn` is the wave's 2 KB of LDS: chunk c
+// of a row lies at c ^ (row % 8), free of bank conflicts both ways.
 template <int FMT>
-__device__ __forceinline__ Matrix matrix_of(const void* w, const uint8_t* bs, int e, int N, int K) {
-  const size_t n = static_cast<size_t>(N) * K;
-  const size_t bytes = FMT == kBF16 ? 2 * n : (FMT == kFP8 ? n : n / 2);
-  Matrix m;
-  m.codes = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(static_cast<const uint8_t*>(w) + bytes * e), 0, static_cast<int>(bytes),
-      kRawBuffer);
-  if constexpr (FMT == kNVFP4)
-    m.scales = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(bs + n / 16 * e), 0,
-                                                 static_cast<int>(n / 16), kRawBuffer);
-  else
-    m.scales = m.codes;
-  return m;
-}
-
-// DOWN selects the FP8 code layout: row-major (up) or panels (down)
-template <int FMT, bool DOWN>
-__device__ __forceinline__ Unit<FMT> load_unit(const Matrix& m, int n0, int N, int K, int u, bool in) {
+__device__ __forceinline__ f32x4 mul_unit(const Unit<FMT>& w, const uint8_t* x, int dx,
+                                          uint8_t* turn, f32x4 acc) {
   const int lane = threadIdx.x & 63, q = lane >> 4;
-  const int n = n0 + (lane & 15);
-  uint32_t at;
-  Unit<FMT> r{};
-  if constexpr (FMT == kBF16) {
-    at = static_cast<uint32_t>(n) * (2 * K) + u * 64 + q * 16;
-  } else if constexpr (FMT == kFP8 && !DOWN) {
-    at = static_cast<uint32_t>(n) * K + u * 64 + q * 16;
-  } else if constexpr (FMT == kFP8) {
-    const int p = n0 / kNvPanel, rows = nv_panel_rows(N, p);
-    const int st = u >> 1, sb = min(kFp8StepK, K - st * kFp8StepK);
-    at = static_cast<uint32_t>(p) * kNvPanel * K + static_cast<uint32_t>(st) * rows * kFp8StepK +
-         (n - p * kNvPanel) * sb + (u & 1) * 64 + q * 16;
-  } else {
-    const int p = n0 / kNvPanel, rows = nv_panel_rows(N, p);
-    const int st = 2 * u + (q >> 1);  // 64-value step of this lane
-    in = in && st * kNvStepK < K;
-    const uint32_t pr = n - p * kNvPanel;
-    const uint32_t sat = static_cast<uint32_t>(p) * kNvPanel * (K / 16) +
-                         static_cast<uint32_t>(st) * rows * 4 + pr * 4 + (q & 1) * 2;
-    at = static_cast<uint32_t>(p) * kNvPanel * (K / 2) + static_cast<uint32_t>(st) * rows * 32 +
-         pr * 32 + (q & 1) * 16;
-    r.sb = __builtin_amdgcn_raw_buffer_load_b16(m.scales, in ? sat : kPastEnd, 0, kStreamOnce);
-  }
-  r.v = __builtin_amdgcn_raw_buffer_load_b128(m.codes, in ? at : kPastEnd, 0, kStreamOnce);
-  return r;
-}
-
-__device__ __forceinline__ bf16x8 fp8_frag(uint32_t w0, uint32_t w1) {
-  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
-  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
-  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
-  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
-  return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-}
-
-// acc += 16 weight rows of the unit times the tokens' values; tok(c) points at
-// the 16-byte chunk (8 values) c of this lane's token column
-template <int FMT, class Tok>
-__device__ __forceinline__ f32x4 mul_unit(const Unit<FMT>& w, int u, int last_chunk, Tok tok,
-                                          f32x4 acc) {
-  const int q = (threadIdx.x & 63) >> 4;
-  if constexpr (FMT == kBF16) {
-    const bf16x8 b = *reinterpret_cast<const bf16x8*>(tok(u * 4 + q));
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v), b, acc, 0, 0, 0);
-  } else if constexpr (FMT == kFP8) {
-    // E4M3 codes as bf16 (exact), so the products are exact in fp32
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bf16x8 b = *reinterpret_cast<const bf16x8*>(tok(u * 8 + q * 2 + i));
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_frag(w.v[2 * i], w.v[2 * i + 1]), b, acc, 0,
-                                                    0, 0);
-    }
-  } else {
+  if constexpr (FMT == kNVFP4) {
     // E2M1 codes times the block scale as fp16 (exact, at most 6 significant
-    // bits); a unit half past K holds zero codes and reads the last chunk
+    // bits)
+    const f16x2 sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.sb, 1.0f, false);
+    x += q * 4 * dx;
+    f16x8 b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const f16x8*>(x + i * dx);
+    f32x4 odd = {0.f, 0.f, 0.f, 0.f};  // two chains of products
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f16x8 b = *reinterpret_cast<const f16x8*>(tok(min(u * 16 + q * 4 + i, last_chunk)));
-      const _Float16 sh = static_cast<_Float16>(e4m3_decode((w.sb >> (i >> 1 ? 8 : 0)) & 0xffu));
-      const f16x2 s2 = {sh, sh};
-      const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[i], 1.0f, 0) * s2;
-      const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[i], 1.0f, 1) * s2;
-      const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[i], 1.0f, 2) * s2;
-      const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[i], 1.0f, 3) * s2;
+      const f16x2 s2 = {sc[i >> 1], sc[i >> 1]};
+      const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[0][i], 1.0f, 0) * s2;
+      const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[0][i], 1.0f, 1) * s2;
+      const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[0][i], 1.0f, 2) * s2;
+      const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.v[0][i], 1.0f, 3) * s2;
       const f16x8 a = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, acc, 0, 0, 0);
+      if (i & 1) odd = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[i], odd, 0, 0, 0);
+      else acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b[i], acc, 0, 0, 0);
+    }
+    acc += odd;
+  } else {
+    const int row = lane >> 3, r = lane & 15;
+    u32x4* const put = reinterpret_cast<u32x4*>(turn + row * 128 + (((lane & 7) ^ row) << 4));
+    put[0] = w.v[0];
+    put[64] = w.v[1];  // 8 rows on, the same row % 8
+    const auto get = [&](int c) {
+      return *reinterpret_cast<const u32x4*>(turn + r * 128 + ((c ^ (r & 7)) << 4));
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (FMT == kBF16) {
+        const bf16x8 b = *reinterpret_cast<const bf16x8*>(x + (i * 4 + q) * dx);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, get(i * 4 + q)), b,
+                                                      acc, 0, 0, 0);
+      } else {
+        // E4M3 codes as bf16 (exact), so the products are exact in fp32
+        const u32x4 v = get(i * 4 + q);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bf16x8 b = *reinterpret_cast<const bf16x8*>(x + ((i * 4 + q) * 2 + h) * dx);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_frag(v[2 * h], v[2 * h + 1]), b, acc, 0,
+                                                        0, 0);
+        }
+      }
     }
   }
   return acc;
 }
 
-// n units through a ring of P loads in flight: load(i) starts the i-th (none
-// past n), use(unit, i) consumes it
-template <int FMT, int P, class Load, class Use>
-__device__ __forceinline__ void stream_units(int n, Load load, Use use) {
+// n units through a ring of P in flight: load(i) starts the i-th (nothing past
+// n), use(unit, i) consumes it.  prime() may run ahead of what use() needs.
+template <int FMT, int P>
+struct Stream {
   Unit<FMT> ring[P];
+  template <class Load>
+  __device__ __forceinline__ void prime(Load load) {
 #pragma unroll
-  for (int j = 0; j < P; ++j) ring[j] = load(j);
-  for (int i = 0; i < n; i += P) {
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      if (i + j < n) use(ring[j], i + j);
-      ring[j] = load(i + j + P);
-    }
+    for (int j = 0; j < P; ++j) ring[j] = load(j);
   }
-}
-
-// ---- activation quantisers, 8 values of one lane (the recipes of quant.hip)
-template <int FMT>
-struct TensorScale {
-  float s = 1.f;  // value = stored * s
-  float a = 0.f;  // FP8: 448 / amax; NVFP4: 6 s
-  __device__ explicit TensorScale(float amax) {
-    if constexpr (FMT == kFP8) {
-      s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
-      a = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
-    } else if constexpr (FMT == kNVFP4) {
-      s = amax > 0.f ? __fdiv_rn(amax, 2688.f) : 0.f;
-      a = 6.f * s;
+  template <class Load, class Use>
+  __device__ __forceinline__ void run(int n, Load load, Use use) {
+    for (int i = 0; i < n; i += P) {
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        if (i + j < n) use(ring[j], i + j);
+        ring[j] = load(i + j + P);
+      }
     }
   }
 };
 
-__device__ __forceinline__ float amax8(u32x4 v) {
-  float m = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    m = fmaxf(m, fabsf(__uint_as_float(v[w] << 16)));
-    m = fmaxf(m, fabsf(__uint_as_float(v[w] & 0xffff0000u)));
-  }
-  return m;
-}
-
-// 8 bf16 values as the GEMM operand: dec(code) in bf16 (FP8), dec(code) *
-// dec(block scale) in fp16 (NVFP4; the other half of the 16-value block is on
-// the neighbouring lane, which must be active)
-template <int FMT>
-__device__ __forceinline__ u32x4 quantise8(u32x4 v, const TensorScale<FMT>& ts) {
-  if constexpr (FMT == kBF16) {
-    return v;
-  } else if constexpr (FMT == kFP8) {
-    uint32_t c[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t a = v[2 * h], b = v[2 * h + 1];
-      c[h] = e4m3_encode4(__uint_as_float(a << 16) * ts.a, __uint_as_float(a & 0xffff0000u) * ts.a,
-                          __uint_as_float(b << 16) * ts.a, __uint_as_float(b & 0xffff0000u) * ts.a);
-    }
-    return __builtin_bit_cast(u32x4, fp8_frag(c[0], c[1]));
-  } else {
-    const float m = amax8(v);
-    // quad_perm [1, 0, 3, 2]: the value of the neighbouring lane
-    const float mo = __builtin_bit_cast(
-        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, m), 0xb1, 0xf, 0xf, false));
-    float sbf = 0.f;
-    if (ts.s > 0.f) sbf = e4m3_decode(e4m3_encode(__fdiv_rn(fmaxf(m, mo), ts.a)));
-    const float r = sbf > 0.f ? __fdiv_rn(1.f, sbf * ts.s) : 0.f;
-    float t[8];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      t[2 * w] = __uint_as_float(v[w] << 16) * r;
-      t[2 * w + 1] = __uint_as_float(v[w] & 0xffff0000u) * r;
-    }
-    const uint32_t q = e2m1_encode8(t);
-    const _Float16 sh = static_cast<_Float16>(sbf);
-    const f16x2 s2 = {sh, sh};
-    const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 0) * s2;
-    const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 1) * s2;
-    const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 2) * s2;
-    const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, 1.0f, 3) * s2;
-    return u32x4{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
-                 __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
-  }
-}
-
 // routing of the batch, the same in every workgroup
 struct Routing {
   uint32_t mask[kMaxE];          // tokens of each expert, a bit each
+  uint32_t used[kMaxE / 32];     // experts with tokens, a bit each
+  __attribute__((aligned(16))) uint32_t key[kMaxRows / 2];  // 16 bits a row, ~0: none
   uint8_t slot[kMaxE][kTok];     // slot of a token at an expert it selected
   float gate[kTok][8];
   int16_t id[kTok][8];           // -1: none
@@ -312,18 +404,22 @@ struct Routing {
 
 struct Shared {
   Routing rt;
-  f32x4 red[kWaves][kWave];
+  // of each wave: its part of a sum, and where its weights are turned around
+  __attribute__((aligned(16))) uint8_t turn[kWaves][2048];
   float wave_part[kWaves];
-  int next, ready;
+  int next;
 };
 
-// element r of the packed partial logits of token t; every wave takes the
-// tokens wave, wave + kWaves, ...
-__device__ void route_tokens(const FewArgs& g, Shared& sm) {
+__device__ __forceinline__ void clear_routing(Shared& sm) {
+  for (int e = threadIdx.x; e < kMaxE; e += kThreads) sm.rt.mask[e] = 0u;
+  if (threadIdx.x < kMaxE / 32) sm.rt.used[threadIdx.x] = 0u;
+  if (threadIdx.x < kMaxRows / 2) sm.rt.key[threadIdx.x] = 0xffffffffu;
+}
+
+// top-k and gates of the tokens wave, wave + kWaves, ...
+__device__ __forceinline__ void select_experts(const FewArgs& g, Shared& sm) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Routing& rt = sm.rt;
-  for (int e = threadIdx.x; e < kMaxE; e += kThreads) rt.mask[e] = 0u;
-  __syncthreads();
   for (int t = wave; t < g.T; t += kWaves) {
     float v[kMaxE / 64];
     uint32_t key[kMaxE / 64];
@@ -349,52 +445,53 @@ __device__ void route_tokens(const FewArgs& g, Shared& sm) {
       z[j] = j < g.k ? expf(sel_v[j] - sel_v[0]) : 0.f;
       sum += z[j];
     }
-    if (lane == 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = j < g.k ? sel_i[j] : -1;
-        rt.id[t][j] = static_cast<int16_t>(e);
-        rt.gate[t][j] = z[j] / sum;
-        if (e >= 0) {
-          rt.slot[e][t] = static_cast<uint8_t>(j);
-          atomicOr(&rt.mask[e], 1u << t);
-        }
+    for (int j = 0; j < 8; ++j) {
+      if (lane != j || j >= g.k) continue;
+      const int e = sel_i[j];
+      rt.id[t][j] = static_cast<int16_t>(e);
+      rt.gate[t][j] = z[j] / sum;
+      if (e >= 0) {
+        rt.slot[e][t] = static_cast<uint8_t>(j);
+        atomicOr(&rt.mask[e], 1u << t);
+        atomicOr(&rt.used[e >> 5], 1u << (e & 31));
+        reinterpret_cast<uint16_t*>(rt.key)[t * g.k + j] = static_cast<uint16_t>(e * kTok + t);
       }
     }
   }
-  __syncthreads();
-  if (wave == 0) {
-    int base = 0, row = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-      const int e = e0 + lane;
-      const uint32_t m = e < g.E ? rt.mask[e] : 0u;
-      const uint64_t any = __ballot(m != 0u);
-      const int cnt = __popc(m);
-      int incl = cnt;
+}
+
+// The rows by expert, then token: a row's place is the number of smaller keys
+// (expert * 16 + token), its expert's place the number of smaller experts used.
+__device__ __forceinline__ void list_rows(const FewArgs& g, Shared& sm) {
+  Routing& rt = sm.rt;
+  const int n = g.T * g.k, p = threadIdx.x;
+  if (p < n) {
+    const uint32_t mine = reinterpret_cast<const uint16_t*>(rt.key)[p];
+    if (mine != 0xffffu) {
+      int at = 0;
+      for (int i = 0; i < (n + 7) / 8; ++i) {
+        const u32x4 v = reinterpret_cast<const u32x4*>(rt.key)[i];
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int n = __shfl_up(incl, o);
-        if (lane >= o) incl += n;
+        for (int w = 0; w < 4; ++w) at += ((v[w] & 0xffffu) < mine) + ((v[w] >> 16) < mine);
       }
-      if (m) {
-        const int d = base + __popcll(any & ((1ull << lane) - 1));
-        int at = row + incl - cnt;
+      const int e = static_cast<int>(mine) / kTok, t = static_cast<int>(mine) % kTok;
+      rt.src[at] = static_cast<uint8_t>(t * 8 + rt.slot[e][t]);
+      if (!(rt.mask[e] & ((1u << t) - 1u))) {  // the expert's first row
+        int d = __popc(rt.used[e >> 5] & ((1u << (e & 31)) - 1u));
+        for (int w = 0; w < (e >> 5); ++w) d += __popc(rt.used[w]);
         rt.expert[d] = static_cast<uint8_t>(e);
         rt.off[d] = static_cast<uint16_t>(at);
-        for (uint32_t b = m; b; b &= b - 1) {
-          const int t = __ffs(static_cast<int>(b)) - 1;
-          rt.src[at++] = static_cast<uint8_t>(t * 8 + rt.slot[e][t]);
-        }
       }
-      base += __popcll(any);
-      row += __shfl(incl, 63);
-    }
-    if (lane == 0) {
-      rt.off[base] = static_cast<uint16_t>(row);
-      rt.n_experts = base;
     }
   }
-  __syncthreads();
+  if (p == kThreads - 1) {
+    int d = 0, rows = 0;
+    for (int w = 0; w < kMaxE / 32; ++w) d += __popc(rt.used[w]);
+    for (int i = 0; i < n; ++i) rows += reinterpret_cast<const uint16_t*>(rt.key)[i] != 0xffffu;
+    rt.off[d] = static_cast<uint16_t>(rows);
+    rt.n_experts = d;
+  }
 }
 
 // this lane's token column of expert e: whether it is served, and its row
@@ -410,49 +507,46 @@ __device__ __forceinline__ Column column_of(const Routing& rt, int e) {
   return Column{live, live ? static_cast<int>(__popc(m & ((1u << c) - 1u))) : 0};
 }
 
-// one token row's values as operand chunks of 16 bytes, with the tensor scale
-// over all T rows.  Chunk c of token t sits at (c * T + t) * 16, so the lanes
-// of one MFMA operand read consecutive addresses.
-template <int FMT>
-__device__ float stage_tokens(const FewArgs& g, uint8_t* xs, Shared& sm) {
-  const int h8 = g.H / 8;
-  float m = 0.f;
-  for (int t = 0; t < g.T; ++t)
-    for (int c = threadIdx.x; c < h8; c += kThreads) {
-      const u32x4 v = reinterpret_cast<const u32x4*>(g.x + static_cast<size_t>(t) * g.H)[c];
-      if constexpr (FMT != kBF16) m = fmaxf(m, amax8(v));
-      *reinterpret_cast<u32x4*>(xs + (static_cast<size_t>(c) * g.T + t) * 16) = v;
-    }
-  if constexpr (FMT == kBF16) return 1.f;
-  m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) sm.wave_part[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = 0.f;
+constexpr int kBatch = 6;  // 16-byte loads a thread starts together when it stages
+
+// stages rows x chunks of 8 values: get(row) is a row's first value, put(row,
+// chunk) where its chunk goes, make(v) what goes there.  Thread pairs (2 i,
+// 2 i + 1) hold neighbouring chunks (chunks is even).  The threads of the last
+// waves go first: the first ones may still be routing.
+template <class Get, class Put, class Make>
+__device__ __forceinline__ void stage_rows(int rows, int chunks, Get get, Put put, Make make) {
+  const int n = rows * chunks;
+  const float inv = 1.0f / static_cast<float>(chunks);
+  const int me = static_cast<int>(kThreads - 1 - threadIdx.x);
+  for (int i0 = me; i0 < n; i0 += kBatch * kThreads) {
+    u32x4 v[kBatch];
+    int r[kBatch], c[kBatch];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sm.wave_part[w]);
-  const TensorScale<FMT> ts(m);
-  // each thread quantises the chunks it stored (a block's halves are on
-  // neighbouring lanes: h8 is even)
-  for (int t = 0; t < g.T; ++t)
-    for (int c = threadIdx.x; c < h8; c += kThreads) {
-      u32x4* p = reinterpret_cast<u32x4*>(xs + (static_cast<size_t>(c) * g.T + t) * 16);
-      *p = quantise8<FMT>(*p, ts);
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = min(i0 + j * kThreads, n - 2 + (me & 1));
+      // i / chunks: i < 2^14 here, so the quotient is off by less than the
+      // distance of (i + 1/2) / chunks from a whole number
+      r[j] = static_cast<int>((static_cast<float>(i) + 0.5f) * inv);
+      c[j] = i - r[j] * chunks;
+      v[j] = reinterpret_cast<const u32x4*>(get(r[j]))[c[j]];
     }
-  return ts.s;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const u32x4 o = make(v[j]);
+      if (i0 + j * kThreads < n) *reinterpret_cast<u32x4*>(put(r[j], c[j])) = o;
+    }
+  }
 }
 
-// waves that share one 16-row tile of the up projection: as many as leave at
-// least one round for every workgroup, so that a few experts still spread over
-// all of them
-__device__ __forceinline__ int up_split(int tiles, int n_groups) {
-  int ks = 1;
-  while (ks < kWaves && tiles * ks < n_groups * kWaves) ks *= 2;
-  return ks;
+// chunks of K values a unit's operand reads: whole units, zeros past K
+template <int FMT>
+__host__ __device__ constexpr int chunks_of(int K) {
+  return units_of<FMT>(K) * kUnitK<FMT> / 8;
 }
 
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
-  constexpr int P = 8;  // loads in flight per wave
+  constexpr int P = FMT == kBF16 ? 4 : 3;  // units in flight per wave
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   Shared& sm = *reinterpret_cast<Shared*>(dyn);
   uint8_t* const stage = dyn + (sizeof(Shared) + 15) / 16 * 16;  // tokens, later rows of a
@@ -460,17 +554,25 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = lane & 15, q = lane >> 4;
   const int H = g.H, F = g.F, T = g.T;
+  uint8_t* const turn = sm.turn[wave];
+  const auto part_of = [&](int w) { return reinterpret_cast<f32x4*>(sm.turn[w]) + lane; };
 
-  int ticket = 0;
-  if (tid == 0) ticket = static_cast<int>(atomicAdd(&g.ctr[0], 1u));
-  route_tokens(g, sm);
-  const float s_x = stage_tokens<FMT>(g, stage, sm);
-  if (tid == 0) {
-    sm.next = ticket;
-    sm.ready = 0;
-  }
+  if (tid == 0) sm.next = static_cast<int>(atomicAdd(&g.ctr[kFewTicket], 1u));
+  clear_routing(sm);
   __syncthreads();
-  ticket = __builtin_amdgcn_readfirstlane(sm.next);
+  select_experts(g, sm);
+  // The tokens as the operand: chunk ch of token t at (ch * T + t) * 16, so the
+  // lanes of one MFMA read consecutive addresses.
+  const int T16 = T * 16;
+  stage_rows(
+      T, H / 8, [&](int t) { return g.tokens + static_cast<size_t>(t) * H; },
+      [&](int t, int ch) { return stage + ch * T16 + t * 16; }, [](u32x4 v) { return v; });
+  for (int i = H / 8 * T16 + tid * 16; i < chunks_of<FMT>(H) * T16; i += kThreads * 16)
+    *reinterpret_cast<u32x4*>(stage + i) = u32x4{0u, 0u, 0u, 0u};
+  __syncthreads();
+  list_rows(g, sm);
+  __syncthreads();
+  int ticket = __builtin_amdgcn_readfirstlane(sm.next);
   if (ticket == 0)
     for (int i = tid; i < T * g.k; i += kThreads) {
       g.ids[i] = rt.id[i / g.k][i % g.k];
@@ -480,199 +582,248 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
   const int D = __builtin_amdgcn_readfirstlane(rt.n_experts);
   const int f16 = F / 16;
   const int up_tiles = D * f16;
-  const int ks = up_split(up_tiles, static_cast<int>(gridDim.x));
-  const int per_round = kWaves / ks;
-  const int up_rounds = (up_tiles + per_round - 1) / per_round;
-  const int down_tiles = H / 16;
-  const int stride = F * 2 + 16;  // LDS row of a: padded against bank conflicts
+  const int groups = static_cast<int>(gridDim.x);
+  const int up_items = min(up_tiles, groups);  // an item: an even share of the tiles
 
-  while (ticket < up_rounds + down_tiles) {
-    int nxt = 0;
-    if (tid == 0) nxt = static_cast<int>(atomicAdd(&g.ctr[0], 1u));
-    if (ticket < up_rounds) {
-      // ---- up: a tile of 16 expert rows per ks waves, K split over them
-      const int tile = ticket * per_round + wave / ks;
-      const bool have = tile < up_tiles;
-      const int d = __builtin_amdgcn_readfirstlane(have ? tile / f16 : 0);
-      const int n0 = __builtin_amdgcn_readfirstlane(have ? tile % f16 : 0) * 16;
-      const int e = __builtin_amdgcn_readfirstlane(rt.expert[d]);
-      const int U = units_of<FMT>(H);
-      const int part = wave % ks;
-      const int u0 = U * part / ks;
-      const int n = have ? U * (part + 1) / ks - u0 : 0;
-      const Matrix m = matrix_of<FMT>(g.up, g.up_bs, e, F, H);
+  // ---- up.  An item's tiles go in rounds of n = 16, 8, 4, 2, 1 of them, a
+  // tile's K split over 16 / n waves, so that nearly every wave streams to the
+  // end of the item; a round's first loads start before the sums of the round
+  // before it are joined.  A last round may hold fewer than n tiles, down to
+  // 5/8: idle waves cost less there than one more round.
+  const uint8_t* const col = stage + min(c, T - 1) * 16;
+  while (ticket < up_items) {
+    float local = 0.f;
+    const int t1 = static_cast<int>(static_cast<int64_t>(up_tiles) * (ticket + 1) / up_items);
+    int t0 = static_cast<int>(static_cast<int64_t>(up_tiles) * ticket / up_items);
+    const int U = units_of<FMT>(H);
+    Tile<FMT, false> w;
+    int ksl = 0, e = 0, n0 = 0, u0 = 0, n = 0;  // of the round that is streaming
+    bool live = false;                          // this wave stores a tile of it
+    const auto start = [&]() {
+      const int left = t1 - t0;
+      ksl = 0;
+      while ((kWaves >> ksl) * 5 > left * 8) ++ksl;
+      const bool mine = t0 + (wave >> ksl) < t1;
+      const int tile = mine ? t0 + (wave >> ksl) : t0, d = tile / f16;
+      const int part = wave & ((1 << ksl) - 1);
+      n0 = __builtin_amdgcn_readfirstlane(tile - d * f16) * 16;
+      e = __builtin_amdgcn_readfirstlane(rt.expert[d]);
+      u0 = __builtin_amdgcn_readfirstlane((U * part) >> ksl);
+      n = mine ? __builtin_amdgcn_readfirstlane((U * (part + 1)) >> ksl) - u0 : 0;
+      live = mine && part == 0;
+      w.point(g.up, g.up_bs, e, n0, F, H);
+    };
+    const auto load = [&](int i) { return w.load(u0 + i, i < n); };
+    Stream<FMT, P> st;
+    start();
+    st.prime(load);
+    int seen = 0;
+    if (tid == 0)
+      seen = static_cast<int>(__hip_atomic_load(&g.ctr[kFewTicket], __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT));
+    while (true) {
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      const uint8_t* col = stage + min(c, T - 1) * 16;
-      stream_units<FMT, P>(
-          n, [&](int i) { return load_unit<FMT, false>(m, n0, F, H, u0 + i, i < n); },
-          [&](const Unit<FMT>& w, int i) {
-            acc = mul_unit<FMT>(
-                w, u0 + i, H / 8 - 1, [&](int ch) { return col + static_cast<size_t>(ch) * T * 16; },
-                acc);
-          });
+      st.run(n, load, [&](const Unit<FMT>& v, int i) {
+        acc = mul_unit<FMT>(v, col + (u0 + i) * (kUnitK<FMT> / 8) * T16, T16, turn, acc);
+      });
+      const int ks = 1 << ksl, ce = e, cn0 = n0;
+      const bool first = live;
+      t0 += kWaves >> ksl;
+      const bool more = t0 < t1;
+      if (more) {
+        start();
+        st.prime(load);
+      }
       if (ks > 1) {
-        sm.red[wave][lane] = acc;
+        *part_of(wave) = acc;
         __syncthreads();
-        if (part == 0)
-          for (int w = 1; w < ks; ++w) acc += sm.red[wave + w][lane];
+        if (first)
+          for (int v = 1; v < ks; ++v) acc += *part_of(wave + v);
       }
-      float local = 0.f;
-      if (have && part == 0) {
+      if (first && ((rt.mask[ce] >> c) & 1u)) {
         float scale = 1.f;
-        if constexpr (FMT != kBF16) scale = s_x * g.up_s[e];
-        if ((rt.mask[e] >> c) & 1u) {
-          uint16_t b[4];
+        if constexpr (FMT != kBF16) scale = *g.x_scale * g.up_s[ce];
+        uint16_t b[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            b[i] = relu_sq_bf16(FMT == kBF16 ? acc[i] : acc[i] * scale);
-            local = fmaxf(local, bf16_to_f32(b[i]));
-          }
-          const size_t row = static_cast<size_t>(c) * g.k + rt.slot[e][c];
-          *reinterpret_cast<uint2*>(g.act + row * F + n0 + 4 * q) =
-              make_uint2(b[0] | (static_cast<uint32_t>(b[1]) << 16),
-                         b[2] | (static_cast<uint32_t>(b[3]) << 16));
+        for (int i = 0; i < 4; ++i) {
+          b[i] = relu_sq_bf16(FMT == kBF16 ? acc[i] : acc[i] * scale);
+          local = fmaxf(local, bf16_to_f32(b[i]));
         }
-        if constexpr (FMT != kBF16) {
-          local = wave_max(local);
-          if (lane == 0) atomic_max_nonneg(&g.ctr[kFewAmax + (tile % kAmaxSlots)], local);
-        }
-        __threadfence();  // the tile is in memory before the round counts as done
+        const size_t row = static_cast<size_t>(c) * g.k + rt.slot[ce][c];
+        const uint32_t lo = b[0] | (static_cast<uint32_t>(b[1]) << 16);
+        const uint32_t hi = b[2] | (static_cast<uint32_t>(b[3]) << 16);
+        __hip_atomic_store(reinterpret_cast<uint64_t*>(g.act + row * F + cn0 + 4 * q),
+                           lo | (static_cast<uint64_t>(hi) << 32), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
       }
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        atomicAdd(&g.ctr[1], 1u);
-      }
-    } else {
-      // ---- down: 16 output columns over all experts
-      if (!sm.ready) {
-        if (tid == 0) {
-          while (__hip_atomic_load(&g.ctr[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) <
-                 static_cast<uint32_t>(up_rounds))
-            __builtin_amdgcn_s_sleep(2);
-        }
-        __syncthreads();
-        __threadfence();  // what the other workgroups wrote is read from memory
-        if (tid == 0) sm.ready = 1;
-      }
-      float amax = 0.f;
-      if constexpr (FMT != kBF16)
-        amax = wave_max(__uint_as_float(__hip_atomic_load(&g.ctr[kFewAmax + lane], __ATOMIC_RELAXED,
-                                                          __HIP_MEMORY_SCOPE_AGENT)));
-      const TensorScale<FMT> ts(amax);
-      const int n0 = (ticket - up_rounds) * 16;
-      const int U = units_of<FMT>(F);
-      const int f8 = F / 8;
-      f32x4 tot = {0.f, 0.f, 0.f, 0.f};
-      for (int d0 = 0; d0 < D;) {
-        // experts whose rows fit the stage (one expert's always do)
-        int d1 = d0 + 1;
-        while (d1 < D && rt.off[d1 + 1] - rt.off[d0] <= g.stage_rows) ++d1;
-        const int r0 = rt.off[d0];
-        __syncthreads();  // the stage is free
-        for (int r = r0 + wave; r < rt.off[d1]; r += kWaves) {
-          const int s = rt.src[r];
-          const u32x4* src = reinterpret_cast<const u32x4*>(
-              g.act + (static_cast<size_t>(s >> 3) * g.k + (s & 7)) * F);
-          u32x4* dst = reinterpret_cast<u32x4*>(stage + static_cast<size_t>(r - r0) * stride);
-          for (int ch = lane; ch < f8; ch += kWave) dst[ch] = quantise8<FMT>(src[ch], ts);
-        }
-        __syncthreads();
-        const int all = (d1 - d0) * U;
-        const int i0 = __builtin_amdgcn_readfirstlane(all * wave / kWaves);
-        const int n = __builtin_amdgcn_readfirstlane(all * (wave + 1) / kWaves) - i0;
-        int ld = d0 + i0 / U, lu = i0 % U;  // expert and unit of the next load
-        int cd = ld, cu = lu;               // and of the next product
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        int ce = __builtin_amdgcn_readfirstlane(rt.expert[cd < D ? cd : 0]);
-        Column col = column_of(rt, ce);
-        const uint8_t* row = stage + static_cast<size_t>(rt.off[cd < D ? cd : 0] - r0 + col.rank) * stride;
-        auto flush = [&]() {
-          if (col.live) {
-            float f = rt.gate[c][rt.slot[ce][c]];
-            if constexpr (FMT != kBF16) f *= ts.s * g.down_s[ce];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[i] += f * acc[i];
-          }
-          acc = f32x4{0.f, 0.f, 0.f, 0.f};
-        };
-        stream_units<FMT, P>(
-            n,
-            [&](int i) {
-              const int e = __builtin_amdgcn_readfirstlane(rt.expert[ld < D ? ld : 0]);
-              const Matrix m = matrix_of<FMT>(g.down, g.down_bs, e, H, F);
-              const Unit<FMT> w = load_unit<FMT, true>(m, n0, H, F, lu, i < n);
-              if (++lu == U) {
-                lu = 0;
-                ++ld;
-              }
-              return w;
-            },
-            [&](const Unit<FMT>& w, int i) {
-              acc = mul_unit<FMT>(w, cu, f8 - 1, [&](int ch) { return row + ch * 16; }, acc);
-              if (++cu == U) {
-                flush();
-                cu = 0;
-                if (++cd < d1) {
-                  ce = __builtin_amdgcn_readfirstlane(rt.expert[cd]);
-                  col = column_of(rt, ce);
-                  row = stage + static_cast<size_t>(rt.off[cd] - r0 + col.rank) * stride;
-                }
-              }
-            });
-        if (n > 0 && cu != 0) flush();
-        d0 = d1;
-      }
-      sm.red[wave][lane] = tot;
-      __syncthreads();
-      if (wave == 0 && c < T) {
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) tot += sm.red[w][lane];
-        const size_t at = static_cast<size_t>(c) * H + n0 + 4 * q;
-        if (g.y_bf16) {
-          const uint32_t lo = f32_to_bf16(tot[0]) | (static_cast<uint32_t>(f32_to_bf16(tot[1])) << 16);
-          const uint32_t hi = f32_to_bf16(tot[2]) | (static_cast<uint32_t>(f32_to_bf16(tot[3])) << 16);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.y) + at) = make_uint2(lo, hi);
-        } else {
-          *reinterpret_cast<f32x4*>(static_cast<float*>(g.y) + at) = tot;
-        }
-      }
+      if (!more) break;
+      if (ks > 1) __syncthreads();  // the parts are read before the next round
     }
-    if (tid == 0) sm.next = nxt;
+    // The item's rows are in memory before it counts as done: agent-scope
+    // stores write through every cache, and this waits for their answers.
+    __builtin_amdgcn_s_waitcnt(0);
+    local = wave_max(local);
+    if (lane == 0) sm.wave_part[wave] = local;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int v = 1; v < kWaves; ++v) local = fmaxf(local, sm.wave_part[v]);
+      // done, with the item's largest a (its sign bit is free)
+      __hip_atomic_store(&g.ctr[kFewDone + ticket], kFewDoneBit | __float_as_uint(local),
+                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      // Items that no workgroup has taken yet are taken before anyone waits; the
+      // count only grows, so what was seen earlier may already say that there
+      // are none.
+      if (seen < up_items) seen = static_cast<int>(atomicAdd(&g.ctr[kFewTicket], 1u));
+      sm.next = seen;
+    }
     __syncthreads();
     ticket = __builtin_amdgcn_readfirstlane(sm.next);
+  }
+
+  // ---- down: 16 output columns over all experts
+  const int F8 = F / 8, cF = chunks_of<FMT>(F);
+  const int stride = cF * 16 + 16;  // LDS row of a: padded against bank conflicts
+  const int U = units_of<FMT>(F);
+  bool ready = false;
+  TensorScale<FMT> ts(0.f);
+  for (int item = blockIdx.x; item < H / 16; item += groups) {
+    const int n0 = item * 16;
+    f32x4 tot = {0.f, 0.f, 0.f, 0.f};
+    for (int d0 = 0; d0 < D;) {
+      // experts whose rows fit the stage (one expert's always do)
+      int d1 = d0 + 1;
+      while (d1 < D && rt.off[d1 + 1] - rt.off[d0] <= g.stage_rows) ++d1;
+      d1 = __builtin_amdgcn_readfirstlane(d1);
+      const int r0 = __builtin_amdgcn_readfirstlane(rt.off[d0]);
+      const int rows = __builtin_amdgcn_readfirstlane(rt.off[d1]) - r0;
+      const int all = (d1 - d0) * U;
+      const int i0 = __builtin_amdgcn_readfirstlane(all * wave / kWaves);
+      const int n = __builtin_amdgcn_readfirstlane(all * (wave + 1) / kWaves) - i0;
+      int ld = d0 + i0 / U, lu = i0 % U;  // expert and unit of the next load
+      int cd = ld, cu = lu;               // and of the next product
+      const auto expert = [&](int d) { return __builtin_amdgcn_readfirstlane(rt.expert[d < D ? d : 0]); };
+      Tile<FMT, true> w;
+      w.point(g.down, g.down_bs, expert(ld), n0, H, F);
+      const auto load = [&](int i) {
+        const Unit<FMT> v = w.load(lu, i < n);
+        if (++lu == U) {
+          lu = 0;
+          w.point(g.down, g.down_bs, expert(++ld), n0, H, F);
+        }
+        return v;
+      };
+      Stream<FMT, P> st;
+      st.prime(load);  // the weights do not wait for a
+      if (!ready) {
+        // every up item is done; the largest a gives the tensor scale
+        if (wave == 0) {
+          float amax = 0.f;
+          for (int i = lane; i < up_items; i += kWave) {
+            uint32_t v;
+            while (!((v = __hip_atomic_load(&g.ctr[kFewDone + i], __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT)) & kFewDoneBit))
+              __builtin_amdgcn_s_sleep(4);
+            amax = fmaxf(amax, __uint_as_float(v & ~kFewDoneBit));
+          }
+          amax = wave_max(amax);
+          // what the other workgroups stored is read from memory from here on
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+          if (lane == 0) sm.wave_part[0] = amax;
+        }
+        __syncthreads();
+        ts = TensorScale<FMT>(sm.wave_part[0]);
+        ready = true;
+      }
+      __syncthreads();  // the stage is free
+      stage_rows(
+          rows, F8,
+          [&](int r) {
+            const int s = rt.src[r0 + r];
+            return g.act + (static_cast<size_t>(s >> 3) * g.k + (s & 7)) * F;
+          },
+          [&](int r, int ch) { return stage + r * stride + ch * 16; },
+          [&](u32x4 v) { return quantise8<FMT>(v, ts); });
+      if (cF > F8)
+        for (int i = tid; i < rows * (cF - F8); i += kThreads)
+          *reinterpret_cast<u32x4*>(stage + i / (cF - F8) * stride + (F8 + i % (cF - F8)) * 16) =
+              u32x4{0u, 0u, 0u, 0u};
+      __syncthreads();
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      int ce = expert(cd);
+      Column col_c = column_of(rt, ce);
+      const uint8_t* row = stage + (rt.off[cd < D ? cd : 0] - r0 + col_c.rank) * stride;
+      const auto flush = [&]() {
+        if (col_c.live) {
+          float f = rt.gate[c][rt.slot[ce][c]];
+          if constexpr (FMT != kBF16) f *= ts.s * g.down_s[ce];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tot[i] += f * acc[i];
+        }
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+      };
+      st.run(n, load, [&](const Unit<FMT>& v, int) {
+        acc = mul_unit<FMT>(v, row + cu * (kUnitK<FMT> * 2), 16, turn, acc);
+        if (++cu == U) {
+          flush();
+          cu = 0;
+          if (++cd < d1) {
+            ce = expert(cd);
+            col_c = column_of(rt, ce);
+            row = stage + (rt.off[cd] - r0 + col_c.rank) * stride;
+          }
+        }
+      });
+      if (n > 0 && cu != 0) flush();
+      d0 = d1;
+    }
+    *part_of(wave) = tot;
     __syncthreads();
+    if (wave == 0 && c < T) {
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) tot += *part_of(w);
+      const size_t at = static_cast<size_t>(c) * H + n0 + 4 * q;
+      if (g.y_bf16) {
+        const uint32_t lo = f32_to_bf16(tot[0]) | (static_cast<uint32_t>(f32_to_bf16(tot[1])) << 16);
+        const uint32_t hi = f32_to_bf16(tot[2]) | (static_cast<uint32_t>(f32_to_bf16(tot[3])) << 16);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.y) + at) = make_uint2(lo, hi);
+      } else {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(g.y) + at) = tot;
+      }
+    }
+    __syncthreads();  // the parts are read before they are written again
   }
 }
 
 constexpr size_t kLdsBytes = 160 * 1024;
 constexpr size_t kFixedLds = (sizeof(Shared) + 15) / 16 * 16;
-constexpr size_t kMaxStage = 144 * 1024;
+constexpr size_t kMaxStage = 120 * 1024;
 static_assert(kFixedLds + kMaxStage <= kLdsBytes, "the stage fits");
-// two workgroups per CU where the tokens' operand allows it
-constexpr size_t kHalfLds = kLdsBytes / 2;
-constexpr int kGroups = 512;
+constexpr int kGroups = kFewGroups;
 
-// bytes of the stage for T tokens: the tokens, and rows of a for at least one
-// expert that all of them select
+// bytes of an LDS row of a, and of the stage for T tokens: the tokens, or rows
+// of a for one expert that all of them select.  Whole units of 128 values
+// cover the three formats.
+size_t row_bytes(int F) { return (static_cast<size_t>(F) + 127) / 128 * 256 + 16; }
 size_t stage_need(int T, int H, int F) {
-  const size_t xs = static_cast<size_t>(T) * H * 2;
-  const size_t as = static_cast<size_t>(T) * (static_cast<size_t>(F) * 2 + 16);
-  return xs > as ? xs : as;
+  const size_t xs = (static_cast<size_t>(H) + 127) / 128 * 256;
+  return static_cast<size_t>(T) * (xs > row_bytes(F) ? xs : row_bytes(F));
 }
 
 template <int FMT>
 hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
   FewArgs g = a;
+  g.tokens = FMT == kBF16 ? g.x : g.x_q;
+  const int blocks = g.E / 16 * kFewSlices + (FMT == kBF16 ? 0 : kQuantGroups);
+  hipLaunchKernelGGL(few_router_kernel<FMT>, dim3(blocks), dim3(kRouterThreads), 0, stream, g);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
   const size_t need = stage_need(g.T, g.H, g.F);
-  const size_t all = static_cast<size_t>(g.T) * g.k * (static_cast<size_t>(g.F) * 2 + 16);
-  const bool two = kFixedLds + need <= kHalfLds;
-  const size_t room = two ? kHalfLds - kFixedLds : kMaxStage;
-  const size_t stage = all > need ? (all < room ? all : room) : need;
-  g.stage_rows = static_cast<int>(stage / (static_cast<size_t>(g.F) * 2 + 16));
+  const size_t all = static_cast<size_t>(g.T) * g.k * row_bytes(g.F);
+  const size_t stage = all > need ? (all < kMaxStage ? all : kMaxStage) : need;
+  g.stage_rows = static_cast<int>(stage / row_bytes(g.F));
   const size_t lds = kFixedLds + stage;
-  const int grid = two ? kGroups : kGroups / 2;
-  hipLaunchKernelGGL(few_layer_kernel<FMT>, dim3(grid), dim3(kThreads), lds, stream, g);
+  hipLaunchKernelGGL(few_layer_kernel<FMT>, dim3(kGroups), dim3(kThreads), lds, stream, g);
   return hipGetLastError();
 }
 
@@ -685,10 +836,6 @@ bool few_fits(int T, int H, int F) {
 }
 
 hipError_t launch_few(int fmt, const FewArgs& g, hipStream_t stream) {
-  hipLaunchKernelGGL(few_router_kernel, dim3(g.E / 16, kFewSlices), dim3(kRouterThreads), 0, stream,
-                     g.x, g.w_router, g.T, g.H, g.E, g.part, g.ctr);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
   switch (fmt) {
     case kBF16: return launch_layer<kBF16>(g, stream);
     case kFP8: return launch_layer<kFP8>(g, stream);

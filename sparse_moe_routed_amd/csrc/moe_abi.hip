@@ -113,7 +113,7 @@ Layout make_layout(const moe_dims* d, int32_t fmt, int32_t T) {
 
 // workspace of moe_layer_few: counters, partial logits, the intermediate
 struct FewLayout {
-  size_t ctr, part, act, total;
+  size_t ctr, part, x_scale, x_q, act, total;
 };
 
 FewLayout few_layout(const moe_dims* d, int32_t T) {
@@ -122,7 +122,9 @@ FewLayout few_layout(const moe_dims* d, int32_t T) {
   FewLayout L{};
   L.ctr = 0;
   L.part = up(moe::kFewCounters * 4);
-  L.act = L.part + up(moe::kFewSlices * rows * d->n_experts * 4);
+  L.x_scale = L.part + up(moe::kFewSlices * rows * d->n_experts * 4);
+  L.x_q = L.x_scale + kAlign;
+  L.act = L.x_q + up(rows * d->hidden * 2);
   L.total = L.act + up(rows * d->top_k * d->ffn * 2);
   return L;
 }
@@ -804,6 +806,8 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   g.down_s = experts->down_s;
   g.ctr = at<uint32_t>(ws, L.ctr);
   g.part = at<float>(ws, L.part);
+  g.x_scale = at<float>(ws, L.x_scale);
+  g.x_q = at<uint16_t>(ws, L.x_q);
   g.act = at<uint16_t>(ws, L.act);
   g.ids = ids;
   g.gates = gates;

@@ -163,9 +163,13 @@ hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream);
 // the whole layer for at most kFewTokens tokens (moe_layer_few)
 constexpr int kFewTokens = 16;
 constexpr int kFewSlices = 4;  // K slices of the partial logits
-// counters: [0] tickets, [1] up rounds done, then kAmaxSlots maxima of a
-constexpr int kFewAmax = 64;
-constexpr int kFewCounters = 128;
+constexpr int kFewGroups = 256;   // workgroups of the second kernel, one per CU
+// counters, tickets and the rest on lines of their own: a word for each item of
+// the up projection, its done bit and the largest |a| of its rows
+constexpr int kFewTicket = 0;
+constexpr int kFewDone = 64;
+constexpr uint32_t kFewDoneBit = 0x80000000u;
+constexpr int kFewCounters = kFewDone + kFewGroups;
 struct FewArgs {
   int T, H, F, E, k;
   const uint16_t* x;
@@ -176,6 +180,9 @@ struct FewArgs {
   const float *up_s, *down_s;
   float* part;     // [kFewSlices, T, E]
   uint32_t* ctr;   // [kFewCounters]
+  uint16_t* x_q;   // FP8, NVFP4: [T, H] code values (the GEMM operand)
+  float* x_scale;  // and their tensor scale
+  const uint16_t* tokens;  // x or x_q (set by the launch)
   uint16_t* act;   // [T * k, F]
   int32_t* ids;
   float* gates;

@@ -23,7 +23,7 @@ SMALL = synth.Dims(hidden=256, ffn=192, n_experts=32, top_k=4)
 WIDE = synth.Dims(hidden=128, ffn=128, n_experts=256, top_k=8)
 ODD = synth.Dims(hidden=192, ffn=320, n_experts=16, top_k=2)   # half-empty last units
 ONE = synth.Dims(hidden=64, ffn=64, n_experts=16, top_k=1)     # smallest
-LONG = synth.Dims(hidden=64, ffn=4416, n_experts=16, top_k=3)  # one expert's rows fill the stage
+LONG = synth.Dims(hidden=64, ffn=3712, n_experts=16, top_k=3)  # one expert's rows fill the stage
 
 
 def _ld(d):
@@ -68,7 +68,7 @@ def test_validation():
                 dict(e=moe.Experts(0, FAKE + 8, FAKE, None, None, None, None))):
         assert call(**bad) == moe.EINVAL, bad
     for bad in (dict(T=17), dict(dims=moe.Dims(2688, 1856, 128, 9)), dict(dims=moe.Dims(2690, 1856, 128, 6)),
-                dict(T=16, dims=moe.Dims(4672, 1856, 128, 6)), dict(T=16, dims=moe.Dims(64, 4608, 128, 6))):
+                dict(T=16, dims=moe.Dims(3904, 1856, 128, 6)), dict(T=16, dims=moe.Dims(64, 3776, 128, 6))):
         assert call(**bad) == moe.EUNSUPPORTED, bad
     for bad in (dict(ws=None), dict(wsb=need - 1), dict(ws=FAKE + 16)):
         assert call(**bad) == moe.EWORKSPACE, bad
