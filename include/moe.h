@@ -69,9 +69,11 @@ typedef enum {
   MOE_WFMT_BF16 = 0,
   MOE_WFMT_FP8 = 1,   /* E4M3 codes, one fp32 scale per expert projection;
                          activations quantised per tensor to E4M3          */
-  MOE_WFMT_NVFP4 = 2  /* E2M1 codes in 16-element blocks along K, one E4M3
+  MOE_WFMT_NVFP4 = 2, /* E2M1 codes in 16-element blocks along K, one E4M3
                          scale per block, one fp32 scale per expert
                          projection; activations quantised the same way    */
+  MOE_WFMT_FP8_BLOCK = 3 /* E4M3 codes, one fp32 scale per 128 x 128 block of
+                         a weight and per 128 values of an activation row   */
 } moe_wfmt;
 
 typedef enum { MOE_Y_BF16 = 0, MOE_Y_F32 = 1 } moe_ydtype;
@@ -114,6 +116,10 @@ typedef struct {
  *          p = n / 128, from the expert's base.  moe_quantize_experts
  *          writes this layout; a GEMM tile then reads one contiguous block
  *          per K step.
+ *   FP8_BLOCK: up u8 E4M3 [E, F, H], down u8 [E, H, F], row-major; up_s fp32
+ *          [E, ceil(F/128), ceil(H/128)], down_s fp32 [E, ceil(H/128),
+ *          ceil(F/128)], a scale for each 128 x 128 block (the last ones of a
+ *          row or column of blocks may be smaller)
  * Unused pointers may be NULL. */
 typedef struct {
   int32_t fmt; /* moe_wfmt */
@@ -166,8 +172,9 @@ int32_t moe_route(const moe_dims* dims, int32_t T, const void* x,
  * grouped expert matrix multiplication).  For each token t:
  *   y_t = sum_{j<k} gates[t,j] * W_down,e . a~,   a = bf16(relu(W_up,e . x~_t)^2)
  * with e = ids[t, j], x~ / a~ the activations as the weight format quantises
- * them (identity for BF16; per-tensor E4M3 for FP8; NVFP4 blocks for 4-bit),
- * fp32 accumulation, slots summed in order j = 0..k-1.
+ * them (identity for BF16; per-tensor E4M3 for FP8; NVFP4 blocks for 4-bit;
+ * E4M3 with a scale for every 128 values of a row for FP8_BLOCK), fp32
+ * accumulation, slots summed in order j = 0..k-1.
  *   x     [dev] bf16 [T, H]        ids [dev] int32 [T, k]    gates [dev] fp32 [T, k]
  *   y     [dev] [T, H], bf16 (MOE_Y_BF16) or fp32 (MOE_Y_F32), written in full
  *   ws    [dev] workspace of ws_bytes >= moe_workspace_size(dims, fmt, T)
@@ -315,10 +322,13 @@ typedef struct {
   int64_t act;        /* bf16 [T*k, F]: a = bf16(relu(h)^2), sorted row order */
   int64_t out_rows;   /* fp32 [T*k, H]: gate * W_down a~, sorted row order   */
   int64_t x_q;        /* [T, H] dequantised token values without the tensor
-                         scale: FP8 bf16 dec(q); NVFP4 fp16 dec(q)*dec(sb)   */
+                         scale: FP8 bf16 dec(q); NVFP4 fp16 dec(q)*dec(sb);
+                         FP8_BLOCK u8 codes, fp32 scales [ceil(H/128), T]
+                         behind them at the next multiple of 256 bytes       */
   int64_t act_q;      /* FP8: u8 [T*k, F] codes; NVFP4: fp16 dec(q)*dec(sb)
-                         in place over act                                   */
-  int64_t scales;     /* fp32 [2]: x scale, act scale                        */
+                         in place over act; FP8_BLOCK: u8 [T*k, F] codes,
+                         scales [ceil(F/128), T*k] behind them as for x_q    */
+  int64_t scales;     /* fp32 [2]: x scale, act scale (FP8, NVFP4)           */
   int64_t total;      /* bytes                                               */
 } moe_ws_layout;
 
@@ -328,7 +338,8 @@ int32_t moe_workspace_layout(const moe_dims* dims, int32_t fmt, int32_t T,
 /* Pack a bf16 expert bank into FP8 or NVFP4 on the device (any expert count
  * 1 <= E <= 256, e.g. a shared expert's one-expert bank; top_k is not used),
  * one fp32 scale per expert projection (recipes: s = f32(amax/448), code = E4M3(f32(w*f32(448/amax)))
- * for FP8; S = f32(amax/2688), block scale sb = E4M3(f32(amax_b/f32(6S))),
+ * for FP8 and, over each 128 x 128 block, FP8_BLOCK (scales as in moe_experts;
+ * a block whose amax is below 2^-100 becomes zero); S = f32(amax/2688), block scale sb = E4M3(f32(amax_b/f32(6S))),
  * code = E2M1(f32(w*f32(1/f32(sb*S)))) for NVFP4; amax == 0 -> zero codes and
  * scale).  Layouts as in moe_experts.
  *   up_bf16 [dev] [E, F, H], down_bf16 [dev] [E, H, F]
@@ -341,11 +352,14 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt,
                              void* stream);
 
 /* Per-tensor activation quantiser of moe_forward as a standalone call (same
- * recipes as moe_quantize_experts, amax over the whole [rows, cols] tensor).
+ * recipes as moe_quantize_experts, amax over the whole [rows, cols] tensor;
+ * FP8_BLOCK: over every 128 values of a row, the last ones of a row may be
+ * fewer).
  *   x [dev] bf16 [rows, cols]; codes [dev] u8 [rows, cols] (FP8) or
  *   [rows, cols/2] (NVFP4: two codes per byte as in the weights, row-major);
- *   bs [dev] u8 [rows, cols/16] (NVFP4 only, row-major); scale [dev] fp32 [1] out;
- *   ws [dev] >= 256 bytes of scratch. */
+ *   bs [dev] u8 [rows, cols/16] (NVFP4 only, row-major); scale [dev] fp32 [1] out
+ *   (FP8_BLOCK: [ceil(cols/128), rows], block by block);
+ *   ws [dev] >= 256 bytes of scratch (FP8_BLOCK: not used, may be NULL). */
 int32_t moe_quantize_activation(int32_t fmt, int32_t rows, int32_t cols,
                                 const void* x, void* codes, uint8_t* bs,
                                 float* scale, void* ws, size_t ws_bytes,
@@ -367,6 +381,36 @@ int32_t moe_prenorm(int32_t T, int32_t H, const void* x, void* out, void* stream
 int32_t moe_residual_add(int32_t T, int32_t H, void* x, const float* y, void* stream);
 int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void* out,
                              void* stream);
+
+/* ---- E4M3 products with a scale per block of 128
+ * Dense products of the decoder's projections in the format of FP8_BLOCK banks:
+ *   y[m, n] = bf16( sum_kb s_x[kb, m] s_w[n / 128, kb]
+ *                   sum_{k in block kb} dec(q_x[m, k]) dec(q_w[n, k]) )
+ * where a block is 128 values of K (the last one may be shorter), its amax
+ * gives s = f32(amax / 448) and codes E4M3(f32(v * f32(448 / amax))); a block
+ * with amax below 2^-100 becomes zero.  Products of a block are summed by the
+ * FP8 matrix instruction (relative error of a block's sum about 2e-5), blocks
+ * in fp32.
+ *   x        [dev] bf16 [M, K]          codes [dev] u8 E4M3 [M, K], row-major
+ *   scales   [dev] fp32 [ceil(K/128), M]: block by block, tokens contiguous
+ *   w        [dev] bf16 [N, K]          w_codes [dev] u8 E4M3 [N, K], row-major
+ *   w_scales [dev] fp32 [ceil(N/128), ceil(K/128)]
+ *   y        [dev] bf16 [M, N], written in full
+ * moe_block_pack quantises a weight (once), moe_block_quantize activations;
+ * moe_block_linear is moe_block_quantize into its workspace followed by
+ * moe_block_matmul.  K % 16 == 0 (MOE_EUNSUPPORTED otherwise), any N, M from 0
+ * (a no-op) to 1 << 20, N and K up to 1 << 20; x, y, w and codes 16-byte
+ * aligned, scales 4-byte; ws 256-byte aligned, ws_bytes >=
+ * moe_block_linear_workspace_size(M, K).  Codes 0x7f and 0xff (NaN) spread to
+ * the rows and columns that read them. */
+int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales, void* stream);
+int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, float* scales,
+                           void* stream);
+int32_t moe_block_matmul(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,
+                         const void* w_codes, const float* w_scales, void* y, void* stream);
+size_t moe_block_linear_workspace_size(int32_t max_rows, int32_t K);
+int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const void* w_codes,
+                         const float* w_scales, void* y, void* ws, size_t ws_bytes, void* stream);
 
 /* The whole layer for a few tokens: moe_route and moe_forward of at most
  * MOE_FEW_TOKENS tokens in two kernels (decode, where the six to nine launches

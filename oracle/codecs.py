@@ -173,6 +173,34 @@ def fp8_dequantize(codes, scale) -> np.ndarray:
     return e4m3_decode(codes) * np.float64(np.float32(scale))
 
 
+def fp8_block_quantize(v, rows: int = 1):
+    """E4M3 codes of bf16-valued v [N, K] with one scale per block of `rows` x 128
+    values (1: an activation's rows, 128: a weight's tiles; the last blocks may
+    be smaller).  Returns (codes uint8 [N, K], scales float32 [ceil(N / rows),
+    ceil(K / 128)]).  A block with amax below 2^-100 becomes zero."""
+    v32 = np.asarray(v, dtype=np.float32)
+    N, K = v32.shape
+    nb, kb = -(-N // rows), -(-K // 128)
+    codes = np.zeros((N, K), np.uint8)
+    scales = np.zeros((nb, kb), np.float32)
+    for i in range(nb):
+        for j in range(kb):
+            at = (slice(i * rows, (i + 1) * rows), slice(j * 128, (j + 1) * 128))
+            amax = _amax32(v32[at])
+            if amax < np.float32(2.0 ** -100):
+                continue
+            inv = np.float32(np.float32(E4M3_MAX) / amax)
+            codes[at] = e4m3_encode((v32[at] * inv).astype(np.float32))
+            scales[i, j] = np.float32(amax / np.float32(E4M3_MAX))
+    return codes, scales
+
+
+def fp8_block_dequantize(codes, scales, rows: int = 1) -> np.ndarray:
+    N, K = codes.shape
+    s = np.repeat(np.repeat(scales.astype(np.float64), rows, 0)[:N], 128, 1)[:, :K]
+    return e4m3_decode(codes) * s
+
+
 def nvfp4_quantize(v, amax=None):
     """Per-tensor NVFP4 quantisation along the last axis (16-element blocks).
 

@@ -79,11 +79,11 @@ class ExpertBank:
     """Dequantised expert weights of one layer, produced one expert at a time.
 
     `up_bf16` [E, F, H] and `down_bf16` [E, H, F] are torch bf16 CPU tensors
-    (or float arrays holding bf16 values).  For "fp8" and "nvfp4" the oracle
+    (or float arrays holding bf16 values).  For the other formats the oracle
     quantises each expert projection itself (oracle.codecs recipes)."""
 
     def __init__(self, up_bf16, down_bf16, fmt: str = "bf16"):
-        if fmt not in ("bf16", "fp8", "nvfp4"):
+        if fmt not in ("bf16", "fp8", "nvfp4", "fp8_block"):
             raise ValueError(fmt)
         self.fmt = fmt
         self._up = up_bf16
@@ -103,6 +103,8 @@ class ExpertBank:
         if self.fmt == "fp8":
             q, s = codecs.fp8_quantize(w)
             return codecs.fp8_dequantize(q, s)
+        if self.fmt == "fp8_block":
+            return codecs.fp8_block_dequantize(*codecs.fp8_block_quantize(w, 128), 128)
         q, sb, S = codecs.nvfp4_quantize(w)
         return codecs.nvfp4_dequantize(q, sb, S)
 
@@ -137,7 +139,8 @@ class ExpertBank:
 
 def quantise_activation(v, fmt: str) -> np.ndarray:
     """The activation a projection consumes: identity for bf16, per-tensor
-    fake quantisation (quantise then dequantise) for fp8 / nvfp4."""
+    fake quantisation (quantise then dequantise) for fp8 / nvfp4, by blocks of
+    128 values of a row for fp8_block."""
     v = np.asarray(v, dtype=np.float64)
     if fmt == "bf16":
         return v
@@ -147,6 +150,8 @@ def quantise_activation(v, fmt: str) -> np.ndarray:
     if fmt == "nvfp4":
         q, sb, S = codecs.nvfp4_quantize(v)
         return codecs.nvfp4_dequantize(q, sb, S)
+    if fmt == "fp8_block":
+        return codecs.fp8_block_dequantize(*codecs.fp8_block_quantize(v))
     raise ValueError(fmt)
 
 

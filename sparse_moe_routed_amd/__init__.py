@@ -23,7 +23,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MOE_LIB") or os.path.join(_PKG, "libmoe.so")
 
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP = 0, 1, 2, 3, 4
-WFMT = {"bf16": 0, "fp8": 1, "nvfp4": 2}
+WFMT = {"bf16": 0, "fp8": 1, "nvfp4": 2, "fp8_block": 3}
 Y_BF16, Y_F32 = 0, 1
 
 
@@ -119,6 +119,15 @@ _SIGS = {
                                           ctypes.c_void_p, ctypes.c_void_p]),
     "moe_residual_prenorm": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_block_pack": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_block_quantize": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_block_matmul": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
+                         + [ctypes.c_void_p] * 6),
+    "moe_block_linear_workspace_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "moe_block_linear": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
+                         + [ctypes.c_void_p] * 5 + [ctypes.c_size_t, ctypes.c_void_p]),
     "moe_layer_few_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims), ctypes.c_int32,
                                                        ctypes.c_int32]),
     "moe_layer_few": (ctypes.c_int32, [ctypes.POINTER(Dims), ctypes.c_int32, ctypes.c_void_p,
@@ -198,7 +207,7 @@ class LayerDims:
 
 @dataclass
 class ExpertBank:
-    """Device expert bank in one of the three formats (see moe_experts in moe.h)."""
+    """Device expert bank in one of the formats of WFMT (see moe_experts in moe.h)."""
     fmt: str
     up: torch.Tensor
     down: torch.Tensor
@@ -471,7 +480,8 @@ def forward_cached(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, cach
 
 def quantize_experts(up: torch.Tensor, down: torch.Tensor, fmt: str,
                      dims: LayerDims = LayerDims()) -> ExpertBank:
-    """moe_quantize_experts: pack a bf16 bank [E,F,H] / [E,H,F] into fp8 or nvfp4."""
+    """moe_quantize_experts: pack a bf16 bank [E,F,H] / [E,H,F] into fp8, nvfp4 or
+    fp8_block."""
     if fmt == "bf16":
         return ExpertBank("bf16", up, down)
     E, F, H = dims.n_experts, dims.ffn, dims.hidden
@@ -489,10 +499,15 @@ def quantize_experts(up: torch.Tensor, down: torch.Tensor, fmt: str,
         down_q = torch.empty((E, H * F // 2), dtype=torch.uint8, device=dev)
         up_bs = torch.empty((E, F * H // 16), dtype=torch.uint8, device=dev)
         down_bs = torch.empty((E, H * F // 16), dtype=torch.uint8, device=dev)
+    elif fmt == "fp8_block":
+        up_q = torch.empty((E, F, H), dtype=torch.uint8, device=dev)
+        down_q = torch.empty((E, H, F), dtype=torch.uint8, device=dev)
+        up_bs = down_bs = None
     else:
         raise ValueError(fmt)
-    up_s = torch.empty(E, dtype=torch.float32, device=dev)
-    down_s = torch.empty(E, dtype=torch.float32, device=dev)
+    nf, nh = (-(-F // 128), -(-H // 128))
+    up_s = torch.empty((E, nf, nh) if fmt == "fp8_block" else E, dtype=torch.float32, device=dev)
+    down_s = torch.empty((E, nh, nf) if fmt == "fp8_block" else E, dtype=torch.float32, device=dev)
     d = dims.c()
     _check("moe_quantize_experts", lib().moe_quantize_experts(
         ctypes.byref(d), WFMT[fmt], _ptr(up), _ptr(down), _ptr(up_q), _ptr(down_q),
@@ -501,11 +516,12 @@ def quantize_experts(up: torch.Tensor, down: torch.Tensor, fmt: str,
 
 
 def quantize_activation(x: torch.Tensor, fmt: str):
-    """moe_quantize_activation: (codes, block scales or None, scale fp32[1])."""
+    """moe_quantize_activation: (codes, block scales or None, scale fp32[1]; fp8_block:
+    [ceil(cols / 128), rows])."""
     rows, cols = x.shape
     _dev(x, torch.bfloat16, "x")
     dev = x.device
-    if fmt == "fp8":
+    if fmt in ("fp8", "fp8_block"):
         codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
         bs = None
     elif fmt == "nvfp4":
@@ -513,7 +529,8 @@ def quantize_activation(x: torch.Tensor, fmt: str):
         bs = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev)
     else:
         raise ValueError(fmt)
-    scale = torch.empty(1, dtype=torch.float32, device=dev)
+    scale = torch.empty((-(-cols // 128), rows) if fmt == "fp8_block" else 1, dtype=torch.float32,
+                        device=dev)
     ws = torch.empty(256, dtype=torch.uint8, device=dev)
     _check("moe_quantize_activation", lib().moe_quantize_activation(
         WFMT[fmt], rows, cols, _ptr(x), _ptr(codes), _ptr(bs), _ptr(scale), _ptr(ws), 256, _stream()))
@@ -684,3 +701,91 @@ def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
             ctypes.byref(d), T, x.data_ptr(), ctypes.byref(r), ctypes.byref(e), ids.data_ptr(),
             gates.data_ptr(), y.data_ptr(), yd, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return y, ids, gates
+
+
+@dataclass
+class BlockWeight:
+    """A weight [N, K] packed by moe_block_pack: E4M3 codes u8 [N, K] and one fp32
+    scale per 128 x 128 block, [ceil(N / 128), ceil(K / 128)]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _matrix(t: torch.Tensor, dtype, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
+    return _dev(t, dtype, name)
+
+
+def block_pack(w: torch.Tensor) -> BlockWeight:
+    """moe_block_pack: bf16 [N, K] -> E4M3 codes with a scale per 128 x 128 block."""
+    N, K = _matrix(w, torch.bfloat16, "w").shape
+    codes = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((-(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
+    with _on(w.device):
+        _check("moe_block_pack", lib().moe_block_pack(N, K, w.data_ptr(), codes.data_ptr(),
+                                                      scales.data_ptr(), _raw_stream(w.device)))
+    return BlockWeight(codes, scales)
+
+
+def block_quantize(x: torch.Tensor):
+    """moe_block_quantize: bf16 [M, K] -> (codes u8 [M, K], scales fp32
+    [ceil(K / 128), M])."""
+    M, K = _matrix(x, torch.bfloat16, "x").shape
+    codes = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((-(-K // 128), M), dtype=torch.float32, device=x.device)
+    with _on(x.device):
+        _check("moe_block_quantize", lib().moe_block_quantize(
+            M, K, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _raw_stream(x.device)))
+    return codes, scales
+
+
+def _block_operands(rows: torch.Tensor, weight: BlockWeight, y: Optional[torch.Tensor]):
+    M, K = rows.shape
+    N = weight.codes.shape[0]
+    _dev(weight.codes, torch.uint8, "weight.codes", (N, K))
+    _dev(weight.scales, torch.float32, "weight.scales", (-(-N // 128), -(-K // 128)))
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=rows.device)
+    else:
+        _dev(y, torch.bfloat16, "y", (M, N))
+    _same_device(rows.device, **{"weight.codes": weight.codes, "weight.scales": weight.scales, "y": y})
+    return M, N, K, y
+
+
+def block_matmul(codes: torch.Tensor, scales: torch.Tensor, weight: BlockWeight,
+                 y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_block_matmul: bf16 [M, N] from codes and scales of block_quantize."""
+    _matrix(codes, torch.uint8, "codes")
+    M, N, K, y = _block_operands(codes, weight, y)
+    _dev(scales, torch.float32, "scales", (-(-K // 128), M))
+    _same_device(codes.device, scales=scales)
+    with _on(codes.device):
+        _check("moe_block_matmul", lib().moe_block_matmul(
+            M, N, K, codes.data_ptr(), scales.data_ptr(), weight.codes.data_ptr(),
+            weight.scales.data_ptr(), y.data_ptr(), _raw_stream(codes.device)))
+    return y
+
+
+def block_linear_workspace(max_rows: int, K: int, device="cuda") -> torch.Tensor:
+    n = int(lib().moe_block_linear_workspace_size(int(max_rows), int(K)))
+    if n == 0:
+        raise ValueError(f"moe_block_linear_workspace_size: invalid rows {max_rows} or K {K}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def block_linear(x: torch.Tensor, weight: BlockWeight, y: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_block_linear: bf16 [M, N] = x [M, K] quantised by rows, times the weight."""
+    _matrix(x, torch.bfloat16, "x")
+    M, N, K, y = _block_operands(x, weight, y)
+    if ws is None:
+        ws = block_linear_workspace(M, K, x.device)
+    else:
+        _dev(ws, torch.uint8, "ws")
+        _same_device(x.device, ws=ws)
+    with _on(x.device):
+        _check("moe_block_linear", lib().moe_block_linear(
+            M, N, K, x.data_ptr(), weight.codes.data_ptr(), weight.scales.data_ptr(), y.data_ptr(),
+            ws.data_ptr(), ws.numel(), _raw_stream(x.device)))
+    return y

@@ -17,6 +17,7 @@ namespace {
 
 using moe::kBF16;
 using moe::kFP8;
+using moe::kFP8Block;
 using moe::kNVFP4;
 
 constexpr int32_t kMaxTokens = 1 << 20;
@@ -53,7 +54,12 @@ moe_status bank_dims_check(const moe_dims* d) {
   return MOE_OK;
 }
 
-bool fmt_ok(int32_t fmt) { return fmt == kBF16 || fmt == kFP8 || fmt == kNVFP4; }
+bool fmt_ok(int32_t fmt) {
+  return fmt == kBF16 || fmt == kFP8 || fmt == kNVFP4 || fmt == kFP8Block;
+}
+
+// blocks of 128 values along a width
+size_t kblocks(size_t n) { return (n + 127) / 128; }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -68,7 +74,7 @@ bool bank_aligned(const moe_experts* ex) {
 
 struct Layout {
   size_t counts, offsets, scales, chunk_counts, chunk_base, tile_off0, tile_off1, sorted_src,
-      inv, row_gate, act, out_rows, x_q, act_q, total;
+      inv, row_gate, act, out_rows, x_q, x_s, act_q, act_s, total;
   bool has_xq, has_actq, actq_inplace;
   int max_tiles;
 };
@@ -104,10 +110,38 @@ Layout make_layout(const moe_dims* d, int32_t fmt, int32_t T) {
   L.has_xq = fmt != kBF16;
   L.has_actq = fmt != kBF16;
   L.actq_inplace = fmt == kNVFP4;
-  L.x_q = L.has_xq ? alloc(static_cast<size_t>(T) * H * 2) : 0;
-  L.act_q = fmt == kFP8 ? alloc(R * F) : L.act;
+  if (fmt == kFP8Block) {  // codes and block scales
+    L.x_q = alloc(static_cast<size_t>(T) * H);
+    L.x_s = alloc(kblocks(H) * T * 4);
+    L.act_q = alloc(R * F);
+    L.act_s = alloc(kblocks(F) * R * 4);
+  } else {
+    L.x_q = L.has_xq ? alloc(static_cast<size_t>(T) * H * 2) : 0;
+    L.act_q = fmt == kFP8 ? alloc(R * F) : L.act;
+  }
   L.total = (off + kAlign - 1) / kAlign * kAlign;
   L.max_tiles = static_cast<int>(max_tiles);
+  return L;
+}
+
+// operands of the block-scaled product: rows of 16-byte chunks, and fewer
+// than 2^31 rows of tiles
+moe_status block_dims_check(int32_t M, int32_t N, int32_t K) {
+  if (M < 0 || M > kMaxTokens || N <= 0 || K <= 0) return MOE_EINVAL;
+  if (K % 16 || N > (1 << 20) || K > (1 << 20)) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// workspace of moe_block_linear: codes, then scales
+struct BlockLinearLayout {
+  size_t scales, total;
+};
+
+BlockLinearLayout block_linear_layout(int32_t M, int32_t K) {
+  const auto up = [](size_t n) { return (n + kAlign - 1) / kAlign * kAlign; };
+  BlockLinearLayout L{};
+  L.scales = up(static_cast<size_t>(M) * K);
+  L.total = L.scales + up(kblocks(K) * M * 4) + kAlign;
   return L;
 }
 
@@ -181,7 +215,7 @@ CacheView cache_view(void* state, int E, int n_slots) {
 // bytes of one expert's codes and (NVFP4) block scales in a projection N x K
 size_t expert_code_bytes(int fmt, int N, int K) {
   const size_t n = static_cast<size_t>(N) * K;
-  return fmt == kBF16 ? 2 * n : (fmt == kFP8 ? n : n / 2);
+  return fmt == kBF16 ? 2 * n : (fmt == kNVFP4 ? n / 2 : n);
 }
 size_t expert_scale_bytes(int fmt, int N, int K) {
   return fmt == kNVFP4 ? static_cast<size_t>(N) * K / 16 : 0;
@@ -362,6 +396,57 @@ struct StageMarks {
   }
 };
 
+// stages 1 to 4 of the forward pass with an "fp8_block" bank: both
+// quantisations take the scale of each block of 128 values of a row, so no
+// stage waits for a maximum over a whole tensor
+hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const moe_experts* ex,
+                        const moe::PermBufs& p, const int32_t* w_slot, const Layout& L, void* ws,
+                        const StageMarks& marks) {
+  const int H = dims->hidden, F = dims->ffn, E = dims->n_experts, R = T * dims->top_k;
+  const hipStream_t st = marks.st;
+  marks.mark(1);
+  hipError_t err = moe::launch_block_quant(static_cast<const uint16_t*>(x), nullptr, T, H,
+                                           at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s), st);
+  if (err != hipSuccess) return err;
+  marks.mark(2);
+  moe::BlockArgs g{};
+  g.M = R;
+  g.N = F;
+  g.K = H;
+  g.a = at<uint8_t>(ws, L.x_q);
+  g.a_s = at<float>(ws, L.x_s);
+  g.a_rows = T;
+  g.w = static_cast<const uint8_t*>(ex->up);
+  g.w_s = ex->up_s;
+  g.out = at<uint16_t>(ws, L.act);
+  g.E = E;
+  g.tile_off = p.tile_off0;
+  g.max_tiles = (R + p.bm0 - 1) / p.bm0 + (R < E ? R : E);
+  g.offsets = p.offsets;
+  g.sorted_src = p.sorted_src;
+  g.top_k = dims->top_k;
+  g.w_slot = w_slot;
+  err = moe::launch_block_experts(0, T, g, st, marks.gemm(0));
+  if (err != hipSuccess) return err;
+  marks.mark(3);
+  err = moe::launch_block_quant(at<uint16_t>(ws, L.act), p.offsets + E, R, F,
+                                at<uint8_t>(ws, L.act_q), at<float>(ws, L.act_s), st);
+  if (err != hipSuccess) return err;
+  marks.mark(4);
+  g.N = H;
+  g.K = F;
+  g.a = at<uint8_t>(ws, L.act_q);
+  g.a_s = at<float>(ws, L.act_s);
+  g.a_rows = R;
+  g.w = static_cast<const uint8_t*>(ex->down);
+  g.w_s = ex->down_s;
+  g.out = at<float>(ws, L.out_rows);
+  g.tile_off = p.tile_off1;
+  g.max_tiles = (R + p.bm1 - 1) / p.bm1 + (R < E ? R : E);
+  g.row_gate = p.row_gate;
+  return moe::launch_block_experts(1, T, g, st, marks.gemm(1));
+}
+
 // The forward pass.  With `cc` set, the expert weights come from the cache:
 // after the permutation the row counts go to the host, the missing experts
 // are uploaded into slots, and the GEMMs read the slots through slot_of.
@@ -430,9 +515,9 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   p.sorted_src = at<int32_t>(ws, L.sorted_src);
   p.inv = at<int32_t>(ws, L.inv);
   p.row_gate = at<float>(ws, L.row_gate);
-  p.bm0 = moe::gemm_shape(fmt, 0, T).bm;
+  p.bm0 = fmt == kFP8Block ? moe::block_tile_rows(T) : moe::gemm_shape(fmt, 0, T).bm;
   p.tile_off0 = at<int32_t>(ws, L.tile_off0);
-  p.bm1 = moe::gemm_shape(fmt, 1, T).bm;
+  p.bm1 = fmt == kFP8Block ? p.bm0 : moe::gemm_shape(fmt, 1, T).bm;
   p.tile_off1 = at<int32_t>(ws, L.tile_off1);
   p.zero_words = amax_x;  // amax slots of x and of the intermediate
   p.n_zero = 2 * moe::kAmaxSlots;
@@ -513,6 +598,16 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
       return MOE_EHIP;
     w_slot = c->slot_of;
     if (cc->stats) *cc->stats = moe_cache_stats{touched, hits, misses, bytes};
+  }
+
+  if (fmt == kFP8Block) {
+    const hipError_t be = block_stages(dims, T, x, ex, p, w_slot, L, ws, marks);
+    if (be != hipSuccess) return MOE_EHIP;
+    marks.mark(5);
+    const int mode = accumulate ? moe::kYF32Add : (y_dtype == MOE_Y_F32 ? moe::kYF32 : moe::kYBF16);
+    err = moe::launch_combine(at<float>(ws, L.out_rows), p.inv, T, k, H, y, mode, st);
+    marks.mark(6);
+    return hip_status(err);
   }
 
   // 2. token quantisation (fp8 / nvfp4)
@@ -655,7 +750,7 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt, const void* up_b
                              const void* down_bf16, void* up_q, void* down_q, uint8_t* up_bs,
                              uint8_t* down_bs, float* up_s, float* down_s, void* stream) {
   if (const moe_status ds = bank_dims_check(dims)) return ds;
-  if (fmt != kFP8 && fmt != kNVFP4) return MOE_EINVAL;
+  if (fmt != kFP8 && fmt != kNVFP4 && fmt != kFP8Block) return MOE_EINVAL;
   if (!up_bf16 || !down_bf16 || !up_q || !down_q || !up_s || !down_s) return MOE_EINVAL;
   if (fmt == kNVFP4 && (!up_bs || !down_bs)) return MOE_EINVAL;
   if (!aligned(up_bf16, 16) || !aligned(down_bf16, 16) || !aligned(up_q, 16) ||
@@ -664,6 +759,14 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt, const void* up_b
     return MOE_EINVAL;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int H = dims->hidden, F = dims->ffn, E = dims->n_experts;
+  if (fmt == kFP8Block) {
+    hipError_t be = moe::launch_block_pack(static_cast<const uint16_t*>(up_bf16), E, F, H,
+                                           static_cast<uint8_t*>(up_q), up_s, st);
+    if (be == hipSuccess)
+      be = moe::launch_block_pack(static_cast<const uint16_t*>(down_bf16), E, H, F,
+                                  static_cast<uint8_t*>(down_q), down_s, st);
+    return hip_status(be);
+  }
   hipError_t err = moe::launch_quant_weights(fmt, static_cast<const uint16_t*>(up_bf16), E, F, H,
                                              static_cast<uint8_t*>(up_q), up_bs, up_s, 0, st);
   if (err == hipSuccess)
@@ -675,14 +778,17 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt, const void* up_b
 int32_t moe_quantize_activation(int32_t fmt, int32_t rows, int32_t cols, const void* x,
                                 void* codes, uint8_t* bs, float* scale, void* ws,
                                 size_t ws_bytes, void* stream) {
-  if (fmt != kFP8 && fmt != kNVFP4) return MOE_EINVAL;
+  if (fmt != kFP8 && fmt != kNVFP4 && fmt != kFP8Block) return MOE_EINVAL;
   if (rows < 0 || cols <= 0 || cols % 64) return MOE_EINVAL;
   if (static_cast<long long>(rows) * cols > (1ll << 31)) return MOE_EUNSUPPORTED;
   if (!x || !codes || !scale || (fmt == kNVFP4 && !bs)) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 8) || !aligned(scale, 4)) return MOE_EINVAL;
-  if (!ws || ws_bytes < kAlign || !aligned(ws, 4)) return MOE_EWORKSPACE;
+  if (fmt != kFP8Block && (!ws || ws_bytes < kAlign || !aligned(ws, 4))) return MOE_EWORKSPACE;
   if (rows == 0) return MOE_OK;
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (fmt == kFP8Block)
+    return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), nullptr, rows, cols,
+                                              static_cast<uint8_t*>(codes), scale, st));
   uint32_t* amax = static_cast<uint32_t*>(ws);  // kAmaxSlots words
   hipError_t err = moe::launch_zero_u32(amax, moe::kAmaxSlots, st);
   if (err == hipSuccess)
@@ -766,7 +872,9 @@ int32_t moe_residual_norm(int32_t T, int32_t H, const void* x, const void* y, in
 }
 
 size_t moe_layer_few_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens) {
-  if (!dims_ok(dims) || !fmt_ok(fmt) || max_tokens < 0 || max_tokens > moe::kFewTokens) return 0;
+  if (!dims_ok(dims) || !fmt_ok(fmt) || fmt == kFP8Block || max_tokens < 0 ||
+      max_tokens > moe::kFewTokens)
+    return 0;
   return few_layout(dims, max_tokens).total;
 }
 
@@ -777,7 +885,7 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   if (!experts || T < 0 || T > kMaxTokens) return MOE_EINVAL;
   if (!fmt_ok(experts->fmt)) return MOE_EINVAL;
   if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
-  if (T > moe::kFewTokens) return MOE_EUNSUPPORTED;
+  if (T > moe::kFewTokens || experts->fmt == kFP8Block) return MOE_EUNSUPPORTED;
   if (!moe::few_fits(T, dims->hidden, dims->ffn)) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;  // nothing is read or written; pointers may be null
   if (!router || !router->w_packed || !x || !ids || !gates || !y) return MOE_EINVAL;
@@ -814,6 +922,69 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   g.y = y;
   g.y_bf16 = y_dtype == MOE_Y_BF16;
   return hip_status(moe::launch_few(experts->fmt, g, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales,
+                       void* stream) {
+  if (const moe_status cs = block_dims_check(0, N, K)) return cs;
+  if (!w || !codes || !scales) return MOE_EINVAL;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
+  return hip_status(moe::launch_block_pack(static_cast<const uint16_t*>(w), 1, N, K,
+                                           static_cast<uint8_t*>(codes), scales,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, float* scales,
+                           void* stream) {
+  if (const moe_status cs = block_dims_check(M, 1, K)) return cs;
+  if (M == 0) return MOE_OK;
+  if (!x || !codes || !scales) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
+  return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), nullptr, M, K,
+                                            static_cast<uint8_t*>(codes), scales,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_block_matmul(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,
+                         const void* w_codes, const float* w_scales, void* y, void* stream) {
+  if (const moe_status cs = block_dims_check(M, N, K)) return cs;
+  if (M == 0) return MOE_OK;
+  if (!codes || !scales || !w_codes || !w_scales || !y) return MOE_EINVAL;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(w_codes, 16) || !aligned(w_scales, 4) ||
+      !aligned(y, 16))
+    return MOE_EINVAL;
+  moe::BlockArgs g{};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.a = static_cast<const uint8_t*>(codes);
+  g.a_s = scales;
+  g.a_rows = M;
+  g.w = static_cast<const uint8_t*>(w_codes);
+  g.w_s = w_scales;
+  g.out = y;
+  return hip_status(moe::launch_block_dense(g, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_block_linear_workspace_size(int32_t max_rows, int32_t K) {
+  if (block_dims_check(max_rows, 1, K) != MOE_OK) return 0;
+  return block_linear_layout(max_rows, K).total;
+}
+
+int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const void* w_codes,
+                         const float* w_scales, void* y, void* ws, size_t ws_bytes, void* stream) {
+  if (const moe_status cs = block_dims_check(M, N, K)) return cs;
+  if (M == 0) return MOE_OK;
+  if (!x || !w_codes || !w_scales || !y) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(y, 16))
+    return MOE_EINVAL;
+  const BlockLinearLayout L = block_linear_layout(M, K);
+  if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
+  uint8_t* codes = at<uint8_t>(ws, 0);
+  float* scales = at<float>(ws, L.scales);
+  const int32_t qs = moe_block_quantize(M, K, x, codes, scales, stream);
+  if (qs != MOE_OK) return qs;
+  return moe_block_matmul(M, N, K, codes, scales, w_codes, w_scales, y, stream);
 }
 
 }  // extern "C"

@@ -6,10 +6,10 @@
 
 namespace moe {
 
-enum Fmt { kBF16 = 0, kFP8 = 1, kNVFP4 = 2 };
+enum Fmt { kBF16 = 0, kFP8 = 1, kNVFP4 = 2, kFP8Block = 3 };
 // GEMM operand modes: kFP8 runs the FP8 MFMA on E4M3 codes; kFP8X expands
 // E4M3 weight codes to bf16 (exact) in LDS and runs the BF16 MFMA.
-constexpr int kFP8X = 3;
+constexpr int kFP8X = 16;
 
 constexpr int kChunk = 2048;  // flat (token, slot) entries per permutation chunk
 
@@ -192,5 +192,37 @@ struct FewArgs {
 };
 bool few_fits(int T, int H, int F);
 hipError_t launch_few(int fmt, const FewArgs& g, hipStream_t stream);
+
+// E4M3 with a scale per block of 128 (moe_block_*, "fp8_block" banks)
+enum BlockMode { kBlockDense = 0, kBlockUp = 1, kBlockDown = 2 };
+constexpr int kBlockDecodeMaxT = 256;  // grouped batches below this: 32-row tiles
+struct BlockArgs {
+  int M, N, K;
+  const uint8_t* a;   // codes [rows, K]
+  const float* a_s;   // [ceil(K / 128), a_rows]
+  int a_rows;
+  const uint8_t* w;   // codes [E, N, K]
+  const float* w_s;   // [E, ceil(N / 128), ceil(K / 128)]
+  void* out;          // dense: bf16 [M, N]; up: bf16 [R, N]; down: fp32 [R, N]
+  // grouped products, as GemmArgs
+  int E;
+  const int32_t* tile_off;
+  int max_tiles;
+  const int32_t* offsets;
+  const int32_t* sorted_src;
+  int top_k;
+  const int32_t* w_slot;
+  const float* row_gate;
+};
+// rows per tile of the grouped products for T tokens
+int block_tile_rows(int T);
+hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_t stream,
+                                const KernelEvents& ev = KernelEvents{});
+hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream);
+// codes [rows, cols] and scales [ceil(cols / 128), rows] of bf16 rows
+hipError_t launch_block_quant(const uint16_t* x, const int32_t* n_rows_dev, int rows, int cols,
+                              uint8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_block_pack(const uint16_t* w, int E, int N, int K, uint8_t* codes, float* scales,
+                             hipStream_t stream);
 
 }  // namespace moe
