@@ -116,7 +116,8 @@ typedef struct {
  *          p = n / 128, from the expert's base.  moe_quantize_experts
  *          writes this layout; a GEMM tile then reads one contiguous block
  *          per K step.
- *   FP8_BLOCK: up u8 E4M3 [E, F, H], down u8 [E, H, F], row-major; up_s fp32
+ *   FP8_BLOCK: up, down u8 E4M3, each expert's [F, H] / [H, F] matrix packed as
+ *          by moe_block_pack (moe_block_packed_size bytes an expert); up_s fp32
  *          [E, ceil(F/128), ceil(H/128)], down_s fp32 [E, ceil(H/128),
  *          ceil(F/128)], a scale for each 128 x 128 block (the last ones of a
  *          row or column of blocks may be smaller)
@@ -393,17 +394,27 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  * in fp32.
  *   x        [dev] bf16 [M, K]          codes [dev] u8 E4M3 [M, K], row-major
  *   scales   [dev] fp32 [ceil(K/128), M]: block by block, tokens contiguous
- *   w        [dev] bf16 [N, K]          w_codes [dev] u8 E4M3 [N, K], row-major
+ *   w        [dev] bf16 [N, K]
+ *   w_codes  [dev] u8, moe_block_packed_size(N, K) = ceil(N/16) * ceil(K/128) *
+ *            2048 bytes: the E4M3 code of w[n, k] at
+ *              (n / 16 * ceil(K/128) + k / 128) * 2048 + k % 32 / 16 * 1024 +
+ *              (k % 128 / 32 * 16 + n % 16) * 16 + k % 16
+ *            and zeros past N and K: the order in which the matrix instruction
+ *            takes them, so that weights are read in contiguous runs
  *   w_scales [dev] fp32 [ceil(N/128), ceil(K/128)]
  *   y        [dev] bf16 [M, N], written in full
- * moe_block_pack quantises a weight (once), moe_block_quantize activations;
+ * moe_block_pack quantises and packs a weight (once), moe_block_pack_codes packs
+ * the row-major codes [N, K] of a checkpoint whose block scales are used as they
+ * are (packed must not be codes); moe_block_quantize quantises activations;
  * moe_block_linear is moe_block_quantize into its workspace followed by
  * moe_block_matmul.  K % 16 == 0 (MOE_EUNSUPPORTED otherwise), any N, M from 0
  * (a no-op) to 1 << 20, N and K up to 1 << 20; x, y, w and codes 16-byte
  * aligned, scales 4-byte; ws 256-byte aligned, ws_bytes >=
- * moe_block_linear_workspace_size(M, K).  Codes 0x7f and 0xff (NaN) spread to
- * the rows and columns that read them. */
+ * moe_block_linear_workspace_size(M, K).  A NaN code (0x7f, 0xff) spreads to the
+ * row or column of y that reads it and no further. */
 int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales, void* stream);
+size_t moe_block_packed_size(int32_t N, int32_t K);
+int32_t moe_block_pack_codes(int32_t N, int32_t K, const void* codes, void* packed, void* stream);
 int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, float* scales,
                            void* stream);
 int32_t moe_block_matmul(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,

@@ -121,6 +121,9 @@ _SIGS = {
                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "moe_block_pack": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_block_packed_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "moe_block_pack_codes": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_void_p]),
     "moe_block_quantize": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "moe_block_matmul": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
@@ -500,8 +503,8 @@ def quantize_experts(up: torch.Tensor, down: torch.Tensor, fmt: str,
         up_bs = torch.empty((E, F * H // 16), dtype=torch.uint8, device=dev)
         down_bs = torch.empty((E, H * F // 16), dtype=torch.uint8, device=dev)
     elif fmt == "fp8_block":
-        up_q = torch.empty((E, F, H), dtype=torch.uint8, device=dev)
-        down_q = torch.empty((E, H, F), dtype=torch.uint8, device=dev)
+        up_q = torch.empty((E, block_packed_size(F, H)), dtype=torch.uint8, device=dev)
+        down_q = torch.empty((E, block_packed_size(H, F)), dtype=torch.uint8, device=dev)
         up_bs = down_bs = None
     else:
         raise ValueError(fmt)
@@ -705,10 +708,19 @@ def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
 
 @dataclass
 class BlockWeight:
-    """A weight [N, K] packed by moe_block_pack: E4M3 codes u8 [N, K] and one fp32
-    scale per 128 x 128 block, [ceil(N / 128), ceil(K / 128)]."""
+    """A weight of `shape` (N, K) packed by moe_block_pack: E4M3 codes u8
+    [block_packed_size(N, K)] and one fp32 scale per 128 x 128 block,
+    [ceil(N / 128), ceil(K / 128)]."""
     codes: torch.Tensor
     scales: torch.Tensor
+    shape: tuple
+
+
+def block_packed_size(N: int, K: int) -> int:
+    n = int(lib().moe_block_packed_size(int(N), int(K)))
+    if n == 0:
+        raise ValueError(f"moe_block_packed_size: invalid N {N} or K {K} (K % 16 == 0)")
+    return n
 
 
 def _matrix(t: torch.Tensor, dtype, name: str):
@@ -720,12 +732,28 @@ def _matrix(t: torch.Tensor, dtype, name: str):
 def block_pack(w: torch.Tensor) -> BlockWeight:
     """moe_block_pack: bf16 [N, K] -> E4M3 codes with a scale per 128 x 128 block."""
     N, K = _matrix(w, torch.bfloat16, "w").shape
-    codes = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+    codes = torch.empty(block_packed_size(N, K), dtype=torch.uint8, device=w.device)
     scales = torch.empty((-(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
     with _on(w.device):
         _check("moe_block_pack", lib().moe_block_pack(N, K, w.data_ptr(), codes.data_ptr(),
                                                       scales.data_ptr(), _raw_stream(w.device)))
-    return BlockWeight(codes, scales)
+    return BlockWeight(codes, scales, (N, K))
+
+
+def block_pack_codes(codes: torch.Tensor, scales: torch.Tensor) -> BlockWeight:
+    """moe_block_pack_codes: row-major E4M3 codes [N, K] (u8 or float8_e4m3fn) and
+    their block scales fp32 [ceil(N / 128), ceil(K / 128)], as a checkpoint holds
+    them."""
+    if isinstance(codes, torch.Tensor) and codes.dtype == torch.float8_e4m3fn:
+        codes = codes.view(torch.uint8)
+    N, K = _matrix(codes, torch.uint8, "codes").shape
+    _dev(scales, torch.float32, "scales", (-(-N // 128), -(-K // 128)))
+    _same_device(codes.device, scales=scales)
+    packed = torch.empty(block_packed_size(N, K), dtype=torch.uint8, device=codes.device)
+    with _on(codes.device):
+        _check("moe_block_pack_codes", lib().moe_block_pack_codes(
+            N, K, codes.data_ptr(), packed.data_ptr(), _raw_stream(codes.device)))
+    return BlockWeight(packed, scales, (N, K))
 
 
 def block_quantize(x: torch.Tensor):
@@ -742,8 +770,10 @@ def block_quantize(x: torch.Tensor):
 
 def _block_operands(rows: torch.Tensor, weight: BlockWeight, y: Optional[torch.Tensor]):
     M, K = rows.shape
-    N = weight.codes.shape[0]
-    _dev(weight.codes, torch.uint8, "weight.codes", (N, K))
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError(f"weight: K is {weight.shape[1]}, the rows have {K}")
+    _dev(weight.codes, torch.uint8, "weight.codes", ((N + 15) // 16 * -(-K // 128) * 2048,))
     _dev(weight.scales, torch.float32, "weight.scales", (-(-N // 128), -(-K // 128)))
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=rows.device)

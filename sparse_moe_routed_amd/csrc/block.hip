@@ -13,10 +13,16 @@
 // row is 100 times the others), far below the bf16 rounding of y (1.7e-3), and
 // sums across blocks are fp32.
 //
-// Codes are stored row-major; K is a multiple of 16.  Scales of activations lie
-// block by block, [ceil(K / 128), rows], so that the tokens of one MFMA read
+// Weight codes are packed in operand order: for each group of 16 rows and each
+// K block 2 KB, [half h][lane l][16 bytes] = row l % 16, values 32 (l / 16) + 16 h
+// and on, zeros past N and K.  A wave reads its operand with two contiguous 1 KB
+// loads straight into registers: weights need no LDS and no masks, and a weight
+// stream is one contiguous run per 16 rows whatever K is.  Activation codes are
+// row-major (their rows are gathered) and go through LDS.  Scales of activations
+// lie block by block, [ceil(K / 128), rows], so that the tokens of one MFMA read
 // consecutive words; weight scales are [ceil(N / 128), ceil(K / 128)].
 #include <hip/hip_ext.h>
+#include <type_traits>
 
 #include "moe_common.h"
 #include "moe_internal.h"
@@ -83,13 +89,22 @@ __global__ __launch_bounds__(kQThreads) void block_quant_kernel(
   }
 }
 
+// where value k of weight row n lies in a packed matrix of kb_n K blocks
+__device__ __forceinline__ size_t packed_at(int n, int k, int kb_n) {
+  const int in = k & 127;
+  return (static_cast<size_t>(n >> 4) * kb_n + (k >> 7)) * 2048 + ((in >> 4) & 1) * 1024 +
+         ((in >> 5) * 16 + (n & 15)) * 16 + (k & 15);
+}
+
 // ---- weights: a workgroup per 128 x 128 block; rows of 16 lanes
 __global__ __launch_bounds__(kQThreads) void block_pack_kernel(const uint16_t* __restrict__ w, int N,
                                                                int K, uint8_t* __restrict__ codes,
                                                                float* __restrict__ scales) {
   __shared__ float part[kQThreads / 64];
   const int kb = blockIdx.x, nb = blockIdx.y;
-  const size_t base = static_cast<size_t>(blockIdx.z) * N * K;
+  const int n16 = (N + 15) / 16 * 16;
+  const uint16_t* const src = w + static_cast<size_t>(blockIdx.z) * N * K;
+  uint8_t* const dst = codes + static_cast<size_t>(blockIdx.z) * n16 * gridDim.x * 128;
   const int r0 = threadIdx.x >> 4, k = kb * 128 + (threadIdx.x & 15) * 8;
   u32x4 v[8];
   float m = 0.f;
@@ -97,7 +112,7 @@ __global__ __launch_bounds__(kQThreads) void block_pack_kernel(const uint16_t* _
   for (int j = 0; j < 8; ++j) {
     const int n = nb * 128 + r0 + 16 * j;
     v[j] = u32x4{0u, 0u, 0u, 0u};
-    if (n < N && k < K) v[j] = *reinterpret_cast<const u32x4*>(w + base + static_cast<size_t>(n) * K + k);
+    if (n < N && k < K) v[j] = *reinterpret_cast<const u32x4*>(src + static_cast<size_t>(n) * K + k);
     m = fmaxf(m, amax8(v[j]));
   }
   m = wave_max(m);
@@ -109,12 +124,25 @@ __global__ __launch_bounds__(kQThreads) void block_pack_kernel(const uint16_t* _
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int n = nb * 128 + r0 + 16 * j;
-    if (n < N && k < K)
-      *reinterpret_cast<uint2*>(codes + base + static_cast<size_t>(n) * K + k) = encode8(v[j], inv);
+    if (n < n16) *reinterpret_cast<uint2*>(dst + packed_at(n, k, gridDim.x)) = encode8(v[j], inv);
   }
   if (threadIdx.x == 0)
     scales[(static_cast<size_t>(blockIdx.z) * gridDim.y + nb) * gridDim.x + kb] =
         live ? __fdiv_rn(m, 448.f) : 0.f;
+}
+
+// row-major codes [N, K] into the packed order, 16 bytes a thread
+__global__ __launch_bounds__(kQThreads) void block_pack_codes_kernel(const uint8_t* __restrict__ q, int N,
+                                                                     int K, uint8_t* __restrict__ codes) {
+  const int kb_n = (K + 127) / 128, n16 = (N + 15) / 16 * 16;
+  const int64_t total = static_cast<int64_t>(n16) * kb_n * 8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kQThreads) {
+    const int n = static_cast<int>(i / (kb_n * 8)), k = static_cast<int>(i % (kb_n * 8)) * 16;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (n < N && k < K) v = *reinterpret_cast<const u32x4*>(q + static_cast<size_t>(n) * K + k);
+    *reinterpret_cast<u32x4*>(codes + packed_at(n, k, kb_n)) = v;
+  }
 }
 
 // ---- products
@@ -135,8 +163,8 @@ __device__ __forceinline__ int owner_expert(const int32_t* __restrict__ tile_off
 struct TileAt {
   int row0, rows;  // first row (of M, or of the sorted rows) and valid rows
   int n0;          // first weight row
-  size_t w_row;    // weight rows before it: the matrix's, then n0
-  size_t w_blk;    // 128 x 128 scale rows before the matrix's
+  const uint8_t* w;  // the matrix's codes
+  size_t w_blk;      // 128 x 128 scale rows before the matrix's
 };
 
 // The tile of this workgroup, false for a surplus one.  Workgroups go round
@@ -169,7 +197,7 @@ __device__ __forceinline__ bool find_tile(const BlockArgs& g, int bm, int bn, Ti
   }
   t.n0 = nt * bn;
   const int ew = MODE != kBlockDense && g.w_slot ? g.w_slot[e] : e;
-  t.w_row = static_cast<size_t>(ew) * g.N + t.n0;
+  t.w = g.w + static_cast<size_t>(ew) * ((g.N + 15) / 16 * 16) * ((g.K + 127) / 128 * 128);
   t.w_blk = static_cast<size_t>(e) * ((g.N + 127) / 128);
   return true;
 }
@@ -212,31 +240,53 @@ __device__ __forceinline__ void store4(const BlockArgs& g, int row, int n, f32x4
   }
 }
 
-// ---- few rows (a decode batch, or a ragged expert's rows): 32 weight rows x 16 G
-// rows per workgroup, the K blocks dealt to 8 waves, each streaming its blocks
-// from memory into registers one block ahead.  Bound by the weights' bytes; the
-// waves' sums are joined through LDS in wave order.  Lines are loaded whole (8
-// lanes to a row's 128 bytes) and turned into operand order in 2 KB pieces of
-// LDS that belong to the wave.
+// Buffer descriptors: raw 32-bit data; a load past num_records reads zero and
+// touches no memory, so loads past the last K block are issued all the same, and
+// every wave has the same number of loads under way.  What lies past the end is
+// past it by the lane's own offset (kPastEnd, or a descriptor of no records with
+// a scalar offset of 0), whether or not the range check counts the scalar offset.
+constexpr int kRawBuffer = 0x00027000;
+constexpr uint32_t kPastEnd = kBlockMaxBytes;  // and 4 KB on: beyond every buffer
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kRawBuffer);
+}
+
+// the operand of 16 weight rows and one K block: `at` is the lane's offset of the
+// rows' first block, kPastEnd for rows past N
+template <bool ONCE>
+__device__ __forceinline__ void load_weights(u32x4 (&w)[2], Buffer b, uint32_t at, uint32_t block_at) {
+  constexpr int kPolicy = ONCE ? 2 : 0;  // non-temporal where no other workgroup reads them
+  w[0] = __builtin_amdgcn_raw_buffer_load_b128(b, at, block_at, kPolicy);
+  w[1] = __builtin_amdgcn_raw_buffer_load_b128(b, at + 1024u, block_at, kPolicy);
+}
+
+// ---- few rows: 32 weight rows x 16 G rows per workgroup, the K blocks dealt to 8
+// waves, each one block ahead of its products.  Bound by the weights' bytes and
+// the latency of a few blocks; the waves' sums are joined through LDS in wave
+// order.  The rows' codes come a line at a time (8 lanes to 128 bytes) and are
+// turned into operand order in 2 KB of LDS that belong to the wave.
 constexpr int kSmallWaves = 8;
 constexpr int kSmallN = 32;
 
 template <int MODE, int G>
 __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockArgs g) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kSmallWaves][8192];
+  constexpr int kTurn = 4096, kJoin = G * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kSmallWaves * (kTurn > kJoin ? kTurn : kJoin)];
   TileAt t;
   if (!find_tile<MODE>(g, 16 * G, kSmallN, t)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
   const int K = g.K, blocks = (K + 127) / 128;
   const int lr = lane >> 3, ch = lane & 7;  // row of 8 and 16-byte chunk this lane loads
   // groups of 16 rows that hold any
   const int live = __builtin_amdgcn_readfirstlane((t.rows + 15) >> 4);
 
-  const uint8_t* wp[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    wp[i] = g.w + (t.w_row - t.n0 + min(t.n0 + i * 8 + lr, g.N - 1)) * K + ch * 16;
+  // two groups of weight rows; the second may lie past N and is then not read
+  const Buffer wb = buffer_of(t.w + static_cast<size_t>(t.n0 / 16) * blocks * 2048,
+                              (t.n0 + 16 < g.N ? 2u : 1u) * blocks * 2048);
+  const uint32_t wat[2] = {lane * 16u, t.n0 + 16 < g.N ? lane * 16u + blocks * 2048u : kPastEnd};
   const uint8_t* xp[G][2];
   size_t sp[G];
 #pragma unroll
@@ -249,18 +299,16 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
   const float* ws = g.w_s + (t.w_blk + t.n0 / 128) * blocks;
 
   struct Block {
-    u32x4 w[4], x[G][2];
+    u32x4 w[2][2], x[G][2];
     float s[G];
   };
   const u32x4 zero = {0u, 0u, 0u, 0u};
   const auto load = [&](Block& b, int kb) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      load_weights<true>(b.w[i], wb, wat[i], kb * 2048);
     const bool in = kb * 128 + ch * 16 < K;  // a last block may be short
     const int at = in ? kb * 128 : -ch * 16;  // the row's first chunk, then made zero
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      b.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + at));
-      if (!in) b.w[i] = zero;
-    }
     const float sw = ws[kb];
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -279,7 +327,7 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
   for (int f = 0; f < 2; ++f)
 #pragma unroll
     for (int j = 0; j < G; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint8_t* const mine = lds[wave];
+  uint8_t* const mine = lds + wave * kTurn;
   // 16 rows of 128 bytes: chunk x of row r lies at x ^ (r % 8)
   const auto put = [&](int piece, u32x4 a, u32x4 b) {
     u32x4* p = reinterpret_cast<u32x4*>(mine + piece * 2048 + lr * 128 + ((ch ^ lr) << 4));
@@ -292,19 +340,17 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
                 *reinterpret_cast<const u32x4*>(p + (((2 * q + 1) ^ (c & 7)) << 4)));
   };
   const auto multiply = [&](const Block& b) {
-    put(0, b.w[0], b.w[1]);
-    put(1, b.w[2], b.w[3]);
-    const i32x8 w0 = get(0), w1 = get(1);
+    const i32x8 w0 = join(b.w[0][0], b.w[0][1]), w1 = join(b.w[1][0], b.w[1][1]);
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       if (j >= live) continue;
-      put(2 + (j & 1), b.x[j][0], b.x[j][1]);
-      const i32x8 x = get(2 + (j & 1));
+      put(j & 1, b.x[j][0], b.x[j][1]);
+      const i32x8 x = get(j & 1);
       const f32x4 p0 = mma128(w0, x), p1 = mma128(w1, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[0][j][i] += b.s[j] * p0[i];
-        acc[1][j][i] += b.s[j] * p1[i];
+        acc[0][j][i] = __builtin_fmaf(b.s[j], p0[i], acc[0][j][i]);
+        acc[1][j][i] = __builtin_fmaf(b.s[j], p1[i], acc[1][j][i]);
       }
     }
   };
@@ -324,134 +370,230 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < G; ++j)
-      if (j < live) reinterpret_cast<f32x4*>(&lds[0][0])[(wave * G + j) * kWave + lane] = acc[f][j];
+      if (j < live) reinterpret_cast<f32x4*>(lds)[(wave * G + j) * kWave + lane] = acc[f][j];
     __syncthreads();
     if (wave < live) {
       f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kSmallWaves; ++w)
-        v += reinterpret_cast<const f32x4*>(&lds[0][0])[(w * G + wave) * kWave + lane];
+        v += reinterpret_cast<const f32x4*>(lds)[(w * G + wave) * kWave + lane];
       const int r = wave * 16 + c, n = t.n0 + f * 16 + 4 * q;
       if (r < t.rows && n < g.N) store4<MODE>(g, t.row0 + r, n, v);
     }
   }
 }
 
-// ---- many rows: BM x BN tiles, both operands from memory straight into LDS
-// (global_load_lds_dwordx4), one K block per step, two buffers.  Rows are 128
-// bytes; chunk x of row r lies at x ^ ((r / 2) % 8), so that the 16 rows of an
-// operand read fall on distinct banks.  WM x WN waves (rows x weight rows).
-__device__ __attribute__((aligned(16))) uint32_t zeros[4];  // what lies past K
-
-// 16 bytes a lane from p straight into LDS at `to` + 16 * lane
-__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint8_t* to) {
-  __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+// ---- tiles of BM rows x BN weight rows, WM x WN waves, one K block per step.  The
+// rows' codes and scales go from memory straight into LDS (NBUF buffers, NBUF - 1
+// steps under way); rows are 128 bytes, chunk x of row r lies at
+// x ^ ((r / 2) % 8), so that the 16 rows of an operand read fall on distinct
+// banks.  The weights go straight into registers (WBUF operands per wave and
+// group, WBUF - 1 steps under way).
+__device__ __forceinline__ void load16_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, at, step_at, 0, 0);
+}
+__device__ __forceinline__ void load4_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 4, at, step_at, 0, 0);
 }
 
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
-template <int MODE, int BM, int BN, int WM, int WN>
+// s_waitcnt immediate: at most n vector memory operations outstanding
+constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+
+template <int MODE, int BM, int BN, int WM, int WN, int NBUF, int WBUF, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   constexpr int NW = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int MS = WTM / 16, NS = WTN / 16;  // 16 x 16 products of a wave
-  constexpr int QA = BM / 8 / NW, QB = BN / 8 / NW;  // loads (8 rows) per wave and step
-  constexpr int BUF = (BM + BN) * 128;
-  static_assert(QA * 8 * NW == BM && QB * 8 * NW == BN && 128 % WTN == 0, "tile");
+  constexpr int QA = BM / 8 / NW;              // loads of 8 rows per wave and step
+  constexpr int kRowLoads = QA + 1;            // and one of 64 scales
+  constexpr int kRowsAhead = (NBUF - 2) * kRowLoads;         // loads that may be under way: of rows,
+  constexpr int kAhead = kRowsAhead + (WBUF - 1) * 2 * NS;   // and with those of the weights
+  constexpr int SOFF = BM * 128;
+  constexpr int kParts = BM < 64 ? 1 : BM / 64;  // loads of 64 rows' scales
+  constexpr int WOFF = SOFF + kParts * 256;
+  constexpr int BUF = WOFF + 256;
+  static_assert(QA * 8 * NW == BM && 128 % WTN == 0 && BN % WTN == 0, "tile");
+  static_assert(BM % 64 == 0 || BM == 32, "scales come 64 at a time");
+  static_assert((NBUF == 2 || NBUF == 4) && (WBUF == 2 || WBUF == 4) && kAhead < 64, "buffers");
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[BUF];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[BUF];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[NBUF == 4 ? BUF : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds3[NBUF == 4 ? BUF : 16];
   TileAt t;
   if (!find_tile<MODE>(g, BM, BN, t)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int c = lane & 15, q = lane >> 4;
   const int K = g.K, steps = (K + 127) / 128;
 
-  const uint8_t *ap[QA], *bp[QB];
-  int ach[QA], bch[QB];
+  // Rows: gathered ones are addressed from the first activation row (fewer than
+  // 2^32 bytes, checked by the caller), others from the tile's first.
+  const bool gather = MODE == kBlockUp;
+  const size_t first = gather ? 0 : static_cast<size_t>(t.row0);
+  const uint32_t a_bytes = static_cast<uint32_t>(static_cast<size_t>(gather ? g.a_rows : t.rows) * K);
+  const uint8_t* const a = g.a + first * K;
+  uint32_t ar[QA];
 #pragma unroll
   for (int i = 0; i < QA; ++i) {
     const int r = (wave * QA + i) * 8 + (lane >> 3);
-    ach[i] = ((lane & 7) ^ swz(r)) * 16;
-    ap[i] = g.a + source_row<MODE>(g, t.row0 + min(r, t.rows - 1)) * K + ach[i];
+    const int ch = ((lane & 7) ^ swz(r)) * 16;
+    const uint32_t row = static_cast<uint32_t>(source_row<MODE>(g, t.row0 + min(r, t.rows - 1)) - first);
+    ar[i] = row * K + ch;
   }
+  // Scales: wave p < kParts loads those of 64 rows, the others those of the
+  // weights' 128-row blocks (all the same words to the same place), so that
+  // every wave issues the same number of loads.
+  const bool of_rows = wave < kParts;
+  const int w_blk = t.n0 / 128, w_blks = (g.N + 127) / 128;
+  const uint32_t s_at =
+      4 * (of_rows ? static_cast<uint32_t>(source_row<MODE>(g, t.row0 + min(wave * 64 + lane, t.rows - 1)))
+                   : static_cast<uint32_t>(min(lane, w_blks - 1 - w_blk) * steps));
+  const float* const s_from = of_rows ? g.a_s : g.w_s + (t.w_blk + w_blk) * steps;
+  const int s_step = of_rows ? g.a_rows : 1;
+  const uint32_t s_bytes = 4u * (of_rows ? g.a_rows : (w_blks - w_blk) * steps);
+  const int s_to = of_rows ? SOFF + wave * 256 : WOFF;
+  const auto load_rows = [&](int step, uint8_t* buf) __attribute__((always_inline)) {
+    const bool in = step < steps;
+    const Buffer b = buffer_of(a, in ? a_bytes : 0u);
+    const int chunks = min(K / 16 - step * 8, 8);  // a last block may be short
 #pragma unroll
-  for (int i = 0; i < QB; ++i) {
-    const int r = (wave * QB + i) * 8 + (lane >> 3);
-    bch[i] = ((lane & 7) ^ swz(r)) * 16;
-    bp[i] = g.w + (t.w_row - t.n0 + min(t.n0 + r, g.N - 1)) * K + bch[i];
-  }
-  const uint8_t* const past = reinterpret_cast<const uint8_t*>(zeros);
-  const auto dma = [&](int step, uint8_t* buf) {
-    const int kb = step * 128;
-    const bool whole = kb + 128 <= K;
+    for (int i = 0; i < QA; ++i) {
+      const int ch = (lane & 7) ^ swz((wave * QA + i) * 8 + (lane >> 3));
+      load16_to_lds(b, ch < chunks ? ar[i] : kPastEnd, in ? step * 128 : 0, buf + (wave * QA + i) * 1024);
+    }
+    const Buffer sb = buffer_of(s_from + static_cast<size_t>(in ? step : 0) * s_step, in ? s_bytes : 0u);
+    load4_to_lds(sb, s_at, 0, buf + s_to);
+    __builtin_amdgcn_sched_barrier(0);  // the order of the loads is what the waits count on
+  };
+  // weights: the wave's groups of 16 rows; the last one stands in for those past N
+  const int m0 = wm * WTM, nw0 = wn * WTN;
+  const int groups = (g.N - t.n0 - nw0 + 15) / 16;
+  const uint8_t* const w_at = t.w + static_cast<size_t>(t.n0 + nw0) / 16 * steps * 2048;
+  const uint32_t w_bytes = groups <= 0 ? 0u : static_cast<uint32_t>(groups < NS ? groups : NS) * steps * 2048;
+  typedef u32x4 Weights[NS][2];
+  const auto load_w = [&](Weights& w, int step) __attribute__((always_inline)) {
+    const Buffer b = buffer_of(w_at, step < steps ? w_bytes : 0u);
 #pragma unroll
-    for (int i = 0; i < QA; ++i)
-      load_to_lds(whole || kb + ach[i] < K ? ap[i] + kb : past, buf + (wave * QA + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < QB; ++i)
-      load_to_lds(whole || kb + bch[i] < K ? bp[i] + kb : past,
-                  buf + BM * 128 + (wave * QB + i) * 1024);
+    for (int i = 0; i < NS; ++i)
+      load_weights<ONCE>(w[i], b, lane * 16, step < steps ? (max(min(i, groups - 1), 0) * steps + step) * 2048 : 0);
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  // 16-row groups of this wave that hold rows; columns past N are not skipped
-  // but for whole waves
-  const int m0 = wm * WTM, nw0 = wn * WTN;
-  const bool idle = m0 >= t.rows || t.n0 + nw0 >= g.N;
-  size_t src[MS];
-#pragma unroll
-  for (int j = 0; j < MS; ++j) src[j] = source_row<MODE>(g, t.row0 + min(m0 + j * 16 + c, t.rows - 1));
-  const float* ws = g.w_s + (t.w_blk + min(t.n0 + nw0, g.N - 1) / 128) * steps;
-
+  // 16-row groups of this wave that hold rows; a wave whose columns all lie past
+  // N multiplies nothing
+  int live_raw = (t.rows - m0 + 15) >> 4;
+  if (groups <= 0) live_raw = 0;
+  const int live = __builtin_amdgcn_readfirstlane(live_raw < 0 ? 0 : (live_raw > MS ? MS : live_raw));
   f32x4 acc[NS][MS];
 #pragma unroll
   for (int i = 0; i < NS; ++i)
 #pragma unroll
     for (int j = 0; j < MS; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float s[MS];
-  const auto load_scales = [&](int step) {
-    const float sw = ws[step];
-#pragma unroll
-    for (int j = 0; j < MS; ++j) s[j] = g.a_s[static_cast<size_t>(step) * g.a_rows + src[j]] * sw;
+  // this lane's two chunks of row c of a 16-row group (groups are 2 KB apart,
+  // and a group's first row is a multiple of 16, so its swizzle is c's)
+  const int off0 = c * 128 + (((2 * q) ^ swz(c)) << 4), off1 = c * 128 + (((2 * q + 1) ^ swz(c)) << 4);
+  const auto frag = [&](const uint8_t* group) __attribute__((always_inline)) {
+    return join(*reinterpret_cast<const u32x4*>(group + off0), *reinterpret_cast<const u32x4*>(group + off1));
   };
-  const auto frag = [&](const uint8_t* rows, int r) {
-    const uint8_t* p = rows + r * 128;
-    return join(*reinterpret_cast<const u32x4*>(p + (((2 * q) ^ swz(r)) << 4)),
-                *reinterpret_cast<const u32x4*>(p + (((2 * q + 1) ^ swz(r)) << 4)));
-  };
-  const auto compute = [&](const uint8_t* buf) {
-    i32x8 w[NS];
+  // Products run kDeep ahead of the multiply-adds that take their results, so
+  // that a wave has other products to issue while one is in the matrix unit.
+  const auto compute = [&](const uint8_t* buf, const Weights& w, auto live_c)
+                           __attribute__((always_inline)) {
+    constexpr int ML = decltype(live_c)::value;
+    constexpr int kDeep = 2;
+    const uint8_t* const xrow = buf + m0 * 128;
+    const float* const srow = reinterpret_cast<const float*>(buf + SOFF) + m0 + c;
+    const float sw = reinterpret_cast<const float*>(buf + WOFF)[nw0 / 128];
+    i32x8 x[2];
+    x[0] = frag(xrow);
+    float s[2];
+    s[0] = srow[0];
+    f32x4 p[kDeep + 1];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) w[i] = frag(buf + BM * 128, nw0 + i * 16 + c);
-#pragma unroll
-    for (int j = 0; j < MS; ++j) {
-      const i32x8 x = frag(buf, m0 + j * 16 + c);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const f32x4 p = mma128(w[i], x);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] += s[j] * p[r];
+    for (int u = 0; u < ML * NS + kDeep; ++u) {
+      if (u < ML * NS) {
+        const int j = u / NS, i = u % NS;
+        if (i == 0 && j + 1 < ML) x[(j + 1) & 1] = frag(xrow + (j + 1) * 2048);
+        p[u % (kDeep + 1)] = mma128(join(w[i][0], w[i][1]), x[j & 1]);
       }
+      if (u >= kDeep) {
+        const int v = u - kDeep, j = v / NS, i = v % NS;
+        if (i == 0) s[j & 1] *= sw;
+        if (i == 0 && j + 1 < ML) s[(j + 1) & 1] = srow[(j + 1) * 16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = __builtin_fmaf(s[j & 1], p[v % (kDeep + 1)][r], acc[i][j][r]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  const auto body = [&](int step, const uint8_t* cur, uint8_t* ahead) {
-    if (step >= steps) return;
-    load_scales(step);
-    __builtin_amdgcn_s_waitcnt(0);  // this wave's loads of the step
+  // One step: its rows have arrived (this wave's, then at the barrier
+  // everyone's), those of step + NBUF - 1 start into the buffer that everyone
+  // has read, the weights of step + WBUF - 1 into the registers of step - 1,
+  // then the products.  A load that nothing uses is not there to be counted, the
+  // compiler drops it: a wave without products loads no weights and counts none,
+  // and the last steps of all (TAIL, fewer than 4) wait for all that is under way.
+  const auto body = [&](int step, const uint8_t* cur, uint8_t* ahead, const Weights& now, Weights& next,
+                        auto live_c, auto tail_c) __attribute__((always_inline)) {
+    constexpr bool TAIL = decltype(tail_c)::value, kAny = decltype(live_c)::value > 0;
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(TAIL ? 0 : (kAny ? kAhead : kRowsAhead)));
     __asm__ volatile("s_barrier" ::: "memory");
-    if (step + 1 < steps) dma(step + 1, ahead);
-    if (!idle) compute(cur);
+    if (!TAIL || NBUF == 2) load_rows(step + NBUF - 1, ahead);
+    if (kAny && (!TAIL || WBUF == 2)) load_w(next, step + WBUF - 1);
+    if constexpr (kAny) compute(cur, now, live_c);
   };
-  dma(0, lds0);
-  for (int step = 0; step < steps; step += 2) {
-    body(step, lds0, lds1);
-    body(step + 1, lds1, lds0);
-  }
-  if (idle) return;
+  const auto run = [&](auto live_c) __attribute__((always_inline)) {
+    Weights w0, w1, w2, w3;
+    load_rows(0, lds0);
+    if (NBUF == 4) {
+      load_rows(1, lds1);
+      load_rows(2, lds2);
+    }
+    if (decltype(live_c)::value > 0) load_w(w0, 0);
+    if (decltype(live_c)::value > 0 && WBUF == 4) {
+      load_w(w1, 1);
+      load_w(w2, 2);
+    }
+    // (the buffers' and operands' places are fixed in the code, so that the
+    // compiler sees which loads each step has to wait for)
+    int step = 0;
+    const auto one = [&](auto k_c, auto tail_c) __attribute__((always_inline)) {
+      constexpr int k = decltype(k_c)::value, n = k % NBUF, a = (k + NBUF - 1) % NBUF;
+      constexpr int v = k % WBUF, y = (k + WBUF - 1) % WBUF;
+      const uint8_t* const cur = n == 0 ? lds0 : (n == 1 ? lds1 : (n == 2 ? lds2 : lds3));
+      uint8_t* const ahead = a == 0 ? lds0 : (a == 1 ? lds1 : (a == 2 ? lds2 : lds3));
+      Weights& now = v == 0 ? w0 : (v == 1 ? w1 : (v == 2 ? w2 : w3));
+      Weights& next = y == 0 ? w0 : (y == 1 ? w1 : (y == 2 ? w2 : w3));
+      body(step + k, cur, ahead, now, next, live_c, tail_c);
+    };
+    constexpr std::integral_constant<int, 0> k0{};
+    constexpr std::integral_constant<int, 1> k1{};
+    constexpr std::integral_constant<int, 2> k2{};
+    constexpr std::integral_constant<int, 3> k3{};
+    for (; step + 4 <= steps; step += 4) {
+      one(k0, std::false_type{});
+      one(k1, std::false_type{});
+      one(k2, std::false_type{});
+      one(k3, std::false_type{});
+    }
+    if (step >= steps) return;
+    one(k0, std::true_type{});
+    if (step + 1 >= steps) return;
+    one(k1, std::true_type{});
+    if (step + 2 >= steps) return;
+    one(k2, std::true_type{});
+  };
+  static_assert(MS == 2 || MS == 4 || MS == 8, "live groups");
+  // a ragged expert's last rows: products of the groups that hold rows only
+  if (live == 0) run(std::integral_constant<int, 0>{});
+  else if (MODE != kBlockDense && live <= MS / 2) run(std::integral_constant<int, MS / 2>{});
+  else run(std::integral_constant<int, MS>{});
 #pragma unroll
   for (int j = 0; j < MS; ++j) {
     const int r = m0 + j * 16 + c;
-    if (r >= t.rows) continue;
+    if (j >= live || r >= t.rows) continue;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int n = t.n0 + nw0 + i * 16 + 4 * q;
@@ -484,30 +626,54 @@ hipError_t launch_small(const BlockArgs& g, hipStream_t stream, const KernelEven
                   tiles_of(g, MODE, 16 * G, kSmallN), kSmallWaves * kWave, g, stream, ev);
 }
 
-template <int MODE, int BM, int BN, int WM, int WN>
+template <int MODE, int BM, int BN, int WM, int WN, int NBUF, int WBUF, bool ONCE = false>
 hipError_t launch_large(const BlockArgs& g, hipStream_t stream, const KernelEvents& ev = KernelEvents{}) {
-  return dispatch(reinterpret_cast<const void*>(&block_gemm_kernel<MODE, BM, BN, WM, WN>),
+  return dispatch(reinterpret_cast<const void*>(&block_gemm_kernel<MODE, BM, BN, WM, WN, NBUF, WBUF, ONCE>),
                   tiles_of(g, MODE, BM, BN), WM * WN * 64, g, stream, ev);
 }
 
 }  // namespace
 
+// Rows per tile of the experts' products.  Short of 256 tokens an expert has a
+// few rows, and the tile of 32 reads each weight once or twice; 128-row tiles are
+// for the longer ones (T = 255: 261 us with 32 rows, T = 256: 275 us with 128 and
+// 297 us with 32).
 int block_tile_rows(int T) { return T < kBlockDecodeMaxT ? 32 : 128; }
 
+// Full layer (128 experts, 2688 -> 1856 -> 2688), whole forward, graph replay:
+// decode tiles 32 x 64 at T = 5 52.5 us, T = 64 162 us (32 x 128: 54 and 164),
+// weights 3 steps ahead, since each is read once and from memory; prefill tiles
+// 128 x 256 with one wave per 32 columns at T = 4096 608-634 us (2 x 4 waves
+// 676, 128 x 128 643, 64 x 256 712, 256 x 128 724, 256 x 256 670).
 hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_t stream,
                                 const KernelEvents& ev) {
   if (T < kBlockDecodeMaxT)
-    return stage == 0 ? launch_small<kBlockUp, 2>(g, stream, ev) : launch_small<kBlockDown, 2>(g, stream, ev);
-  return stage == 0 ? launch_large<kBlockUp, 128, 128, 2, 2>(g, stream, ev)
-                    : launch_large<kBlockDown, 128, 128, 2, 2>(g, stream, ev);
+    return stage == 0 ? launch_large<kBlockUp, 32, 64, 1, 4, 4, 4, true>(g, stream, ev)
+                      : launch_large<kBlockDown, 32, 64, 1, 4, 4, 4, true>(g, stream, ev);
+  return stage == 0 ? launch_large<kBlockUp, 128, 256, 1, 8, 4, 2>(g, stream, ev)
+                    : launch_large<kBlockDown, 128, 256, 1, 8, 4, 2>(g, stream, ev);
 }
 
+// One matrix.  Few rows (up to 128) split K over the waves of a workgroup, since
+// there are too few tiles for the 256 CUs.  Past that the largest tile is taken
+// that still has about a tile per CU (kFill); each halving of the tile costs
+// 10-20 % of the rate and is worth it only to fill the chip.  3712 x 2688 weights:
+// M = 256 9.5 us with 64 x 64 (64 x 128 12.8, 128 x 128 16.9), M = 512 13.3 with
+// 64 x 128 (64 x 64 15.4, 128 x 128 17.8), M = 1024 19.3 with 128 x 128 (64 x 128
+// 22.0, 128 x 256 30.6), M = 2048 29.8 with 128 x 256 (128 x 128 31.1), M = 4096
+// 50-53 with 256 x 256 (128 x 256 55.7); 1856 x 2688, M = 4096 29.4 with 128 x 256
+// (256 x 256, half the chip, 47.7).
+constexpr int kFill = 200;
 hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream) {
   if (g.M <= 16) return launch_small<kBlockDense, 1>(g, stream);
   if (g.M <= 32) return launch_small<kBlockDense, 2>(g, stream);
   if (g.M <= 128) return launch_small<kBlockDense, 4>(g, stream);
-  if (tiles_of(g, kBlockDense, 256, 256) >= 128) return launch_large<kBlockDense, 256, 256, 2, 4>(g, stream);
-  return launch_large<kBlockDense, 128, 128, 2, 2>(g, stream);
+  const auto fills = [&](int bm, int bn) { return tiles_of(g, kBlockDense, bm, bn) >= kFill; };
+  if (fills(256, 256)) return launch_large<kBlockDense, 256, 256, 2, 4, 4, 2>(g, stream);
+  if (fills(128, 256)) return launch_large<kBlockDense, 128, 256, 1, 8, 4, 2>(g, stream);
+  if (fills(128, 128)) return launch_large<kBlockDense, 128, 128, 2, 4, 4, 2>(g, stream);
+  if (fills(64, 128)) return launch_large<kBlockDense, 64, 128, 2, 4, 4, 2>(g, stream);
+  return launch_large<kBlockDense, 64, 64, 2, 4, 4, 4>(g, stream);
 }
 
 hipError_t launch_block_quant(const uint16_t* x, const int32_t* n_rows_dev, int rows, int cols,
@@ -518,6 +684,15 @@ hipError_t launch_block_quant(const uint16_t* x, const int32_t* n_rows_dev, int 
   if (blocks > 8192) blocks = 8192;
   hipLaunchKernelGGL(block_quant_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0,
                      stream, x, n_rows_dev, rows, cols, rows, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_block_pack_codes(const uint8_t* q, int N, int K, uint8_t* codes, hipStream_t stream) {
+  const int64_t n = static_cast<int64_t>((N + 15) / 16 * 16) * ((K + 127) / 128) * 8;
+  int64_t blocks = (n + kQThreads - 1) / kQThreads;
+  if (blocks > 8192) blocks = 8192;
+  hipLaunchKernelGGL(block_pack_codes_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0,
+                     stream, q, N, K, codes);
   return hipGetLastError();
 }
 

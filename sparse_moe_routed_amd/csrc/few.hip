@@ -292,15 +292,18 @@ struct Tile {
         const_cast<uint8_t*>(codes), 0, in ? static_cast<int>(bytes) : 0, kRawBuffer);
     Unit<FMT> r{};
     const bool tail = u == last;
+    // past the end by the lane's own offset (no records, scalar offset 0, or
+    // kPastEnd), whether or not the range check counts the scalar offset
+    const uint32_t so = in ? u * step : 0u;
     if constexpr (FMT == kNVFP4) {
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<uint8_t*>(scales), 0, in ? static_cast<int>(bytes / 8) : 0, kRawBuffer);
-      r.sb = __builtin_amdgcn_raw_buffer_load_b16(rs, tail ? sat_last : sat, u * (step / 8), kStreamOnce);
-      r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, tail ? at_last : at, u * step, kStreamOnce);
+      r.sb = __builtin_amdgcn_raw_buffer_load_b16(rs, tail ? sat_last : sat, so / 8, kStreamOnce);
+      r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, tail ? at_last : at, so, kStreamOnce);
     } else {
       const uint32_t o = tail ? at_last : at;
-      r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, o, u * step, kStreamOnce);
-      r.v[1] = __builtin_amdgcn_raw_buffer_load_b128(rc, o + (tail ? row8_last : row8), u * step, kStreamOnce);
+      r.v[0] = __builtin_amdgcn_raw_buffer_load_b128(rc, o, so, kStreamOnce);
+      r.v[1] = __builtin_amdgcn_raw_buffer_load_b128(rc, o + (tail ? row8_last : row8), so, kStreamOnce);
     }
     __builtin_amdgcn_sched_barrier(0);
     return r;

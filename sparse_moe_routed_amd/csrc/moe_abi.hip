@@ -215,6 +215,7 @@ CacheView cache_view(void* state, int E, int n_slots) {
 // bytes of one expert's codes and (NVFP4) block scales in a projection N x K
 size_t expert_code_bytes(int fmt, int N, int K) {
   const size_t n = static_cast<size_t>(N) * K;
+  if (fmt == kFP8Block) return (static_cast<size_t>(N) + 15) / 16 * kblocks(K) * 2048;
   return fmt == kBF16 ? 2 * n : (fmt == kNVFP4 ? n / 2 : n);
 }
 size_t expert_scale_bytes(int fmt, int N, int K) {
@@ -492,6 +493,9 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(ids, 4) || !aligned(gates, 4) ||
       !bank_aligned(ex))
     return MOE_EINVAL;
+  // the block-scaled products address the tokens' codes by 32 bits
+  if (ex->fmt == kFP8Block && static_cast<size_t>(T) * dims->hidden >= moe::kBlockMaxBytes)
+    return MOE_EUNSUPPORTED;
   const Layout L = make_layout(dims, ex->fmt, T);
   if (!ws || ws_bytes < L.total) return MOE_EWORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MOE_EWORKSPACE;
@@ -932,6 +936,20 @@ int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* 
   return hip_status(moe::launch_block_pack(static_cast<const uint16_t*>(w), 1, N, K,
                                            static_cast<uint8_t*>(codes), scales,
                                            static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_block_packed_size(int32_t N, int32_t K) {
+  if (block_dims_check(0, N, K) != MOE_OK) return 0;
+  return expert_code_bytes(kFP8Block, N, K);
+}
+
+int32_t moe_block_pack_codes(int32_t N, int32_t K, const void* codes, void* packed, void* stream) {
+  if (const moe_status cs = block_dims_check(0, N, K)) return cs;
+  if (!codes || !packed || codes == packed) return MOE_EINVAL;
+  if (!aligned(codes, 16) || !aligned(packed, 16)) return MOE_EINVAL;
+  return hip_status(moe::launch_block_pack_codes(static_cast<const uint8_t*>(codes), N, K,
+                                                 static_cast<uint8_t*>(packed),
+                                                 static_cast<hipStream_t>(stream)));
 }
 
 int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, float* scales,

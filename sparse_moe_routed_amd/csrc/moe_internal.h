@@ -195,13 +195,14 @@ hipError_t launch_few(int fmt, const FewArgs& g, hipStream_t stream);
 
 // E4M3 with a scale per block of 128 (moe_block_*, "fp8_block" banks)
 enum BlockMode { kBlockDense = 0, kBlockUp = 1, kBlockDown = 2 };
+constexpr uint32_t kBlockMaxBytes = 0xf0000000u;  // gathered activation codes stay below
 constexpr int kBlockDecodeMaxT = 256;  // grouped batches below this: 32-row tiles
 struct BlockArgs {
   int M, N, K;
   const uint8_t* a;   // codes [rows, K]
   const float* a_s;   // [ceil(K / 128), a_rows]
   int a_rows;
-  const uint8_t* w;   // codes [E, N, K]
+  const uint8_t* w;   // codes of E matrices [N, K], packed (block.hip)
   const float* w_s;   // [E, ceil(N / 128), ceil(K / 128)]
   void* out;          // dense: bf16 [M, N]; up: bf16 [R, N]; down: fp32 [R, N]
   // grouped products, as GemmArgs
@@ -222,6 +223,7 @@ hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream);
 // codes [rows, cols] and scales [ceil(cols / 128), rows] of bf16 rows
 hipError_t launch_block_quant(const uint16_t* x, const int32_t* n_rows_dev, int rows, int cols,
                               uint8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_block_pack_codes(const uint8_t* q, int N, int K, uint8_t* codes, hipStream_t stream);
 hipError_t launch_block_pack(const uint16_t* w, int E, int N, int K, uint8_t* codes, float* scales,
                              hipStream_t stream);
 

@@ -56,6 +56,13 @@ def test_validation():
     assert L.moe_block_pack(0, 64, FAKE, FAKE, FAKE, None) == moe.EINVAL
     assert L.moe_block_quantize((1 << 20) + 1, 64, FAKE, FAKE, FAKE, None) == moe.EINVAL
     assert L.moe_block_quantize(0, 64, None, None, None, None) == moe.OK
+    assert L.moe_block_packed_size(17, 144) == 2 * 2 * 2048 and L.moe_block_packed_size(0, 64) == 0
+    assert L.moe_block_packed_size(16, 24) == 0
+    pc = L.moe_block_pack_codes
+    for bad in ((0, 64, FAKE, FAKE + 4096), (16, 0, FAKE, FAKE + 4096), (16, 64, None, FAKE), (16, 64, FAKE, None),
+                (16, 64, FAKE, FAKE), (16, 64, FAKE + 8, FAKE + 4096), (16, 64, FAKE, FAKE + 4104)):
+        assert pc(*bad, None) == moe.EINVAL, bad
+    assert pc(16, 40, FAKE, FAKE + 4096, None) == moe.EUNSUPPORTED
 
     def mm(M=4, N=64, K=64, c=FAKE, s=FAKE, wc=FAKE, ws=FAKE, y=FAKE):
         return L.moe_block_matmul(M, N, K, c, s, wc, ws, y, None)
@@ -113,6 +120,15 @@ def _weight(N, K, seed):
     return (torch.randn((N, K), generator=g) * (0.1 + torch.rand((N, 1), generator=g))).bfloat16()
 
 
+def _unpack(packed, N, K):
+    """Row-major codes [N, K] of packed ones; the padding must be zero."""
+    n, kb = (N + 15) // 16, -(-K // 128)
+    # [group, block, half, k / 32, row, 16] -> [group, row, block, k / 32, half, 16]
+    full = packed.reshape(n, kb, 2, 4, 16, 16).transpose(0, 4, 1, 3, 2, 5).reshape(n * 16, kb * 128)
+    assert not full[N:].any() and not full[:, K:].any()
+    return full[:N, :K]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("N,K", [(1, 16), (3, 80), (130, 144), (64, 128), (257, 192), (12, 2688)])
 def test_quantisers_bit_exact(N, K):
@@ -123,7 +139,12 @@ def test_quantisers_bit_exact(N, K):
     assert np.array_equal(q.cpu().numpy(), qo) and np.array_equal(s.cpu().numpy().T, so)
     w = moe.block_pack(x.cuda())
     qo, so = codecs.fp8_block_quantize(x.float().numpy(), 128)
-    assert np.array_equal(w.codes.cpu().numpy(), qo) and np.array_equal(w.scales.cpu().numpy(), so)
+    assert np.array_equal(_unpack(w.codes.cpu().numpy(), N, K), qo) and np.array_equal(w.scales.cpu().numpy(), so)
+    # codes of a checkpoint
+    row_major = torch.from_numpy(qo).cuda()
+    for c in (row_major, row_major.view(torch.float8_e4m3fn)):
+        again = moe.block_pack_codes(c, w.scales)
+        assert torch.equal(again.codes, w.codes) and again.shape == (N, K)
     tiny = torch.full((2, K), 1e-38).bfloat16().cuda()
     q, s = moe.block_quantize(tiny)
     assert not q.any() and not s.any()
@@ -180,6 +201,23 @@ def test_matmul(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(150, 1000, 2688), (500, 3700, 2000), (1000, 3700, 2688), (2000, 3700, 1856),
+                                   (4000, 3600, 1840), (1500, 9000, 400)])
+def test_tiles_of_long_rows(M, N, K):
+    """Past 128 rows every tile shape adds a row's blocks in the same order, so a
+    row's result is the same bits in any batch; ragged last tiles (some of their
+    waves have no column or row at all) and long K; the same bits every time."""
+    x, w = _rows(M, K, M), _weight(N, K, N)
+    W = moe.block_pack(w.cuda())
+    y = moe.block_linear(x.cuda(), W)
+    few = torch.cat([moe.block_linear(x[i:i + 150].cuda(), W) for i in range(0, M - 149, 150)])
+    assert torch.equal(y[:len(few)], few)
+    for _ in range(8):
+        assert torch.equal(moe.block_linear(x.cuda(), W), y)
+    _check(y[:150], x[:150], w)
+
+
+@pytest.mark.gpu
 def test_rows_are_apart():
     """A row of NaN and one of infinities leave the others as they are, whatever
     kernel the row count selects; so do NaN codes behind a short last block."""
@@ -196,8 +234,9 @@ def test_rows_are_apart():
         q[3] = 0x7F
         got = moe.block_matmul(q, s, W)
         assert torch.equal(got[keep + [4]], want[keep + [4]])
-        V = moe.BlockWeight(W.codes.clone(), W.scales)
-        V.codes[7] = 0xFF
+        rows = torch.from_numpy(_unpack(W.codes.cpu().numpy(), 130, 144)).cuda()
+        rows[7] = 0xFF
+        V = moe.block_pack_codes(rows, W.scales)
         got = moe.block_linear(x.cuda(), V)
         cols = [i for i in range(130) if i != 7]
         assert torch.equal(got[:, cols], want[:, cols])
@@ -212,7 +251,10 @@ def test_refusals_of_the_binding():
                 lambda: moe.block_linear(x[:, :32], W), lambda: moe.block_linear(x[0], W),
                 lambda: moe.block_linear(x, W, y=torch.empty((4, 31), dtype=torch.bfloat16, device="cuda")),
                 lambda: moe.block_linear(x, W, ws=torch.empty(9, device="cuda")),
-                lambda: moe.block_linear(x, moe.BlockWeight(W.codes, W.scales[:, :0])),
+                lambda: moe.block_linear(x, moe.BlockWeight(W.codes, W.scales[:, :0], W.shape)),
+                lambda: moe.block_linear(x, moe.BlockWeight(W.codes[16:], W.scales, W.shape)),
+                lambda: moe.block_linear(x, moe.BlockWeight(W.codes, W.scales, (32, 128))),
+                lambda: moe.block_pack_codes(q.float(), W.scales), lambda: moe.block_pack_codes(q, W.scales[0]),
                 lambda: moe.block_matmul(q, s.t(), W), lambda: moe.block_matmul(q.t(), s, W),
                 lambda: moe.block_pack(x.float()), lambda: moe.block_quantize(x.t())):
         with pytest.raises(ValueError):
@@ -275,7 +317,8 @@ def test_bank_codes_bit_exact():
     for e in (0, 15):
         for src, q, s in ((L.up, L.bank.up, L.bank.up_s), (L.down, L.bank.down, L.bank.down_s)):
             qo, so = codecs.fp8_block_quantize(src[e].float().numpy(), 128)
-            assert np.array_equal(q[e].cpu().numpy(), qo) and np.array_equal(s[e].cpu().numpy(), so)
+            assert np.array_equal(_unpack(q[e].cpu().numpy(), *src[e].shape), qo)
+            assert np.array_equal(s[e].cpu().numpy(), so)
 
 
 @pytest.mark.gpu
@@ -342,6 +385,23 @@ def test_forward_matches_oracle(name, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,T", [("FULL", 4096), ("FULL", 700), ("ODD", 2000), ("WIDE", 1111)])
+def test_long_batch_is_its_parts(name, T):
+    """A token's result does not depend on the batch: the long batches' tiles
+    against the short ones', bit for bit, and the same every time."""
+    L = layer(globals()[name])
+    x = synth.make_tokens(T, L.dims, outliers=True).cuda()
+    ids, gates = moe.route(x, L.router, L.ld)
+    y = moe.forward(x, ids, gates, L.bank, L.ld)
+    parts = [moe.forward(x[i:i + 250], ids[i:i + 250], gates[i:i + 250], L.bank, L.ld) for i in range(0, T, 250)]
+    assert torch.equal(y, torch.cat(parts))
+    ws = moe.workspace(L.ld, "fp8_block", T)
+    for _ in range(8):
+        ws.fill_(255)  # NaN in every format: what no kernel has written shows
+        assert torch.equal(moe.forward(x, ids, gates, L.bank, L.ld, ws=ws), y)
+
+
+@pytest.mark.gpu
 def test_other_calls_with_the_bank():
     L = layer(SMALL)
     x = synth.make_tokens(9, SMALL).cuda()
@@ -354,7 +414,7 @@ def test_other_calls_with_the_bank():
         assert torch.equal(y, want)
     assert st["misses"] == 0 and st["hits"] == len(torch.unique(ids))
     y, st = moe.forward_cached(x, ids, gates, moe.ExpertCache(L.bank, 31, L.ld), L.ld)
-    assert torch.equal(y, want) and st["bytes_uploaded"] == st["misses"] * 2 * 256 * 192
+    assert torch.equal(y, want) and st["bytes_uploaded"] == st["misses"] * (192 * 256 + 256 * 256)
     evs = [torch.cuda.Event(enable_timing=True) for _ in range(moe.N_TIMED_EVENTS)]
     for e in evs:
         e.record()
