@@ -191,7 +191,8 @@ int32_t moe_forward(const moe_dims* dims, int32_t T, const void* x,
  * events[i] is recorded on `stream` before stage i and events[6] after the
  * last one.  Stages: 0 permutation (histogram, prefix sum, scatter), 1 token
  * quantisation (FP8/NVFP4), 2 up projection + ReLU^2, 3 intermediate
- * quantisation (FP8/NVFP4), 4 down projection, 5 combine.
+ * quantisation (FP8/NVFP4; FP8_BLOCK makes the codes in stage 2),
+ * 4 down projection, 5 combine.
  * With n_events >= 11, events[7], events[8] take the start and end of the up
  * projection kernel itself and events[9], events[10] those of the down
  * projection kernel (stamped from the kernels' dispatch packets through
@@ -320,7 +321,8 @@ typedef struct {
   int64_t offsets;    /* int32 [E+1]: exclusive prefix sum of counts         */
   int64_t sorted_src; /* int32 [T*k]: flat (t*k + j) index of each sorted row */
   int64_t inv;        /* int32 [T*k]: sorted row of each flat index, -1 = dropped */
-  int64_t act;        /* bf16 [T*k, F]: a = bf16(relu(h)^2), sorted row order */
+  int64_t act;        /* bf16 [T*k, F]: a = bf16(relu(h)^2), sorted row order;
+                         FP8_BLOCK: 0, only its codes are kept               */
   int64_t out_rows;   /* fp32 [T*k, H]: gate * W_down a~, sorted row order   */
   int64_t x_q;        /* [T, H] dequantised token values without the tensor
                          scale: FP8 bf16 dec(q); NVFP4 fp16 dec(q)*dec(sb);

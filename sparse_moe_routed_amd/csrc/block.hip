@@ -33,6 +33,10 @@ namespace {
 
 constexpr int kQThreads = 256;
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 // amax below this makes a zero block: 448 / amax must stay finite
 constexpr float kTinyAmax = 7.888609e-31f;  // 2^-100
 
@@ -46,15 +50,22 @@ __device__ __forceinline__ float amax8(u32x4 v) {
   return m;
 }
 
+// codes of four bf16 values
+__device__ __forceinline__ uint32_t encode4(uint32_t a, uint32_t b, float inv) {
+  return e4m3_encode4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
+                      __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv);
+}
+
+// the same of values that are 0 or more and at most 448 / inv: nothing to clamp
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, float inv) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(__uint_as_float(a << 16) * inv,
+                                                 __uint_as_float(a & 0xffff0000u) * inv, 0, false);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(__uint_as_float(b << 16) * inv,
+                                         __uint_as_float(b & 0xffff0000u) * inv, lo, true);
+}
+
 __device__ __forceinline__ uint2 encode8(u32x4 v, float inv) {
-  uint32_t c[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t a = v[2 * h], b = v[2 * h + 1];
-    c[h] = e4m3_encode4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
-                        __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv);
-  }
-  return make_uint2(c[0], c[1]);
+  return make_uint2(encode4(v[0], v[1], inv), encode4(v[2], v[3], inv));
 }
 
 // max over each row of 16 lanes, in all of them
@@ -66,12 +77,11 @@ __device__ __forceinline__ float row16_max(float v) {
 
 // ---- activations: 16 lanes take one block of 128 values, 8 values each
 __global__ __launch_bounds__(kQThreads) void block_quant_kernel(
-    const uint16_t* __restrict__ x, const int32_t* n_rows_dev, int rows, int cols, int row_stride,
-    uint8_t* __restrict__ codes, float* __restrict__ scales) {
-  const int nr = n_rows_dev ? min(*n_rows_dev, rows) : rows;
+    const uint16_t* __restrict__ x, int rows, int cols, uint8_t* __restrict__ codes,
+    float* __restrict__ scales) {
   const int kb_n = (cols + 127) / 128;
   const int l16 = threadIdx.x & 15;
-  const int64_t n = static_cast<int64_t>(nr) * kb_n;
+  const int64_t n = static_cast<int64_t>(rows) * kb_n;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kQThreads / 16);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kQThreads / 16) + (threadIdx.x >> 4); i < n;
        i += step) {
@@ -85,7 +95,7 @@ __global__ __launch_bounds__(kQThreads) void block_quant_kernel(
     if (k < cols)
       *reinterpret_cast<uint2*>(codes + at) = encode8(v, live ? __fdiv_rn(448.f, amax) : 0.f);
     if (l16 == 0)
-      scales[static_cast<size_t>(kb) * row_stride + r] = live ? __fdiv_rn(amax, 448.f) : 0.f;
+      scales[static_cast<size_t>(kb) * rows + r] = live ? __fdiv_rn(amax, 448.f) : 0.f;
   }
 }
 
@@ -227,9 +237,9 @@ __device__ __forceinline__ void store4(const BlockArgs& g, int row, int n, f32x4
   } else {
     uint16_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = MODE == kBlockUp ? relu_sq_bf16(v[i]) : f32_to_bf16(v[i]);
+    for (int i = 0; i < 4; ++i) b[i] = f32_to_bf16(v[i]);
     uint16_t* o = static_cast<uint16_t*>(g.out) + static_cast<size_t>(row) * g.N + n;
-    if (MODE == kBlockUp || g.N % 4 == 0) {
+    if (g.N % 4 == 0) {
       *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | (static_cast<uint32_t>(b[1]) << 16),
                                                 b[2] | (static_cast<uint32_t>(b[3]) << 16));
     } else {
@@ -590,14 +600,83 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   if (live == 0) run(std::integral_constant<int, 0>{});
   else if (MODE != kBlockDense && live <= MS / 2) run(std::integral_constant<int, MS / 2>{});
   else run(std::integral_constant<int, MS>{});
+  if constexpr (MODE == kBlockUp) {
+    // bf16(relu(h)^2), then E4M3 with the scale of the row's block of 128
+    // columns, as block_quant_kernel makes them: the tile holds whole blocks, a
+    // block lies in 128 / WTN waves, which join their maxima through LDS.
+    // Columns come in whole groups of 16 (N is a multiple of 16).
+    static_assert(BN % 128 == 0, "whole blocks");
+    __shared__ float part[WN][BM];
+    // Half the work of this part is the rounding of the squares: the fast form
+    // rounds the fp32 square, which is wrong only where that lies on a midpoint
+    // (as one in 2^16 does); then the wave takes the exact form.
+    u16x2 v[MS][NS][2];  // four bf16 values each
+    u16x2 least = {0xffff, 0xffff};
 #pragma unroll
-  for (int j = 0; j < MS; ++j) {
-    const int r = m0 + j * 16 + c;
-    if (j >= live || r >= t.rows) continue;
+    for (int j = 0; j < MS; ++j)
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int n = t.n0 + nw0 + i * 16 + 4 * q;
-      if (n < g.N) store4<MODE>(g, t.row0 + r, n, acc[i][j]);
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float a = fmaxf(acc[i][j][2 * h], 0.f), b = fmaxf(acc[i][j][2 * h + 1], 0.f);
+          const f32x2 sq = {a * a, b * b};
+          v[j][i][h] = __builtin_bit_cast(u16x2, __builtin_convertvector(sq, bf16x2));
+          const u16x2 low = __builtin_bit_cast(
+              u16x2, __builtin_amdgcn_perm(__float_as_uint(sq[1]), __float_as_uint(sq[0]), 0x05040100u));
+          least = __builtin_elementwise_min(least, low ^ 0x8000);
+        }
+    if (__ballot(least[0] == 0 || least[1] == 0)) {
+#pragma unroll
+      for (int j = 0; j < MS; ++j)
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            v[j][i][h] = u16x2{relu_sq_bf16(acc[i][j][2 * h]), relu_sq_bf16(acc[i][j][2 * h + 1])};
+    }
+#pragma unroll
+    for (int j = 0; j < MS; ++j) {
+      u16x2 m2 = {0, 0};  // bf16 values of one sign compare as integers
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i < groups) m2 = __builtin_elementwise_max(m2, __builtin_elementwise_max(v[j][i][0], v[j][i][1]));
+      int amax = m2[0] > m2[1] ? m2[0] : m2[1];
+      amax = max(amax, __shfl_xor(amax, 16));
+      amax = max(amax, __shfl_xor(amax, 32));
+      if (q == 0) part[wn][m0 + j * 16 + c] = __uint_as_float(static_cast<uint32_t>(amax) << 16);
+    }
+    __syncthreads();
+    constexpr int kSharers = 128 / WTN;
+    uint8_t* const codes = static_cast<uint8_t*>(g.out);
+    const int w0 = wn / kSharers * kSharers;
+#pragma unroll
+    for (int j = 0; j < MS; ++j) {
+      const int r = m0 + j * 16 + c;
+      if (j >= live || r >= t.rows) continue;
+      float amax = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSharers; ++w) amax = fmaxf(amax, part[w0 + w][r]);
+      const bool any = amax >= kTinyAmax;
+      const float inv = any ? __fdiv_rn(448.f, amax) : 0.f;
+      const size_t row = static_cast<size_t>(t.row0 + r);
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i < groups)
+          *reinterpret_cast<uint32_t*>(codes + row * g.N + t.n0 + nw0 + i * 16 + 4 * q) =
+              codes4(__builtin_bit_cast(uint32_t, v[j][i][0]), __builtin_bit_cast(uint32_t, v[j][i][1]), inv);
+      if (wn == w0 && q == 0)
+        g.out_s[static_cast<size_t>((t.n0 + nw0) / 128) * g.M + row] = any ? __fdiv_rn(amax, 448.f) : 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < MS; ++j) {
+      const int r = m0 + j * 16 + c;
+      if (j >= live || r >= t.rows) continue;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int n = t.n0 + nw0 + i * 16 + 4 * q;
+        if (n < g.N) store4<MODE>(g, t.row0 + r, n, acc[i][j]);
+      }
     }
   }
 }
@@ -648,7 +727,7 @@ int block_tile_rows(int T) { return T < kBlockDecodeMaxT ? 32 : 128; }
 hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_t stream,
                                 const KernelEvents& ev) {
   if (T < kBlockDecodeMaxT)
-    return stage == 0 ? launch_large<kBlockUp, 32, 64, 1, 4, 4, 4, true>(g, stream, ev)
+    return stage == 0 ? launch_large<kBlockUp, 32, 128, 1, 4, 4, 4, true>(g, stream, ev)
                       : launch_large<kBlockDown, 32, 64, 1, 4, 4, 4, true>(g, stream, ev);
   return stage == 0 ? launch_large<kBlockUp, 128, 256, 1, 8, 4, 2>(g, stream, ev)
                     : launch_large<kBlockDown, 128, 256, 1, 8, 4, 2>(g, stream, ev);
@@ -676,14 +755,14 @@ hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream) {
   return launch_large<kBlockDense, 64, 64, 2, 4, 4, 4>(g, stream);
 }
 
-hipError_t launch_block_quant(const uint16_t* x, const int32_t* n_rows_dev, int rows, int cols,
-                              uint8_t* codes, float* scales, hipStream_t stream) {
+hipError_t launch_block_quant(const uint16_t* x, int rows, int cols, uint8_t* codes, float* scales,
+                              hipStream_t stream) {
   if (rows <= 0) return hipSuccess;
   const int64_t n = static_cast<int64_t>(rows) * ((cols + 127) / 128);
   int64_t blocks = (n + kQThreads / 16 - 1) / (kQThreads / 16);
   if (blocks > 8192) blocks = 8192;
   hipLaunchKernelGGL(block_quant_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0,
-                     stream, x, n_rows_dev, rows, cols, rows, codes, scales);
+                     stream, x, rows, cols, codes, scales);
   return hipGetLastError();
 }
 

@@ -105,7 +105,7 @@ Layout make_layout(const moe_dims* d, int32_t fmt, int32_t T) {
   L.sorted_src = alloc(R * 4);
   L.inv = alloc(R * 4);
   L.row_gate = alloc(R * 4);
-  L.act = alloc(R * F * 2);
+  L.act = fmt == kFP8Block ? 0 : alloc(R * F * 2);
   L.out_rows = alloc(R * H * 4);
   L.has_xq = fmt != kBF16;
   L.has_actq = fmt != kBF16;
@@ -406,7 +406,7 @@ hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const mo
   const int H = dims->hidden, F = dims->ffn, E = dims->n_experts, R = T * dims->top_k;
   const hipStream_t st = marks.st;
   marks.mark(1);
-  hipError_t err = moe::launch_block_quant(static_cast<const uint16_t*>(x), nullptr, T, H,
+  hipError_t err = moe::launch_block_quant(static_cast<const uint16_t*>(x), T, H,
                                            at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s), st);
   if (err != hipSuccess) return err;
   marks.mark(2);
@@ -419,7 +419,8 @@ hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const mo
   g.a_rows = T;
   g.w = static_cast<const uint8_t*>(ex->up);
   g.w_s = ex->up_s;
-  g.out = at<uint16_t>(ws, L.act);
+  g.out = at<uint8_t>(ws, L.act_q);
+  g.out_s = at<float>(ws, L.act_s);
   g.E = E;
   g.tile_off = p.tile_off0;
   g.max_tiles = (R + p.bm0 - 1) / p.bm0 + (R < E ? R : E);
@@ -429,10 +430,7 @@ hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const mo
   g.w_slot = w_slot;
   err = moe::launch_block_experts(0, T, g, st, marks.gemm(0));
   if (err != hipSuccess) return err;
-  marks.mark(3);
-  err = moe::launch_block_quant(at<uint16_t>(ws, L.act), p.offsets + E, R, F,
-                                at<uint8_t>(ws, L.act_q), at<float>(ws, L.act_s), st);
-  if (err != hipSuccess) return err;
+  marks.mark(3);  // the up projection's tiles have written the codes already
   marks.mark(4);
   g.N = H;
   g.K = F;
@@ -791,7 +789,7 @@ int32_t moe_quantize_activation(int32_t fmt, int32_t rows, int32_t cols, const v
   if (rows == 0) return MOE_OK;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (fmt == kFP8Block)
-    return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), nullptr, rows, cols,
+    return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), rows, cols,
                                               static_cast<uint8_t*>(codes), scale, st));
   uint32_t* amax = static_cast<uint32_t*>(ws);  // kAmaxSlots words
   hipError_t err = moe::launch_zero_u32(amax, moe::kAmaxSlots, st);
@@ -958,7 +956,7 @@ int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, flo
   if (M == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
-  return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), nullptr, M, K,
+  return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), M, K,
                                             static_cast<uint8_t*>(codes), scales,
                                             static_cast<hipStream_t>(stream)));
 }

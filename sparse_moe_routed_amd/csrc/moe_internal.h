@@ -204,7 +204,8 @@ struct BlockArgs {
   int a_rows;
   const uint8_t* w;   // codes of E matrices [N, K], packed (block.hip)
   const float* w_s;   // [E, ceil(N / 128), ceil(K / 128)]
-  void* out;          // dense: bf16 [M, N]; up: bf16 [R, N]; down: fp32 [R, N]
+  void* out;          // dense: bf16 [M, N]; up: codes [M, N]; down: fp32 [M, N]
+  float* out_s;       // up: scales [ceil(N / 128), M]
   // grouped products, as GemmArgs
   int E;
   const int32_t* tile_off;
@@ -221,8 +222,8 @@ hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_
                                 const KernelEvents& ev = KernelEvents{});
 hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream);
 // codes [rows, cols] and scales [ceil(cols / 128), rows] of bf16 rows
-hipError_t launch_block_quant(const uint16_t* x, const int32_t* n_rows_dev, int rows, int cols,
-                              uint8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_block_quant(const uint16_t* x, int rows, int cols, uint8_t* codes, float* scales,
+                              hipStream_t stream);
 hipError_t launch_block_pack_codes(const uint8_t* q, int N, int K, uint8_t* codes, hipStream_t stream);
 hipError_t launch_block_pack(const uint16_t* w, int E, int N, int K, uint8_t* codes, float* scales,
                              hipStream_t stream);

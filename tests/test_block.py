@@ -332,13 +332,20 @@ def test_forward_matches_oracle(name, T):
     y = moe.forward(x.cuda(), ids, gates, L.bank, L.ld, ws=ws)
     bank = om.ExpertBank(L.up, L.down, "fp8_block").preload(np.unique(ids.cpu().numpy()), threads=8)
     ref, a = om.forward(x.float().numpy(), ids.cpu().numpy(), gates.double().cpu().numpy(), bank, return_a=True)
-    # The intermediate.  Both sides are rounded to bf16, each by at most half a
-    # step (2^-8), so they are at most one step apart where the squares agree;
-    # h is off by the matrix instruction's cut-off as in _check, e_h, and its
-    # square by 2 h e_h + e_h^2.
+    # The intermediate, from its codes and scales.  Both sides are rounded to
+    # bf16, each by at most half a step (2^-8), so they are at most one step apart
+    # where the squares agree; h is off by the matrix instruction's cut-off as in
+    # _check, e_h, and its square by 2 h e_h + e_h^2: e_a together.  Its code is
+    # off by at most half an E4M3 step (2^-4 of the value, 2^-10 of the scale for
+    # the smallest) and by the fp32 roundings of the scale, 448 / amax and the
+    # product; the scale by the maximum's own error, at most the block's largest.
     lay = moe.workspace_layout(L.ld, "fp8_block", T)
     R, F, k = T * L.dims.top_k, L.dims.ffn, L.dims.top_k
-    act = ws[lay["act"]:lay["act"] + R * F * 2].view(torch.bfloat16).view(R, F).float().cpu().numpy()
+    kb = -(-F // 128)
+    codes = ws[lay["act_q"]:lay["act_q"] + R * F].view(R, F).cpu().numpy()
+    at = lay["act_q"] + -(-R * F // 256) * 256
+    scales = ws[at:at + kb * R * 4].view(torch.float32).view(kb, R).cpu().numpy().T
+    act = codecs.fp8_block_dequantize(codes, scales)
     order = ws[lay["sorted_src"]:lay["sorted_src"] + R * 4].view(torch.int32).cpu().numpy()
     xd = om.quantise_activation(x.float().numpy(), "fp8_block")
     flat = ids.cpu().numpy().reshape(-1)
@@ -349,19 +356,23 @@ def test_forward_matches_oracle(name, T):
             e_h[r] += 2.0 ** -6 * np.outer(np.abs(xd[order[r] // k, b:b + 128]).max(axis=1),
                                            np.abs(bank.up(int(e))[:, b:b + 128]).max(axis=1))
     want = a[order]
-    assert (np.abs(act - want) <= 2.0 ** -7 * want + 2 * np.sqrt(want) * e_h + e_h ** 2).all()
-    assert (act != want).mean() <= 0.05  # one value in a hundred lies that near a border
-    # Its codes, bit for bit from the values the kernel stored.
-    codes = ws[lay["act_q"]:lay["act_q"] + R * F].view(R, F).cpu().numpy()
-    qo, so = codecs.fp8_block_quantize(act)
-    assert np.array_equal(codes, qo)
+    e_a = 2.0 ** -7 * want + 2 * np.sqrt(want) * e_h + e_h ** 2
+    steps = np.repeat(scales.astype(np.float64), 128, 1)[:, :F]
+    assert (np.abs(act - want) <= e_a + (2.0 ** -4 + 2.0 ** -21) * (want + e_a) + 2.0 ** -10 * steps).all()
+    for b in range(kb):
+        w, e = want[:, b * 128:b * 128 + 128].max(1), e_a[:, b * 128:b * 128 + 128].max(1)
+        assert (np.abs(448 * scales[:, b].astype(np.float64) - w) <= e + 2.0 ** -23 * w).all()
+    # One bf16 value in twenty at most lies near enough to a border to fall on its
+    # other side: a code differs where its value does, or its block's maximum.
+    qo, so = codecs.fp8_block_quantize(want)
+    assert (codes != qo).mean() <= 0.1
     # The output, against the oracle's: one value of the intermediate on the
     # other side of a border moves its code by a whole step, whatever its
     # distance, so the difference of the two intermediates is carried through
     # |W_down|; on top come the second product's cut-off and the fp32 sum of
     # top_k rows of up to 3 blocks.
     got_a = np.empty((R, F))
-    got_a[order] = codecs.fp8_block_dequantize(qo, so)
+    got_a[order] = act
     want_a = om.quantise_activation(a, "fp8_block")
     g = gates.double().cpu().numpy().reshape(-1)
     bound = np.zeros((T, L.dims.hidden))
@@ -382,6 +393,42 @@ def test_forward_matches_oracle(name, T):
     yb = moe.forward(x.cuda(), ids, gates, L.bank, L.ld, y_dtype=torch.bfloat16, ws=ws)
     assert torch.equal(yb, y.bfloat16())
     assert torch.equal(moe.forward(x.cuda(), ids, gates, L.bank, L.ld), y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 300, 2100])
+@pytest.mark.parametrize("H,F", [(256, 320), (384, 448), (128, 128)])
+def test_intermediate_codes_bit_exact(T, H, F):
+    """Up rows of one value each: h is a product of a token's code and scales,
+    which fp32 rounds once, so the intermediate's codes and scales are known."""
+    E, k = 16, 3
+    d = moe.LayerDims(H, F, E, k)
+    rng = np.random.default_rng(T + H)
+    col = rng.integers(0, H, (E, F))
+    up = torch.zeros((E, F, H))
+    up[torch.arange(E)[:, None], torch.arange(F)[None], torch.from_numpy(col)] = 1.75
+    down = torch.randn((E, H, F), generator=torch.Generator().manual_seed(2))
+    bank = moe.quantize_experts(up.bfloat16().cuda(), down.bfloat16().cuda(), "fp8_block", d)
+    x = _rows(T, H, T + F)
+    ids = torch.from_numpy(np.stack([rng.permutation(E)[:k] for _ in range(T)])).int()
+    ids[:, 0] = ids[:, 0] % 2 * 7  # two experts hold most rows, and may be a token's twice
+    gates = torch.full((T, k), 1.0 / k)
+    ws = moe.workspace(d, "fp8_block", T)
+    moe.forward(x.cuda(), ids.cuda(), gates.cuda(), bank, d, ws=ws)
+    lay, R, kb = moe.workspace_layout(d, "fp8_block", T), T * k, -(-F // 128)
+    order = ws[lay["sorted_src"]:lay["sorted_src"] + R * 4].view(torch.int32).cpu().numpy()
+    q, s = codecs.fp8_block_quantize(x.float().numpy())
+    e, src = ids.numpy().reshape(-1)[order], col[ids.numpy().reshape(-1)[order]]
+    value = codecs.fp8_block_dequantize(q, np.ones_like(s)).astype(np.float32)  # of the codes alone
+    t = order[:, None] // k
+    # the largest of a weight block is 1.75, code 448, where the block holds any
+    scale = s[t, src // 128] * np.float32(np.float32(1.75) / np.float32(448))
+    h = scale * (value[t, src] * np.float32(448))
+    want, sw = codecs.fp8_block_quantize(codecs.bf16_rne(np.maximum(h, 0).astype(np.float64) ** 2))
+    codes = ws[lay["act_q"]:lay["act_q"] + R * F].view(R, F).cpu().numpy()
+    at = lay["act_q"] + -(-R * F // 256) * 256
+    scales = ws[at:at + kb * R * 4].view(torch.float32).view(kb, R).cpu().numpy().T
+    assert np.array_equal(scales, sw) and np.array_equal(codes, want)
 
 
 @pytest.mark.gpu
