@@ -408,12 +408,15 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  * moe_block_pack quantises and packs a weight (once), moe_block_pack_codes packs
  * the row-major codes [N, K] of a checkpoint whose block scales are used as they
  * are (packed must not be codes); moe_block_quantize quantises activations;
- * moe_block_linear is moe_block_quantize into its workspace followed by
- * moe_block_matmul.  K % 16 == 0 (MOE_EUNSUPPORTED otherwise), any N, M from 0
+ * moe_block_linear is moe_block_quantize followed by moe_block_matmul: in one
+ * kernel up to MOE_BLOCK_FEW_ROWS rows, where no workspace is used and ws may be
+ * NULL, with the codes in the workspace past that.  K % 16 == 0 (MOE_EUNSUPPORTED otherwise), any N, M from 0
  * (a no-op) to 1 << 20, N and K up to 1 << 20; x, y, w and codes 16-byte
  * aligned, scales 4-byte; ws 256-byte aligned, ws_bytes >=
- * moe_block_linear_workspace_size(M, K).  A NaN code (0x7f, 0xff) spreads to the
- * row or column of y that reads it and no further. */
+ * moe_block_linear_workspace_size(M, K).  A NaN or infinity becomes a NaN code;
+ * a NaN code (0x7f, 0xff) spreads to the row or column of y that reads it and no
+ * further. */
+#define MOE_BLOCK_FEW_ROWS 32
 int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales, void* stream);
 size_t moe_block_packed_size(int32_t N, int32_t K);
 int32_t moe_block_pack_codes(int32_t N, int32_t K, const void* codes, void* packed, void* stream);

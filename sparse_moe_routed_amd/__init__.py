@@ -192,7 +192,7 @@ def _dev(t: torch.Tensor, dtype, name: str, shape=None):
         raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -582,7 +582,7 @@ def _raw_stream(device: torch.device):
 
 def _on(device: torch.device):
     """Makes `device` current for the launches below it; free when it is."""
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _NO_SWITCH
+    return torch.cuda.device(device) if device.index != torch._C._cuda_getDevice() else _NO_SWITCH
 
 
 class _NoSwitch:
@@ -600,6 +600,10 @@ def _same_device(device: torch.device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name}: on {t.device}, x is on {device}")
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torch.Tensor] = None,
@@ -644,11 +648,10 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torc
         if not pre_norm:
             raise ValueError("out: given with pre_norm=False")
         _dev(out, torch.bfloat16, "out", (T, H))
-    p = lambda t: None if t is None else t.data_ptr()
     with _on(x.device):
         _check("moe_residual_norm", lib().moe_residual_norm(
-            T, H, x.data_ptr(), p(y), yd, p(gate), kind, p(post_weight), p(pre_weight), scale, eps,
-            int(bool(post_norm)), p(x_out), p(out), _raw_stream(x.device)))
+            T, H, x.data_ptr(), _p(y), yd, _p(gate), kind, _p(post_weight), _p(pre_weight), scale, eps,
+            int(bool(post_norm)), _p(x_out), _p(out), _raw_stream(x.device)))
     return (x if y is None else x_out), out
 
 
@@ -704,6 +707,9 @@ def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
             ctypes.byref(d), T, x.data_ptr(), ctypes.byref(r), ctypes.byref(e), ids.data_ptr(),
             gates.data_ptr(), y.data_ptr(), yd, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return y, ids, gates
+
+
+BLOCK_FEW_ROWS = 32  # MOE_BLOCK_FEW_ROWS of include/moe.h
 
 
 @dataclass
@@ -779,7 +785,9 @@ def _block_operands(rows: torch.Tensor, weight: BlockWeight, y: Optional[torch.T
         y = torch.empty((M, N), dtype=torch.bfloat16, device=rows.device)
     else:
         _dev(y, torch.bfloat16, "y", (M, N))
-    _same_device(rows.device, **{"weight.codes": weight.codes, "weight.scales": weight.scales, "y": y})
+    dev = rows.device
+    if weight.codes.device != dev or weight.scales.device != dev or y.device != dev:
+        _same_device(dev, **{"weight.codes": weight.codes, "weight.scales": weight.scales, "y": y})
     return M, N, K, y
 
 
@@ -809,13 +817,13 @@ def block_linear(x: torch.Tensor, weight: BlockWeight, y: Optional[torch.Tensor]
     """moe_block_linear: bf16 [M, N] = x [M, K] quantised by rows, times the weight."""
     _matrix(x, torch.bfloat16, "x")
     M, N, K, y = _block_operands(x, weight, y)
-    if ws is None:
-        ws = block_linear_workspace(M, K, x.device)
-    else:
+    if ws is not None:
         _dev(ws, torch.uint8, "ws")
         _same_device(x.device, ws=ws)
+    elif M > BLOCK_FEW_ROWS:
+        ws = block_linear_workspace(M, K, x.device)
     with _on(x.device):
         _check("moe_block_linear", lib().moe_block_linear(
             M, N, K, x.data_ptr(), weight.codes.data_ptr(), weight.scales.data_ptr(), y.data_ptr(),
-            ws.data_ptr(), ws.numel(), _raw_stream(x.device)))
+            _p(ws), 0 if ws is None else ws.numel(), _raw_stream(x.device)))
     return y

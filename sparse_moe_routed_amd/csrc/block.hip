@@ -50,29 +50,36 @@ __device__ __forceinline__ float amax8(u32x4 v) {
   return m;
 }
 
-// codes of four bf16 values
+// codes of v inv for four bf16 values of at most 448 / inv: nothing to clamp, and
+// NaN (and infinity, whose block has inv = 0) becomes a NaN code.  The added 0
+// makes -0 the code 0 and costs nothing in a multiply-add.
 __device__ __forceinline__ uint32_t encode4(uint32_t a, uint32_t b, float inv) {
-  return e4m3_encode4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
-                      __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv);
-}
-
-// the same of values that are 0 or more and at most 448 / inv: nothing to clamp
-__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, float inv) {
-  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(__uint_as_float(a << 16) * inv,
-                                                 __uint_as_float(a & 0xffff0000u) * inv, 0, false);
-  return __builtin_amdgcn_cvt_pk_fp8_f32(__uint_as_float(b << 16) * inv,
-                                         __uint_as_float(b & 0xffff0000u) * inv, lo, true);
+  const auto low = [&](uint32_t u) { return __builtin_fmaf(__uint_as_float(u << 16), inv, 0.f); };
+  const auto high = [&](uint32_t u) { return __builtin_fmaf(__uint_as_float(u & 0xffff0000u), inv, 0.f); };
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(low(a), high(a), 0, false);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(low(b), high(b), lo, true);
 }
 
 __device__ __forceinline__ uint2 encode8(u32x4 v, float inv) {
   return make_uint2(encode4(v[0], v[1], inv), encode4(v[2], v[3], inv));
 }
 
-// max over each row of 16 lanes, in all of them
+// max of v (0 or more, or NaN as fmaxf takes it) over each 8 lanes, in all of them
+__device__ __forceinline__ float row8_max(float v) {
+  const auto other = [&](auto how) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), decltype(how)::value,
+                                                              0xf, 0xf, true));
+  };
+  v = fmaxf(v, other(std::integral_constant<int, 0xb1>{}));   // lane ^ 1
+  v = fmaxf(v, other(std::integral_constant<int, 0x4e>{}));   // lane ^ 2
+  return fmaxf(v, other(std::integral_constant<int, 0x141>{}));  // the other 4 of 8
+}
+
+// and over each 16
 __device__ __forceinline__ float row16_max(float v) {
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  v = row8_max(v);
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x140, 0xf, 0xf,
+                                                                     true)));  // lane 15 - i
 }
 
 // ---- activations: 16 lanes take one block of 128 values, 8 values each
@@ -276,16 +283,18 @@ __device__ __forceinline__ void load_weights(u32x4 (&w)[2], Buffer b, uint32_t a
 // waves, each one block ahead of its products.  Bound by the weights' bytes and
 // the latency of a few blocks; the waves' sums are joined through LDS in wave
 // order.  The rows' codes come a line at a time (8 lanes to 128 bytes) and are
-// turned into operand order in 2 KB of LDS that belong to the wave.
+// turned into operand order in 2 KB of LDS that belong to the wave.  With QUANT
+// the rows are bf16 and become codes on their way into that LDS.
 constexpr int kSmallWaves = 8;
 constexpr int kSmallN = 32;
 
-template <int MODE, int G>
+template <int G, bool QUANT>
 __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockArgs g) {
   constexpr int kTurn = 4096, kJoin = G * 1024;
+  constexpr int kRaw = QUANT ? 2 : 1;  // 16-byte loads per 16 values
   __shared__ __attribute__((aligned(16))) uint8_t lds[kSmallWaves * (kTurn > kJoin ? kTurn : kJoin)];
   TileAt t;
-  if (!find_tile<MODE>(g, 16 * G, kSmallN, t)) return;
+  if (!find_tile<kBlockDense>(g, 16 * G, kSmallN, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
   const int K = g.K, blocks = (K + 127) / 128;
@@ -303,14 +312,14 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
   for (int j = 0; j < G; ++j) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      xp[j][h] = g.a + source_row<MODE>(g, t.row0 + min(j * 16 + h * 8 + lr, t.rows - 1)) * K + ch * 16;
-    sp[j] = source_row<MODE>(g, t.row0 + min(j * 16 + c, t.rows - 1));
+      xp[j][h] = g.a + (static_cast<size_t>(t.row0 + min(j * 16 + h * 8 + lr, t.rows - 1)) * K + ch * 16) * kRaw;
+    sp[j] = t.row0 + min(j * 16 + c, t.rows - 1);
   }
   const float* ws = g.w_s + (t.w_blk + t.n0 / 128) * blocks;
 
   struct Block {
-    u32x4 w[2][2], x[G][2];
-    float s[G];
+    u32x4 w[2][2], x[G][2][kRaw];
+    float s[G];  // QUANT: of the weights alone
   };
   const u32x4 zero = {0u, 0u, 0u, 0u};
   const auto load = [&](Block& b, int kb) {
@@ -318,17 +327,19 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
     for (int i = 0; i < 2; ++i)
       load_weights<true>(b.w[i], wb, wat[i], kb * 2048);
     const bool in = kb * 128 + ch * 16 < K;  // a last block may be short
-    const int at = in ? kb * 128 : -ch * 16;  // the row's first chunk, then made zero
+    const int at = (in ? kb * 128 : -ch * 16) * kRaw;  // the row's first chunk, then made zero
     const float sw = ws[kb];
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       if (j >= live) continue;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        b.x[j][h] = *reinterpret_cast<const u32x4*>(xp[j][h] + at);
-        if (!in) b.x[j][h] = zero;
-      }
-      b.s[j] = g.a_s[static_cast<size_t>(kb) * g.a_rows + sp[j]] * sw;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kRaw; ++i) {
+          b.x[j][h][i] = reinterpret_cast<const u32x4*>(xp[j][h] + at)[i];
+          if (!in) b.x[j][h][i] = zero;
+        }
+      b.s[j] = QUANT ? sw : g.a_s[static_cast<size_t>(kb) * g.a_rows + sp[j]] * sw;
     }
   };
 
@@ -354,13 +365,38 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       if (j >= live) continue;
-      put(j & 1, b.x[j][0], b.x[j][1]);
+      float s = b.s[j];
+      if constexpr (QUANT) {  // as block_quant_kernel: 8 lanes hold a row's block
+        u32x4 code[2];
+        float scale[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && t.rows <= j * 16 + 8) {  // rows that are not there
+            code[1] = code[0];
+            scale[1] = scale[0];
+            continue;
+          }
+          const u32x4 lo = b.x[j][h][0], hi = b.x[j][h][1];
+          const float amax = row8_max(fmaxf(amax8(lo), amax8(hi)));
+          const bool any = amax >= kTinyAmax;
+          const float inv = any ? __fdiv_rn(448.f, amax) : 0.f;
+          scale[h] = any ? __fdiv_rn(amax, 448.f) : 0.f;
+          const uint2 a = encode8(lo, inv), z = encode8(hi, inv);
+          code[h] = u32x4{a.x, a.y, z.x, z.y};
+        }
+        put(j & 1, code[0], code[1]);
+        // row c's scale lies with the lanes that hold row c
+        const float s0 = __shfl(scale[0], (c & 7) * 8), s1 = __shfl(scale[1], (c & 7) * 8);
+        s *= c < 8 ? s0 : s1;
+      } else {
+        put(j & 1, b.x[j][0][0], b.x[j][1][0]);
+      }
       const i32x8 x = get(j & 1);
       const f32x4 p0 = mma128(w0, x), p1 = mma128(w1, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[0][j][i] = __builtin_fmaf(b.s[j], p0[i], acc[0][j][i]);
-        acc[1][j][i] = __builtin_fmaf(b.s[j], p1[i], acc[1][j][i]);
+        acc[0][j][i] = __builtin_fmaf(s, p0[i], acc[0][j][i]);
+        acc[1][j][i] = __builtin_fmaf(s, p1[i], acc[1][j][i]);
       }
     }
   };
@@ -388,7 +424,7 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
       for (int w = 0; w < kSmallWaves; ++w)
         v += reinterpret_cast<const f32x4*>(lds)[(w * G + wave) * kWave + lane];
       const int r = wave * 16 + c, n = t.n0 + f * 16 + 4 * q;
-      if (r < t.rows && n < g.N) store4<MODE>(g, t.row0 + r, n, v);
+      if (r < t.rows && n < g.N) store4<kBlockDense>(g, t.row0 + r, n, v);
     }
   }
 }
@@ -663,7 +699,7 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
       for (int i = 0; i < NS; ++i)
         if (i < groups)
           *reinterpret_cast<uint32_t*>(codes + row * g.N + t.n0 + nw0 + i * 16 + 4 * q) =
-              codes4(__builtin_bit_cast(uint32_t, v[j][i][0]), __builtin_bit_cast(uint32_t, v[j][i][1]), inv);
+              encode4(__builtin_bit_cast(uint32_t, v[j][i][0]), __builtin_bit_cast(uint32_t, v[j][i][1]), inv);
       if (wn == w0 && q == 0)
         g.out_s[static_cast<size_t>((t.n0 + nw0) / 128) * g.M + row] = any ? __fdiv_rn(amax, 448.f) : 0.f;
     }
@@ -699,11 +735,12 @@ hipError_t dispatch(const void* kernel, long long blocks, int threads, const Blo
   return hipLaunchKernel(kernel, grid, block, args, 0, stream);
 }
 
-template <int MODE, int G>
-hipError_t launch_small(const BlockArgs& g, hipStream_t stream, const KernelEvents& ev = KernelEvents{}) {
-  return dispatch(reinterpret_cast<const void*>(&block_small_kernel<MODE, G>),
-                  tiles_of(g, MODE, 16 * G, kSmallN), kSmallWaves * kWave, g, stream, ev);
+template <int G, bool QUANT>
+hipError_t launch_small(const BlockArgs& g, hipStream_t stream) {
+  return dispatch(reinterpret_cast<const void*>(&block_small_kernel<G, QUANT>),
+                  tiles_of(g, kBlockDense, 16 * G, kSmallN), kSmallWaves * kWave, g, stream, KernelEvents{});
 }
+
 
 template <int MODE, int BM, int BN, int WM, int WN, int NBUF, int WBUF, bool ONCE = false>
 hipError_t launch_large(const BlockArgs& g, hipStream_t stream, const KernelEvents& ev = KernelEvents{}) {
@@ -744,15 +781,23 @@ hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_
 // (256 x 256, half the chip, 47.7).
 constexpr int kFill = 200;
 hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream) {
-  if (g.M <= 16) return launch_small<kBlockDense, 1>(g, stream);
-  if (g.M <= 32) return launch_small<kBlockDense, 2>(g, stream);
-  if (g.M <= 128) return launch_small<kBlockDense, 4>(g, stream);
+  if (g.M <= 16) return launch_small<1, false>(g, stream);
+  if (g.M <= 32) return launch_small<2, false>(g, stream);
+  if (g.M <= 128) return launch_small<4, false>(g, stream);
   const auto fills = [&](int bm, int bn) { return tiles_of(g, kBlockDense, bm, bn) >= kFill; };
   if (fills(256, 256)) return launch_large<kBlockDense, 256, 256, 2, 4, 4, 2>(g, stream);
   if (fills(128, 256)) return launch_large<kBlockDense, 128, 256, 1, 8, 4, 2>(g, stream);
   if (fills(128, 128)) return launch_large<kBlockDense, 128, 128, 2, 4, 4, 2>(g, stream);
   if (fills(64, 128)) return launch_large<kBlockDense, 64, 128, 2, 4, 4, 2>(g, stream);
   return launch_large<kBlockDense, 64, 64, 2, 4, 4, 4>(g, stream);
+}
+
+// Quantised by every workgroup that multiplies them, which for one tile of rows
+// costs less than a kernel of its own: 3712 x 2688, M = 1 5.8 us (two kernels
+// 6.9, and 3.5 us more on the host), M = 16 7.3 (7.6), M = 24 9.5 (9.3); with more
+// rows it loses: M = 77 18.9 us (11.3).
+hipError_t launch_block_few_linear(const BlockArgs& g, hipStream_t stream) {
+  return g.M <= 16 ? launch_small<1, true>(g, stream) : launch_small<2, true>(g, stream);
 }
 
 hipError_t launch_block_quant(const uint16_t* x, int rows, int cols, uint8_t* codes, float* scales,

@@ -994,6 +994,18 @@ int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const v
   if (!x || !w_codes || !w_scales || !y) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(y, 16))
     return MOE_EINVAL;
+  static_assert(moe::kBlockFewRows == MOE_BLOCK_FEW_ROWS, "the header's limit");
+  if (M <= moe::kBlockFewRows) {
+    moe::BlockArgs g{};
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.a = static_cast<const uint8_t*>(x);
+    g.w = static_cast<const uint8_t*>(w_codes);
+    g.w_s = w_scales;
+    g.out = y;
+    return hip_status(moe::launch_block_few_linear(g, static_cast<hipStream_t>(stream)));
+  }
   const BlockLinearLayout L = block_linear_layout(M, K);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
   uint8_t* codes = at<uint8_t>(ws, 0);

@@ -199,7 +199,7 @@ constexpr uint32_t kBlockMaxBytes = 0xf0000000u;  // gathered activation codes s
 constexpr int kBlockDecodeMaxT = 256;  // grouped batches below this: 32-row tiles
 struct BlockArgs {
   int M, N, K;
-  const uint8_t* a;   // codes [rows, K]
+  const uint8_t* a;   // codes [rows, K]; launch_block_few_linear: bf16 [M, K]
   const float* a_s;   // [ceil(K / 128), a_rows]
   int a_rows;
   const uint8_t* w;   // codes of E matrices [N, K], packed (block.hip)
@@ -221,6 +221,9 @@ int block_tile_rows(int T);
 hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_t stream,
                                 const KernelEvents& ev = KernelEvents{});
 hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream);
+// at most kBlockFewRows rows, quantised by the product's own kernel
+constexpr int kBlockFewRows = 32;
+hipError_t launch_block_few_linear(const BlockArgs& g, hipStream_t stream);
 // codes [rows, cols] and scales [ceil(cols / 128), rows] of bf16 rows
 hipError_t launch_block_quant(const uint16_t* x, int rows, int cols, uint8_t* codes, float* scales,
                               hipStream_t stream);

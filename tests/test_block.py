@@ -74,11 +74,11 @@ def test_validation():
     assert mm(K=40) == moe.EUNSUPPORTED and mm(N=(1 << 20) + 1) == moe.EUNSUPPORTED
     assert mm(M=0, c=None, s=None, y=None) == moe.OK
 
-    need = L.moe_block_linear_workspace_size(4, 64)
-    assert need >= 4 * 64 + 16 and need % 256 == 0
+    need = L.moe_block_linear_workspace_size(40, 64)
+    assert need >= 40 * 64 + 160 and need % 256 == 0
     assert L.moe_block_linear_workspace_size(-1, 64) == 0 and L.moe_block_linear_workspace_size(4, 20) == 0
 
-    def lin(M=4, N=64, K=64, x=FAKE, wc=FAKE, s=FAKE, y=FAKE, ws=FAKE, nb=need):
+    def lin(M=40, N=64, K=64, x=FAKE, wc=FAKE, s=FAKE, y=FAKE, ws=FAKE, nb=need):
         return L.moe_block_linear(M, N, K, x, wc, s, y, ws, nb, None)
 
     for bad in (dict(x=None), dict(wc=None), dict(s=None), dict(y=None), dict(x=FAKE + 8), dict(y=FAKE + 4)):
@@ -230,6 +230,11 @@ def test_rows_are_apart():
         got = moe.block_linear(x2.cuda(), W)
         keep = [i for i in range(M) if i not in (3, 4)]
         assert torch.equal(got[keep], want[keep])
+        assert got[3].isnan().all() and got[4].isnan().all()
+        w2 = w.clone()
+        w2[5, 7] = float("nan")
+        got = moe.block_linear(x.cuda(), moe.block_pack(w2.cuda()))
+        assert got[:, 5].isnan().all() and not got[:, 6:].isnan().any() and torch.equal(got[:, 128:], want[:, 128:])
         q, s = moe.block_quantize(x.cuda())
         q[3] = 0x7F
         got = moe.block_matmul(q, s, W)
@@ -263,7 +268,7 @@ def test_refusals_of_the_binding():
         moe.block_quantize(torch.zeros((4, 24), dtype=torch.bfloat16, device="cuda"))
     assert e.value.status == moe.EUNSUPPORTED
     with pytest.raises(moe.MoeError) as e:
-        moe.block_linear(x, W, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        moe.block_linear(x.repeat(10, 1), W, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == moe.EWORKSPACE
     assert moe.block_linear(x[:0], W).shape == (0, 32)
 
