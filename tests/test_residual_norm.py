@@ -82,6 +82,14 @@ def _case(T, H, ydt, kind, seed):
     (3, 4 * 6 * 512 + 5, torch.bfloat16, "element", True, True),  # first of sixteen
     (2, 49152, torch.float32, "channel", True, True),         # widest
     (4096, 192, torch.float32, "token", True, True),
+    (1999, 512, torch.bfloat16, "element", True, True),       # the widths and row counts at
+    (1536, 513, torch.float32, "none", True, True),           # which a row's waves change
+    (1537, 2690, torch.bfloat16, "element", True, True),
+    (1537, 6 * 512 + 3, torch.float32, "channel", True, True),
+    (5, 8192, torch.bfloat16, "token", True, True),
+    (1600, 8191, torch.float32, "channel", False, True),
+    (3, 8193, torch.float32, "element", True, True),
+    (2, 16385, torch.bfloat16, "channel", True, False),
 ])
 def test_matches_oracle(T, H, ydt, kind, post, weights):
     x, y, gate, pw, rw = _case(T, H, ydt, kind, 7 * T + H)
