@@ -750,24 +750,28 @@ hipError_t launch_large(const BlockArgs& g, hipStream_t stream, const KernelEven
 
 }  // namespace
 
-// Rows per tile of the experts' products.  Short of 256 tokens an expert has a
-// few rows, and the tile of 32 reads each weight once or twice; 128-row tiles are
-// for the longer ones (T = 255: 261 us with 32 rows, T = 256: 275 us with 128 and
-// 297 us with 32).
-int block_tile_rows(int T) { return T < kBlockDecodeMaxT ? 32 : 128; }
+// Rows per tile of the experts' products.  Experts of a few rows take tiles of 32,
+// which read each weight once or twice; from 16 rows per expert on, tiles of 128
+// (full layer, T = 256, 12 rows per expert: 243 us with 32 rows, 275 with 128;
+// T = 384: 287 and 285; T = 768: 364 and 319).  So do short batches of few
+// experts, whose 128-row tiles are too few for the chip.
+int block_tile_rows(int R, int E) { return R < (16 * E > 256 ? 16 * E : 256) ? 32 : 128; }
 
 // Full layer (128 experts, 2688 -> 1856 -> 2688), whole forward, graph replay:
-// decode tiles 32 x 64 at T = 5 52.5 us, T = 64 162 us (32 x 128: 54 and 164),
-// weights 3 steps ahead, since each is read once and from memory; prefill tiles
-// 128 x 256 with one wave per 32 columns at T = 4096 608-634 us (2 x 4 waves
-// 676, 128 x 128 643, 64 x 256 712, 256 x 128 724, 256 x 256 670).
-hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_t stream,
-                                const KernelEvents& ev) {
-  if (T < kBlockDecodeMaxT)
+// decode tiles 32 x 64 (32 x 128 where the tile makes the codes) with the weights
+// 3 steps ahead, since each is read once and from memory: T = 5 52-58 us, T = 64
+// 158.  Prefill tiles 128 x 128 in 4 waves, two workgroups or more to a CU:
+// T = 4096 573 us, T = 1024 335 (128 x 256 in 8 waves 581 and 345, 128 x 128 in 8
+// waves 607 and 344, 64 x 128 620 and 338, 256 x 256 631 and 378; column tiles
+// dealt round the XCDs 605 and 340).  There matrix unit, LDS and vector unit are
+// each busy a quarter to a third of the time and HBM runs at 3.4 TB/s: the steps'
+// latencies are what is left.
+hipError_t launch_block_experts(int stage, const BlockArgs& g, hipStream_t stream, const KernelEvents& ev) {
+  if (block_tile_rows(g.M, g.E) == 32)
     return stage == 0 ? launch_large<kBlockUp, 32, 128, 1, 4, 4, 4, true>(g, stream, ev)
                       : launch_large<kBlockDown, 32, 64, 1, 4, 4, 4, true>(g, stream, ev);
-  return stage == 0 ? launch_large<kBlockUp, 128, 256, 1, 8, 4, 2>(g, stream, ev)
-                    : launch_large<kBlockDown, 128, 256, 1, 8, 4, 2>(g, stream, ev);
+  return stage == 0 ? launch_large<kBlockUp, 128, 128, 1, 4, 2, 2>(g, stream, ev)
+                    : launch_large<kBlockDown, 128, 128, 1, 4, 2, 2>(g, stream, ev);
 }
 
 // One matrix.  Few rows (up to 128) split K over the waves of a workgroup, since

@@ -428,7 +428,7 @@ hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const mo
   g.sorted_src = p.sorted_src;
   g.top_k = dims->top_k;
   g.w_slot = w_slot;
-  err = moe::launch_block_experts(0, T, g, st, marks.gemm(0));
+  err = moe::launch_block_experts(0, g, st, marks.gemm(0));
   if (err != hipSuccess) return err;
   marks.mark(3);  // the up projection's tiles have written the codes already
   marks.mark(4);
@@ -443,7 +443,7 @@ hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const mo
   g.tile_off = p.tile_off1;
   g.max_tiles = (R + p.bm1 - 1) / p.bm1 + (R < E ? R : E);
   g.row_gate = p.row_gate;
-  return moe::launch_block_experts(1, T, g, st, marks.gemm(1));
+  return moe::launch_block_experts(1, g, st, marks.gemm(1));
 }
 
 // The forward pass.  With `cc` set, the expert weights come from the cache:
@@ -517,7 +517,7 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   p.sorted_src = at<int32_t>(ws, L.sorted_src);
   p.inv = at<int32_t>(ws, L.inv);
   p.row_gate = at<float>(ws, L.row_gate);
-  p.bm0 = fmt == kFP8Block ? moe::block_tile_rows(T) : moe::gemm_shape(fmt, 0, T).bm;
+  p.bm0 = fmt == kFP8Block ? moe::block_tile_rows(R, E) : moe::gemm_shape(fmt, 0, T).bm;
   p.tile_off0 = at<int32_t>(ws, L.tile_off0);
   p.bm1 = fmt == kFP8Block ? p.bm0 : moe::gemm_shape(fmt, 1, T).bm;
   p.tile_off1 = at<int32_t>(ws, L.tile_off1);

@@ -196,7 +196,6 @@ hipError_t launch_few(int fmt, const FewArgs& g, hipStream_t stream);
 // E4M3 with a scale per block of 128 (moe_block_*, "fp8_block" banks)
 enum BlockMode { kBlockDense = 0, kBlockUp = 1, kBlockDown = 2 };
 constexpr uint32_t kBlockMaxBytes = 0xf0000000u;  // gathered activation codes stay below
-constexpr int kBlockDecodeMaxT = 256;  // grouped batches below this: 32-row tiles
 struct BlockArgs {
   int M, N, K;
   const uint8_t* a;   // codes [rows, K]; launch_block_few_linear: bf16 [M, K]
@@ -216,9 +215,9 @@ struct BlockArgs {
   const int32_t* w_slot;
   const float* row_gate;
 };
-// rows per tile of the grouped products for T tokens
-int block_tile_rows(int T);
-hipError_t launch_block_experts(int stage, int T, const BlockArgs& g, hipStream_t stream,
+// rows per tile of the grouped products of R rows over E experts
+int block_tile_rows(int R, int E);
+hipError_t launch_block_experts(int stage, const BlockArgs& g, hipStream_t stream,
                                 const KernelEvents& ev = KernelEvents{});
 hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream);
 // at most kBlockFewRows rows, quantised by the product's own kernel
