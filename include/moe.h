@@ -410,10 +410,10 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  * are (packed must not be codes); moe_block_quantize quantises activations;
  * moe_block_linear is moe_block_quantize followed by moe_block_matmul: in one
  * kernel up to MOE_BLOCK_FEW_ROWS rows, where no workspace is used and ws may be
- * NULL, with the codes in the workspace past that.  K % 16 == 0 (MOE_EUNSUPPORTED otherwise), any N, M from 0
- * (a no-op) to 1 << 20, N and K up to 1 << 20; x, y, w and codes 16-byte
- * aligned, scales 4-byte; ws 256-byte aligned, ws_bytes >=
- * moe_block_linear_workspace_size(M, K).  A NaN or infinity becomes a NaN code;
+ * NULL, with the codes in the workspace past that.  K % 16 == 0
+ * (MOE_EUNSUPPORTED otherwise), any N, M from 0 (a no-op) to 1 << 20, N and K up
+ * to 1 << 20; x, y, w and codes 16-byte aligned, scales 4-byte; ws 256-byte
+ * aligned, ws_bytes >= moe_block_linear_workspace_size(M, K).  A NaN or infinity becomes a NaN code;
  * a NaN code (0x7f, 0xff) spreads to the row or column of y that reads it and no
  * further. */
 #define MOE_BLOCK_FEW_ROWS 32
@@ -430,19 +430,20 @@ int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const v
 
 /* The whole layer for a few tokens: moe_route and moe_forward of at most
  * MOE_FEW_TOKENS tokens in two kernels (decode, where the six to nine launches
- * of the two calls cost more than the weights of one token).  Formulas, routing
- * order and quantisation are those of the two calls; sums run in another fixed
- * order (a token's experts by index instead of by slot), so y agrees with
- * moe_forward's to fp32 summation order and repeats bit for bit.
+ * of the two calls cost more than the weights of one token), or as the two calls
+ * where those are faster or the two kernels do not apply: FP8_BLOCK banks; more
+ * than 100000 (BF16) or 50000 (NVFP4) values in the T*k rows of the
+ * intermediate; T rows of H or F + 8 bf16 values, H and F rounded up to 128,
+ * beyond 120 KiB; expert matrices of 2^30 values and more.  Formulas, routing
+ * order and quantisation are those of the two calls; the two kernels sum in
+ * another fixed order (a token's experts by index instead of by slot), so y
+ * agrees with moe_forward's to fp32 summation order and repeats bit for bit.
  *   x [dev] bf16 [T, H]; router, experts as moe_route and moe_forward
  *   ids [dev] int32 [T, k], gates [dev] fp32 [T, k], y [dev] [T, H]: written
  *   ws [dev] workspace of ws_bytes >= moe_layer_few_workspace_size(dims, fmt, T),
  *      256-byte aligned; its contents need no initialisation
- * MOE_EUNSUPPORTED for T > MOE_FEW_TOKENS, and where T rows of H or F + 8
- * bf16 values, H and F rounded up to 128, exceed 120 KiB of the GPU's shared
- * memory (H up to 3840 and F up to 3712 at 16
- * tokens), or an expert matrix exceeds 2^30 values.  Errors otherwise as
- * moe_route and moe_forward.  Capturable in a HIP graph. */
+ * MOE_EUNSUPPORTED for T > MOE_FEW_TOKENS.  Errors otherwise as moe_route and
+ * moe_forward.  Capturable in a HIP graph. */
 #define MOE_FEW_TOKENS 16
 size_t moe_layer_few_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens);
 int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_router* router,

@@ -672,8 +672,8 @@ def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
               dims: LayerDims = LayerDims(), y_dtype: torch.dtype = torch.float32,
               ids: Optional[torch.Tensor] = None, gates: Optional[torch.Tensor] = None,
               ws: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
-    """moe_layer_few: route and forward of at most FEW_TOKENS tokens in two
-    kernels; (y [T, H], ids int32 [T, k], gates fp32 [T, k])."""
+    """moe_layer_few: route and forward of at most FEW_TOKENS tokens, in two
+    kernels where that is faster; (y [T, H], ids int32 [T, k], gates fp32 [T, k])."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a [T, H] tensor")
     T, dev = x.shape[0], x.device

@@ -76,7 +76,9 @@ __device__ __forceinline__ float amax8(u32x4 v) {
 // the neighbouring lane, which must be active).  The values are those of the
 // encoders of moe_common.h; a code's sign may be that of -0, whose products
 // add nothing.
-template <int FMT>
+// POSITIVE: values of 0 or more, so that v * ts.a is at most 448 and nothing is
+// left to clamp (FP8).
+template <int FMT, bool POSITIVE = false>
 __device__ __forceinline__ u32x4 quantise8(u32x4 v, const TensorScale<FMT>& ts) {
   if constexpr (FMT == kBF16) {
     return v;
@@ -87,7 +89,15 @@ __device__ __forceinline__ u32x4 quantise8(u32x4 v, const TensorScale<FMT>& ts) 
       f[2 * w] = __uint_as_float(v[w] << 16);
       f[2 * w + 1] = __uint_as_float(v[w] & 0xffff0000u);
     }
-    if constexpr (FMT == kFP8) {
+    if constexpr (FMT == kFP8 && POSITIVE) {
+      uint32_t c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * ts.a, f[4 * h + 1] * ts.a, 0, false);
+        c[h] = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * ts.a, f[4 * h + 3] * ts.a, lo, true);
+      }
+      return __builtin_bit_cast(u32x4, fp8_frag(c[0], c[1]));
+    } else if constexpr (FMT == kFP8) {
       const uint32_t c0 = e4m3_encode4(f[0] * ts.a, f[1] * ts.a, f[2] * ts.a, f[3] * ts.a);
       const uint32_t c1 = e4m3_encode4(f[4] * ts.a, f[5] * ts.a, f[6] * ts.a, f[7] * ts.a);
       return __builtin_bit_cast(u32x4, fp8_frag(c0, c1));
@@ -746,7 +756,7 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
             return g.act + (static_cast<size_t>(s >> 3) * g.k + (s & 7)) * F;
           },
           [&](int r, int ch) { return stage + r * stride + ch * 16; },
-          [&](u32x4 v) { return quantise8<FMT>(v, ts); });
+          [&](u32x4 v) { return quantise8<FMT, true>(v, ts); });
       if (cF > F8)
         for (int i = tid; i < rows * (cF - F8); i += kThreads)
           *reinterpret_cast<u32x4*>(stage + i / (cF - F8) * stride + (F8 + i % (cF - F8)) * 16) =
@@ -832,8 +842,16 @@ hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// the operands fit LDS and one expert's matrix is addressed by 32 bits
-bool few_fits(int T, int H, int F) {
+// The operands fit LDS, one expert's matrix is addressed by 32 bits, and the two
+// kernels are not slower than moe_route and moe_forward.  What they save is
+// launches, about 20 us; what they cost grows with the rows of a that every
+// workgroup stages, and for NVFP4 quantises, T k F values.  Full layer (k F =
+// 11136), these against the two calls: BF16 T = 1 37 us (55), 8 120 (119),
+// 16 192 (183); NVFP4 T = 1 30 (42), 4 48 (50), 8 68 (61), 16 105 (81); FP8
+// T = 1 29 (48), 8 78 (89), 16 116 (122).
+bool few_pays(int fmt, int T, int H, int F, int k) {
+  const size_t staged = static_cast<size_t>(T) * k * F;
+  if (fmt == kFP8Block || (fmt == kBF16 && staged > 100000) || (fmt == kNVFP4 && staged > 50000)) return false;
   return stage_need(T, H, F) <= kMaxStage &&
          static_cast<size_t>(H) * F * 2 < (static_cast<size_t>(1) << 31);
 }

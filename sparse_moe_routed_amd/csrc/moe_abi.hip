@@ -874,10 +874,11 @@ int32_t moe_residual_norm(int32_t T, int32_t H, const void* x, const void* y, in
 }
 
 size_t moe_layer_few_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens) {
-  if (!dims_ok(dims) || !fmt_ok(fmt) || fmt == kFP8Block || max_tokens < 0 ||
-      max_tokens > moe::kFewTokens)
-    return 0;
-  return few_layout(dims, max_tokens).total;
+  if (!dims_ok(dims) || !fmt_ok(fmt) || max_tokens < 0 || max_tokens > moe::kFewTokens) return 0;
+  // if the most tokens take the two kernels, fewer do so too
+  const size_t two = few_layout(dims, max_tokens).total;
+  if (moe::few_pays(fmt, max_tokens, dims->hidden, dims->ffn, dims->top_k)) return two;
+  return std::max(two, moe_route_workspace_size(dims, max_tokens) + make_layout(dims, fmt, max_tokens).total);
 }
 
 int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_router* router,
@@ -887,8 +888,7 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   if (!experts || T < 0 || T > kMaxTokens) return MOE_EINVAL;
   if (!fmt_ok(experts->fmt)) return MOE_EINVAL;
   if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
-  if (T > moe::kFewTokens || experts->fmt == kFP8Block) return MOE_EUNSUPPORTED;
-  if (!moe::few_fits(T, dims->hidden, dims->ffn)) return MOE_EUNSUPPORTED;
+  if (T > moe::kFewTokens) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;  // nothing is read or written; pointers may be null
   if (!router || !router->w_packed || !x || !ids || !gates || !y) return MOE_EINVAL;
   if (!experts->up || !experts->down) return MOE_EINVAL;
@@ -897,8 +897,15 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   if (!aligned(x, 16) || !aligned(router->w_packed, 16) || !aligned(router->bias, 4) ||
       !aligned(ids, 4) || !aligned(gates, 4) || !aligned(y, 16) || !bank_aligned(experts))
     return MOE_EINVAL;
+  if (!ws || ws_bytes < moe_layer_few_workspace_size(dims, experts->fmt, T) || !aligned(ws, kAlign))
+    return MOE_EWORKSPACE;
+  if (!moe::few_pays(experts->fmt, T, dims->hidden, dims->ffn, dims->top_k)) {
+    const size_t rb = moe_route_workspace_size(dims, T);
+    const int32_t rs = moe_route(dims, T, x, router, ids, gates, ws, rb, stream);
+    if (rs != MOE_OK) return rs;
+    return moe_forward(dims, T, x, ids, gates, experts, y, y_dtype, at<uint8_t>(ws, rb), ws_bytes - rb, stream);
+  }
   const FewLayout L = few_layout(dims, T);
-  if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
   moe::FewArgs g{};
   g.T = T;
   g.H = dims->hidden;

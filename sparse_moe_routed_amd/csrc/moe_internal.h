@@ -190,7 +190,7 @@ struct FewArgs {
   int y_bf16;
   int stage_rows;  // rows of a that the LDS stage holds (set by the launch)
 };
-bool few_fits(int T, int H, int F);
+bool few_pays(int fmt, int T, int H, int F, int k);
 hipError_t launch_few(int fmt, const FewArgs& g, hipStream_t stream);
 
 // E4M3 with a scale per block of 128 (moe_block_*, "fp8_block" banks)

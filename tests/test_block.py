@@ -481,9 +481,9 @@ def test_other_calls_with_the_bank():
     g2[:, 1] = 0
     assert (y - moe.forward(x, ids, g2, L.bank, L.ld)).abs().max() <= 1e-5 * want.abs().max()
     assert moe.forward(x[:0], ids[:0], gates[:0], L.bank, L.ld).shape == (0, 256)
-    # no single-kernel layer for this format
-    with pytest.raises(ValueError):
-        moe.layer_few_workspace(L.ld, "fp8_block")
+    # a few tokens: as route and forward
+    y, i2, g2 = moe.layer_few(x, L.router, L.bank, L.ld)
+    assert torch.equal(y, want) and torch.equal(i2, ids) and torch.equal(g2, gates)
 
 
 def _shared(T):

@@ -67,9 +67,15 @@ def test_validation():
                 dict(router=moe.Router(FAKE + 2, None)), dict(router=moe.Router(FAKE, FAKE + 2)),
                 dict(e=moe.Experts(0, FAKE + 8, FAKE, None, None, None, None))):
         assert call(**bad) == moe.EINVAL, bad
-    for bad in (dict(T=17), dict(dims=moe.Dims(2688, 1856, 128, 9)), dict(dims=moe.Dims(2690, 1856, 128, 6)),
-                dict(T=16, dims=moe.Dims(3904, 1856, 128, 6)), dict(T=16, dims=moe.Dims(64, 3776, 128, 6))):
+    for bad in (dict(T=17), dict(dims=moe.Dims(2688, 1856, 128, 9)), dict(dims=moe.Dims(2690, 1856, 128, 6))):
         assert call(**bad) == moe.EUNSUPPORTED, bad
+    # as two calls: the workspaces of both
+    for fmt, T, dims in ((3, 4, d), (0, 16, d), (2, 8, d), (1, 16, moe.Dims(64, 3776, 16, 1))):
+        n = moe.lib().moe_layer_few_workspace_size(ctypes.byref(dims), fmt, T)
+        assert n >= (moe.lib().moe_route_workspace_size(ctypes.byref(dims), T) +
+                     moe.lib().moe_workspace_size(ctypes.byref(dims), fmt, T))
+        e = moe.Experts(fmt, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE)
+        assert call(dims=dims, T=T, e=e, wsb=n - 1) == moe.EWORKSPACE
     for bad in (dict(ws=None), dict(wsb=need - 1), dict(ws=FAKE + 16)):
         assert call(**bad) == moe.EWORKSPACE, bad
     assert call(T=0, x=None, router=None, ids=None, gates=None, y=None, ws=None, wsb=0) == moe.OK
