@@ -191,8 +191,8 @@ int32_t moe_forward(const moe_dims* dims, int32_t T, const void* x,
  * events[i] is recorded on `stream` before stage i and events[6] after the
  * last one.  Stages: 0 permutation (histogram, prefix sum, scatter), 1 token
  * quantisation (FP8/NVFP4), 2 up projection + ReLU^2, 3 intermediate
- * quantisation (FP8/NVFP4; FP8_BLOCK makes the codes in stage 2),
- * 4 down projection, 5 combine.
+ * quantisation (FP8/NVFP4), 4 down projection, 5 combine; FP8_BLOCK quantises
+ * the tokens in stage 0 and the intermediate in stage 2.
  * With n_events >= 11, events[7], events[8] take the start and end of the up
  * projection kernel itself and events[9], events[10] those of the down
  * projection kernel (stamped from the kernels' dispatch packets through

@@ -398,17 +398,14 @@ struct StageMarks {
 };
 
 // stages 1 to 4 of the forward pass with an "fp8_block" bank: both
-// quantisations take the scale of each block of 128 values of a row, so no
-// stage waits for a maximum over a whole tensor
-hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const moe_experts* ex,
+// quantisations take the scale of each block of 128 values of a row, so none
+// waits for a maximum over a whole tensor, or is a stage of its own
+hipError_t block_stages(const moe_dims* dims, int32_t T, const moe_experts* ex,
                         const moe::PermBufs& p, const int32_t* w_slot, const Layout& L, void* ws,
                         const StageMarks& marks) {
   const int H = dims->hidden, F = dims->ffn, E = dims->n_experts, R = T * dims->top_k;
   const hipStream_t st = marks.st;
-  marks.mark(1);
-  hipError_t err = moe::launch_block_quant(static_cast<const uint16_t*>(x), T, H,
-                                           at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s), st);
-  if (err != hipSuccess) return err;
+  marks.mark(1);  // the permutation has quantised the tokens beside its own work
   marks.mark(2);
   moe::BlockArgs g{};
   g.M = R;
@@ -428,7 +425,7 @@ hipError_t block_stages(const moe_dims* dims, int32_t T, const void* x, const mo
   g.sorted_src = p.sorted_src;
   g.top_k = dims->top_k;
   g.w_slot = w_slot;
-  err = moe::launch_block_experts(0, g, st, marks.gemm(0));
+  const hipError_t err = moe::launch_block_experts(0, g, st, marks.gemm(0));
   if (err != hipSuccess) return err;
   marks.mark(3);  // the up projection's tiles have written the codes already
   marks.mark(4);
@@ -523,6 +520,8 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   p.tile_off1 = at<int32_t>(ws, L.tile_off1);
   p.zero_words = amax_x;  // amax slots of x and of the intermediate
   p.n_zero = 2 * moe::kAmaxSlots;
+  if (fmt == kFP8Block)
+    p.quant = {static_cast<const uint16_t*>(x), T, H, at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s)};
   marks.mark(0);
   hipError_t err = shared ? moe::launch_permute_identity(R, p, st)
                           : moe::launch_permute(ids, gates, T, E, k, p, st);
@@ -603,7 +602,7 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   }
 
   if (fmt == kFP8Block) {
-    const hipError_t be = block_stages(dims, T, x, ex, p, w_slot, L, ws, marks);
+    const hipError_t be = block_stages(dims, T, ex, p, w_slot, L, ws, marks);
     if (be != hipSuccess) return MOE_EHIP;
     marks.mark(5);
     const int mode = accumulate ? moe::kYF32Add : (y_dtype == MOE_Y_F32 ? moe::kYF32 : moe::kYBF16);
@@ -789,8 +788,8 @@ int32_t moe_quantize_activation(int32_t fmt, int32_t rows, int32_t cols, const v
   if (rows == 0) return MOE_OK;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (fmt == kFP8Block)
-    return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), rows, cols,
-                                              static_cast<uint8_t*>(codes), scale, st));
+    return hip_status(moe::launch_block_quant({static_cast<const uint16_t*>(x), rows, cols,
+                                               static_cast<uint8_t*>(codes), scale}, st));
   uint32_t* amax = static_cast<uint32_t*>(ws);  // kAmaxSlots words
   hipError_t err = moe::launch_zero_u32(amax, moe::kAmaxSlots, st);
   if (err == hipSuccess)
@@ -963,8 +962,8 @@ int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, flo
   if (M == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
-  return hip_status(moe::launch_block_quant(static_cast<const uint16_t*>(x), M, K,
-                                            static_cast<uint8_t*>(codes), scales,
+  return hip_status(moe::launch_block_quant({static_cast<const uint16_t*>(x), M, K,
+                                             static_cast<uint8_t*>(codes), scales},
                                             static_cast<hipStream_t>(stream)));
 }
 

@@ -33,6 +33,14 @@ __host__ __device__ __forceinline__ int nv_panel_rows(int N, int p) {
   return left < kNvPanel ? left : kNvPanel;
 }
 
+// codes [rows, cols] and scales [ceil(cols / 128), rows] of bf16 rows
+struct BlockQuantArgs {
+  const uint16_t* x;
+  int rows, cols;
+  uint8_t* codes;
+  float* scales;
+};
+
 struct PermBufs {
   int32_t* chunk_counts;  // [n_chunks, E]
   int32_t* chunk_base;    // [n_chunks, E]
@@ -47,6 +55,8 @@ struct PermBufs {
   int32_t* tile_off1;     // [E + 1]
   uint32_t* zero_words;   // cleared by the scan (amax slots)
   int n_zero;
+  // tokens that further workgroups of the first kernel quantise (rows 0: none)
+  BlockQuantArgs quant;
 };
 
 // K slices of the router GEMV for T tokens (partial logits [S, T, E] fp32)
@@ -223,9 +233,7 @@ hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream);
 // at most kBlockFewRows rows, quantised by the product's own kernel
 constexpr int kBlockFewRows = 32;
 hipError_t launch_block_few_linear(const BlockArgs& g, hipStream_t stream);
-// codes [rows, cols] and scales [ceil(cols / 128), rows] of bf16 rows
-hipError_t launch_block_quant(const uint16_t* x, int rows, int cols, uint8_t* codes, float* scales,
-                              hipStream_t stream);
+hipError_t launch_block_quant(const BlockQuantArgs& q, hipStream_t stream);
 hipError_t launch_block_pack_codes(const uint8_t* q, int N, int K, uint8_t* codes, hipStream_t stream);
 hipError_t launch_block_pack(const uint16_t* w, int E, int N, int K, uint8_t* codes, float* scales,
                              hipStream_t stream);

@@ -14,6 +14,11 @@
 // perm_scatter recomputes each entry's stable rank inside its chunk with wave
 // ballots.  When all ids fit one chunk (decode batches) perm_single does the
 // three steps in one workgroup.  No host sync.
+//
+// For an "fp8_block" bank the tokens' codes are made beside it: the first kernel
+// gets workgroups of its own for them, which saves a launch (full layer, T = 1
+// 28.0 -> 26.0 us, T = 64 157.8 -> 156.3).
+#include "block_quant.h"
 #include "moe_common.h"
 #include "moe_internal.h"
 
@@ -23,6 +28,7 @@ namespace {
 
 constexpr int kPermThreads = 256;
 constexpr int kRounds = kChunk / kPermThreads;  // entries per thread per chunk
+static_assert(kPermThreads == kQThreads, "workgroups of both kinds");
 
 // this thread's entries of one chunk (round r holds flat index chunk * kChunk
 // + r * kPermThreads + threadIdx.x), all loads issued together: the expert id
@@ -46,8 +52,11 @@ __device__ __forceinline__ void count_chunk(const int (&ev)[kRounds], int32_t* c
 }
 
 __global__ __launch_bounds__(kPermThreads) void perm_count_kernel(
-    const int32_t* __restrict__ ids, int R, int E, int32_t* __restrict__ chunk_counts) {
+    const int32_t* __restrict__ ids, int R, int E, int32_t* __restrict__ chunk_counts, int n_chunks,
+    BlockQuantArgs quant) {
   __shared__ int32_t cnt[256];
+  if (static_cast<int>(blockIdx.x) >= n_chunks)
+    return block_quantise(quant, blockIdx.x - n_chunks, gridDim.x - n_chunks);
   int ev[kRounds];
   load_chunk(ids, R, E, blockIdx.x, ev);
   for (int e = threadIdx.x; e < E; e += kPermThreads) cnt[e] = 0;
@@ -201,7 +210,8 @@ __global__ __launch_bounds__(kPermThreads) void perm_single_kernel(
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int bm0,
     int32_t* __restrict__ tile_off0, int bm1, int32_t* __restrict__ tile_off1,
     uint32_t* __restrict__ zero_words, int n_zero, int32_t* __restrict__ sorted_src,
-    int32_t* __restrict__ inv, float* __restrict__ row_gate) {
+    int32_t* __restrict__ inv, float* __restrict__ row_gate, BlockQuantArgs quant) {
+  if (blockIdx.x > 0) return block_quantise(quant, blockIdx.x - 1, gridDim.x - 1);
   __shared__ int32_t cnt[256];
   __shared__ int32_t wcnt[kPermThreads / 64][256];
   __shared__ int tmp[kPermThreads / 64];
@@ -230,8 +240,10 @@ __global__ __launch_bounds__(kPermThreads) void perm_identity_kernel(
     int R, int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int bm0,
     int32_t* __restrict__ tile_off0, int bm1, int32_t* __restrict__ tile_off1,
     uint32_t* __restrict__ zero_words, int n_zero, int32_t* __restrict__ sorted_src,
-    int32_t* __restrict__ inv, float* __restrict__ row_gate) {
-  for (int i = blockIdx.x * kPermThreads + threadIdx.x; i < R; i += gridDim.x * kPermThreads) {
+    int32_t* __restrict__ inv, float* __restrict__ row_gate, int groups, BlockQuantArgs quant) {
+  if (static_cast<int>(blockIdx.x) >= groups)
+    return block_quantise(quant, blockIdx.x - groups, gridDim.x - groups);
+  for (int i = blockIdx.x * kPermThreads + threadIdx.x; i < R; i += groups * kPermThreads) {
     sorted_src[i] = i;
     inv[i] = i;
     row_gate[i] = 1.0f;
@@ -255,9 +267,9 @@ __global__ __launch_bounds__(kPermThreads) void perm_identity_kernel(
 hipError_t launch_permute_identity(int R, const PermBufs& p, hipStream_t stream) {
   int g = (R + kPermThreads - 1) / kPermThreads;
   g = g < 1 ? 1 : (g > 1024 ? 1024 : g);
-  hipLaunchKernelGGL(perm_identity_kernel, dim3(g), dim3(kPermThreads), 0, stream, R, p.counts,
-                     p.offsets, p.bm0, p.tile_off0, p.bm1, p.tile_off1, p.zero_words, p.n_zero,
-                     p.sorted_src, p.inv, p.row_gate);
+  hipLaunchKernelGGL(perm_identity_kernel, dim3(g + block_quant_groups(p.quant)), dim3(kPermThreads), 0,
+                     stream, R, p.counts, p.offsets, p.bm0, p.tile_off0, p.bm1, p.tile_off1,
+                     p.zero_words, p.n_zero, p.sorted_src, p.inv, p.row_gate, g, p.quant);
   return hipGetLastError();
 }
 
@@ -265,14 +277,15 @@ hipError_t launch_permute(const int32_t* ids, const float* gates, int T, int E, 
                           const PermBufs& p, hipStream_t stream) {
   const int R = T * k;
   const int n_chunks = (R + kChunk - 1) / kChunk;
+  const int quant = block_quant_groups(p.quant);
   if (n_chunks <= 1) {
-    hipLaunchKernelGGL(perm_single_kernel, dim3(1), dim3(kPermThreads), 0, stream, ids, gates, R,
-                       E, p.counts, p.offsets, p.bm0, p.tile_off0, p.bm1, p.tile_off1,
-                       p.zero_words, p.n_zero, p.sorted_src, p.inv, p.row_gate);
+    hipLaunchKernelGGL(perm_single_kernel, dim3(1 + quant), dim3(kPermThreads), 0, stream, ids, gates,
+                       R, E, p.counts, p.offsets, p.bm0, p.tile_off0, p.bm1, p.tile_off1,
+                       p.zero_words, p.n_zero, p.sorted_src, p.inv, p.row_gate, p.quant);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(perm_count_kernel, dim3(n_chunks), dim3(kPermThreads), 0, stream, ids, R,
-                     E, p.chunk_counts);
+  hipLaunchKernelGGL(perm_count_kernel, dim3(n_chunks + quant), dim3(kPermThreads), 0, stream, ids, R,
+                     E, p.chunk_counts, n_chunks, p.quant);
   hipLaunchKernelGGL(perm_scan_kernel, dim3(1), dim3(kPermThreads), 0, stream,
                      p.chunk_counts, n_chunks, E, p.chunk_base, p.counts, p.offsets, p.bm0,
                      p.tile_off0, p.bm1, p.tile_off1, p.zero_words, p.n_zero);
