@@ -390,7 +390,14 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   constexpr int QA = BM / 8 / NW;              // loads of 8 rows per wave and step
   constexpr int kRowLoads = QA + 1;            // and one of 64 scales
   constexpr int kRowsAhead = (NBUF - 2) * kRowLoads;         // loads that may be under way: of rows,
-  constexpr int kAhead = kRowsAhead + (WBUF - 1) * 2 * NS;   // and with those of the weights
+  // Loads go between the products, weights first, so that the matrix unit starts
+  // with the step and not after them (3712 x 2688, M = 4096 50.9 -> 46.6 us, M = 1024
+  // 18.8 -> 16.9); all at once, rows first, where the step is short of time for
+  // them: two buffers, or weights from memory (T = 4096 571 us, spread 583).
+  constexpr bool kSpread = NBUF == 4 && !ONCE;
+  // with the weights': those of steps from this one on that were issued after
+  // the rows of this one
+  constexpr int kAhead = kRowsAhead + (kSpread ? WBUF / 2 : WBUF - 1) * 2 * NS;
   constexpr int SOFF = BM * 128;
   constexpr int kParts = BM < 64 ? 1 : BM / 64;  // loads of 64 rows' scales
   constexpr int WOFF = SOFF + kParts * 256;
@@ -435,18 +442,23 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   const int s_step = of_rows ? g.a_rows : 1;
   const uint32_t s_bytes = 4u * (of_rows ? g.a_rows : (w_blks - w_blk) * steps);
   const int s_to = of_rows ? SOFF + wave * 256 : WOFF;
-  const auto load_rows = [&](int step, uint8_t* buf) __attribute__((always_inline)) {
+  // load i of kRowLoads
+  const auto load_row = [&](int step, uint8_t* buf, int i) __attribute__((always_inline)) {
     const bool in = step < steps;
-    const Buffer b = buffer_of(a, in ? a_bytes : 0u);
-    const int chunks = min(K / 16 - step * 8, 8);  // a last block may be short
-#pragma unroll
-    for (int i = 0; i < QA; ++i) {
+    if (i < QA) {
+      const Buffer b = buffer_of(a, in ? a_bytes : 0u);
+      const int chunks = min(K / 16 - step * 8, 8);  // a last block may be short
       const int ch = (lane & 7) ^ swz((wave * QA + i) * 8 + (lane >> 3));
       load16_to_lds(b, ch < chunks ? ar[i] : kPastEnd, in ? step * 128 : 0, buf + (wave * QA + i) * 1024);
+    } else {
+      const Buffer sb = buffer_of(s_from + static_cast<size_t>(in ? step : 0) * s_step, in ? s_bytes : 0u);
+      load4_to_lds(sb, s_at, 0, buf + s_to);
     }
-    const Buffer sb = buffer_of(s_from + static_cast<size_t>(in ? step : 0) * s_step, in ? s_bytes : 0u);
-    load4_to_lds(sb, s_at, 0, buf + s_to);
     __builtin_amdgcn_sched_barrier(0);  // the order of the loads is what the waits count on
+  };
+  const auto load_rows = [&](int step, uint8_t* buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i) load_row(step, buf, i);
   };
   // weights: the wave's groups of 16 rows; the last one stands in for those past N
   const int m0 = wm * WTM, nw0 = wn * WTN;
@@ -454,12 +466,14 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   const uint8_t* const w_at = t.w + static_cast<size_t>(t.n0 + nw0) / 16 * steps * 2048;
   const uint32_t w_bytes = groups <= 0 ? 0u : static_cast<uint32_t>(groups < NS ? groups : NS) * steps * 2048;
   typedef u32x4 Weights[NS][2];
-  const auto load_w = [&](Weights& w, int step) __attribute__((always_inline)) {
+  const auto load_w1 = [&](Weights& w, int step, int i) __attribute__((always_inline)) {
     const Buffer b = buffer_of(w_at, step < steps ? w_bytes : 0u);
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-      load_weights<ONCE>(w[i], b, lane * 16, step < steps ? (max(min(i, groups - 1), 0) * steps + step) * 2048 : 0);
+    load_weights<ONCE>(w[i], b, lane * 16, step < steps ? (max(min(i, groups - 1), 0) * steps + step) * 2048 : 0);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto load_w = [&](Weights& w, int step) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) load_w1(w, step, i);
   };
 
   // 16-row groups of this wave that hold rows; a wave whose columns all lie past
@@ -480,7 +494,7 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   };
   // Products run kDeep ahead of the multiply-adds that take their results, so
   // that a wave has other products to issue while one is in the matrix unit.
-  const auto compute = [&](const uint8_t* buf, const Weights& w, auto live_c)
+  const auto compute = [&](const uint8_t* buf, const Weights& w, auto live_c, auto issue)
                            __attribute__((always_inline)) {
     constexpr int ML = decltype(live_c)::value;
     constexpr int kDeep = 2;
@@ -498,6 +512,7 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
         const int j = u / NS, i = u % NS;
         if (i == 0 && j + 1 < ML) x[(j + 1) & 1] = frag(xrow + (j + 1) * 2048);
         p[u % (kDeep + 1)] = mma128(join(w[i][0], w[i][1]), x[j & 1]);
+        issue(u);
       }
       if (u >= kDeep) {
         const int v = u - kDeep, j = v / NS, i = v % NS;
@@ -521,9 +536,21 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
     constexpr bool TAIL = decltype(tail_c)::value, kAny = decltype(live_c)::value > 0;
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(TAIL ? 0 : (kAny ? kAhead : kRowsAhead)));
     __asm__ volatile("s_barrier" ::: "memory");
-    if (!TAIL || NBUF == 2) load_rows(step + NBUF - 1, ahead);
-    if (kAny && (!TAIL || WBUF == 2)) load_w(next, step + WBUF - 1);
-    if constexpr (kAny) compute(cur, now, live_c);
+    if constexpr (kAny && !TAIL && kSpread) {
+      constexpr int kLoads = kRowLoads + NS, kProducts = decltype(live_c)::value * NS;
+      compute(cur, now, live_c, [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) {
+          if (l * kProducts / kLoads != u) continue;
+          if (l < NS) load_w1(next, step + WBUF - 1, l);
+          else load_row(step + NBUF - 1, ahead, l - NS);
+        }
+      });
+    } else {
+      if (!TAIL || NBUF == 2) load_rows(step + NBUF - 1, ahead);
+      if (kAny && (!TAIL || WBUF == 2)) load_w(next, step + WBUF - 1);
+      if constexpr (kAny) compute(cur, now, live_c, [](int) {});
+    }
   };
   const auto run = [&](auto live_c) __attribute__((always_inline)) {
     Weights w0, w1, w2, w3;
@@ -713,11 +740,10 @@ hipError_t launch_block_experts(int stage, const BlockArgs& g, hipStream_t strea
 // there are too few tiles for the 256 CUs.  Past that the largest tile is taken
 // that still has about a tile per CU (kFill); each halving of the tile costs
 // 10-20 % of the rate and is worth it only to fill the chip.  3712 x 2688 weights:
-// M = 256 9.5 us with 64 x 64 (64 x 128 12.8, 128 x 128 16.9), M = 512 13.3 with
-// 64 x 128 (64 x 64 15.4, 128 x 128 17.8), M = 1024 19.3 with 128 x 128 (64 x 128
-// 22.0, 128 x 256 30.6), M = 2048 29.8 with 128 x 256 (128 x 128 31.1), M = 4096
-// 50-53 with 256 x 256 (128 x 256 55.7); 1856 x 2688, M = 4096 29.4 with 128 x 256
-// (256 x 256, half the chip, 47.7).
+// M = 256 9.2 us with 64 x 64, M = 512 12.0 with 64 x 128, M = 1024 16.9 with 128 x
+// 128, M = 2048 27.6 with 128 x 256, M = 4096 46.4 with 256 x 256 (one size larger,
+// loads not yet spread: 12.8, 17.8, 30.6, 33.6; one smaller: 15.4, 22.0, 31.1,
+// 55.7); 1856 x 2688, M = 4096 29.5 with 128 x 256 (256 x 256, half the chip, 47.7).
 constexpr int kFill = 200;
 hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream) {
   if (g.M <= 16) return launch_small<1, false>(g, stream);
