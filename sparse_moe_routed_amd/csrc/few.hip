@@ -8,7 +8,11 @@
 // per expert at the full width) and computes next to nothing, so the bound is
 // HBM, and below it the latency of the chain router -> selection -> up ->
 // (tensor scale of a) -> down, which as separate launches costs more than the
-// weights of one token.
+// weights of one token.  Full layer, T = 1 and T = 4: BF16 37 and 82 us, FP8 29
+// and 55, NVFP4 30 and 49 (as separate launches 55 and 81, 47 and 65, 43 and 54).
+// Of NVFP4's 30 us the router's kernel takes 5, the selection 4 to 5, the up
+// projection 8, the wait for it 3, fetching a 3.6 and the down projection 2.3;
+// with more tokens the products stream at 5 to 5.5 TB/s.
 //
 // few_router_kernel writes partial logits.  few_layer_kernel does the rest: its
 // workgroups each redo the selection (a few KB of partial logits), then take

@@ -536,3 +536,69 @@ def test_block_of_the_decoder():
     _check(p, h1.cpu(), w)
     xr, _ = om.residual_norm(x1.float().cpu().numpy(), p.double().cpu().numpy(), gate=t.double().numpy())
     assert (np.abs(x2.double().cpu().numpy() - xr) <= 2.0 ** -8 * np.abs(xr) + 1e-5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 9, 300])
+def test_forward_captured_and_on_two_streams(T):
+    """A captured forward (and shared expert added to it) replayed with new tokens
+    and routing, eager work between the replays; two at once on two streams,
+    each with its own workspace."""
+    L = layer(ODD)
+    sd, d = moe.shared_dims(192, 320), L.dims
+    shared = moe.quantize_experts(L.up[:1].cuda(), L.down[:1].cuda(), "fp8_block", sd)
+    x = synth.make_tokens(T, d).cuda()
+    ids, gates = moe.route(x, L.router, L.ld)
+    ws, y = moe.workspace(L.ld, "fp8_block", T), torch.empty((T, 192), device="cuda")
+    sws = moe.shared_workspace(sd, "fp8_block", T)
+
+    def step(x, ids, gates, y, ws, sws):
+        moe.forward(x, ids, gates, L.bank, L.ld, y=y, ws=ws)
+        return moe.shared_forward(x, shared, sd, y=y, accumulate=True, ws=sws)
+
+    step(x, ids, gates, y, ws, sws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(x, ids, gates, y, ws, sws)
+    for k in range(4):
+        x.copy_(torch.roll(synth.make_tokens(T + 7 * k, d, outliers=k % 2 == 1)[:T], k, 1))
+        i2, g2 = moe.route(x, L.router, L.ld)
+        ids.copy_(i2)
+        gates.copy_(g2)
+        want = step(x, ids, gates, torch.empty_like(y), moe.workspace(L.ld, "fp8_block", T),
+                    moe.shared_workspace(sd, "fp8_block", T)).clone()
+        y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(y) for _ in streams]
+    wss = [(moe.workspace(L.ld, "fp8_block", T), moe.shared_workspace(sd, "fp8_block", T)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, o, w in zip(streams, outs, wss):
+            with torch.cuda.stream(s):
+                step(x, ids, gates, o, *w)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 32, 33, 200])
+def test_linear_captured(M):
+    x, w = _rows(M, 400, M).cuda(), _weight(200, 400, M)
+    W = moe.block_pack(w.cuda())
+    ws = moe.block_linear_workspace(M, 400)
+    y = moe.block_linear(x, W, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.block_linear(x, W, y=y, ws=ws)
+    for k in range(4):
+        x.copy_(_rows(M, 400, 100 + k))
+        want = moe.block_linear(x, W)
+        y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)

@@ -281,3 +281,31 @@ def test_decode_step_between_norms():
                                  post_weight=w[1].double().cpu().numpy(), scale=0.5)
         got = x.double().cpu().numpy()
         assert (np.abs(got - xr) <= 2.0 ** -8 * np.abs(xr) + 1e-5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("T", [4, 5, 9, 16])
+def test_both_ways_captured(fmt, T):
+    """The two kernels and the two calls, whichever the batch takes: captured and
+    replayed on new tokens with eager work between, the same bits as the eager
+    call's, in a workspace full of NaN."""
+    L = layer(FULL)
+    bank = L.bank(fmt)
+    x = synth.make_tokens(T, FULL).cuda()
+    ws = moe.layer_few_workspace(L.ld, fmt, T)
+    ws.fill_(255)
+    y, ids, gates = [t.clone() for t in moe.layer_few(x, L.router, bank, L.ld, ws=ws)]
+    i2, g2 = moe.route(x, L.router, L.ld)
+    assert torch.equal(ids, i2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.layer_few(x, L.router, bank, L.ld, y=y, ids=ids, gates=gates, ws=ws)
+    for k in range(3):
+        x.copy_(torch.roll(synth.make_tokens(T + k, FULL)[:T], k + 1, 1))
+        want = [t.clone() for t in moe.layer_few(x, L.router, bank, L.ld)]
+        y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((y, ids, gates), want))
