@@ -13,6 +13,7 @@ visible, the compute calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -574,26 +575,18 @@ def residual_prenorm(x: torch.Tensor, y: torch.Tensor,
 GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ELEMENT = 0, 1, 2, 3
 
 
-def _raw_stream(device: torch.device):
-    """The current stream of `device` (the tensors' device, which is made the
-    current one by the caller when it is not)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _on(device: torch.device):
-    """Makes `device` current for the launches below it; free when it is."""
-    return torch.cuda.device(device) if device.index != torch._C._cuda_getDevice() else _NO_SWITCH
-
-
-class _NoSwitch:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NO_SWITCH = _NoSwitch()
+def _launch(name: str, fn, index: int, *args):
+    """fn(*args, the current stream of device `index`), with that device current."""
+    here = torch._C._cuda_getDevice()
+    if here != index:
+        torch._C._cuda_setDevice(index)
+    try:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    finally:
+        if here != index:
+            torch._C._cuda_setDevice(here)
+    if status != OK:
+        raise MoeError(name, status)
 
 
 def _same_device(device: torch.device, **tensors):
@@ -604,6 +597,18 @@ def _same_device(device: torch.device, **tensors):
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _arg(t, dtype, name: str, shape, device: torch.device):
+    """_dev and _same_device in one look, for calls whose kernels are shorter than
+    their arguments' checks: a microsecond of a call with seven tensors."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.device == device and t.is_contiguous()):
+        _dev(t, dtype, name, shape)
+        _same_device(device, **{name: t})
+
+
+_Y_DTYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
 
 
 def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torch.Tensor] = None,
@@ -617,41 +622,41 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torc
     stays and out is its pre-norm."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a [T, H] tensor")
-    T, H = x.shape
+    T, H = rows = x.shape
     _dev(x, torch.bfloat16, "x")
-    _same_device(x.device, y=y, out=out, x_out=x_out, gate=gate, post_weight=post_weight,
-                 pre_weight=pre_weight)
+    dev = x.device
     kind, yd = GATE_NONE, Y_F32
     if y is not None:
-        yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}.get(y.dtype)
+        yd = _Y_DTYPES.get(y.dtype)
         if yd is None:
             raise ValueError(f"y: expected float32 or bfloat16, got {y.dtype}")
-        _dev(y, y.dtype, "y", (T, H))
+        _arg(y, y.dtype, "y", rows, dev)
         if x_out is None:
             x_out = x
-        _dev(x_out, torch.bfloat16, "x_out", (T, H))
+        else:
+            _arg(x_out, torch.bfloat16, "x_out", rows, dev)
     elif x_out is not None or gate is not None or post_weight is not None:
         raise ValueError("x_out, gate and post_weight need a block output y")
     if gate is not None:
-        kinds = {(T, 1): GATE_TOKEN, (H,): GATE_CHANNEL, (T, H): GATE_ELEMENT}
-        kind = kinds.get(tuple(gate.shape))
+        shape = gate.shape
+        kind = (GATE_TOKEN if shape == (T, 1) else GATE_CHANNEL if shape == (H,) else
+                GATE_ELEMENT if shape == rows else None)
         if kind is None:
             raise ValueError(f"gate: expected shape ({T}, 1), ({H},) or ({T}, {H}), got {tuple(gate.shape)}")
-        _dev(gate, torch.float32, "gate")
+        _arg(gate, torch.float32, "gate", shape, dev)
     if post_weight is not None:
-        _dev(post_weight, torch.float32, "post_weight", (H,))
+        _arg(post_weight, torch.float32, "post_weight", (H,), dev)
     if pre_weight is not None:
-        _dev(pre_weight, torch.float32, "pre_weight", (H,))
+        _arg(pre_weight, torch.float32, "pre_weight", (H,), dev)
     if pre_norm and out is None:
         out = torch.empty_like(x)
     if out is not None:
         if not pre_norm:
             raise ValueError("out: given with pre_norm=False")
-        _dev(out, torch.bfloat16, "out", (T, H))
-    with _on(x.device):
-        _check("moe_residual_norm", lib().moe_residual_norm(
+        _arg(out, torch.bfloat16, "out", rows, dev)
+    _launch("moe_residual_norm", lib().moe_residual_norm, dev.index,
             T, H, x.data_ptr(), _p(y), yd, _p(gate), kind, _p(post_weight), _p(pre_weight), scale, eps,
-            int(bool(post_norm)), _p(x_out), _p(out), _raw_stream(x.device)))
+            1 if post_norm else 0, _p(x_out), _p(out))
     return (x if y is None else x_out), out
 
 
@@ -702,10 +707,9 @@ def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
     r = Router(router.w_packed.data_ptr(),
                router.bias.data_ptr() if router.bias is not None else None)
     e = experts.c()
-    with _on(dev):
-        _check("moe_layer_few", lib().moe_layer_few(
+    _launch("moe_layer_few", lib().moe_layer_few, dev.index,
             ctypes.byref(d), T, x.data_ptr(), ctypes.byref(r), ctypes.byref(e), ids.data_ptr(),
-            gates.data_ptr(), y.data_ptr(), yd, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
+            gates.data_ptr(), y.data_ptr(), yd, ws.data_ptr(), ws.numel())
     return y, ids, gates
 
 
@@ -740,9 +744,8 @@ def block_pack(w: torch.Tensor) -> BlockWeight:
     N, K = _matrix(w, torch.bfloat16, "w").shape
     codes = torch.empty(block_packed_size(N, K), dtype=torch.uint8, device=w.device)
     scales = torch.empty((-(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
-    with _on(w.device):
-        _check("moe_block_pack", lib().moe_block_pack(N, K, w.data_ptr(), codes.data_ptr(),
-                                                      scales.data_ptr(), _raw_stream(w.device)))
+    _launch("moe_block_pack", lib().moe_block_pack, w.device.index,
+            N, K, w.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return BlockWeight(codes, scales, (N, K))
 
 
@@ -756,9 +759,8 @@ def block_pack_codes(codes: torch.Tensor, scales: torch.Tensor) -> BlockWeight:
     _dev(scales, torch.float32, "scales", (-(-N // 128), -(-K // 128)))
     _same_device(codes.device, scales=scales)
     packed = torch.empty(block_packed_size(N, K), dtype=torch.uint8, device=codes.device)
-    with _on(codes.device):
-        _check("moe_block_pack_codes", lib().moe_block_pack_codes(
-            N, K, codes.data_ptr(), packed.data_ptr(), _raw_stream(codes.device)))
+    _launch("moe_block_pack_codes", lib().moe_block_pack_codes, codes.device.index,
+            N, K, codes.data_ptr(), packed.data_ptr())
     return BlockWeight(packed, scales, (N, K))
 
 
@@ -768,9 +770,8 @@ def block_quantize(x: torch.Tensor):
     M, K = _matrix(x, torch.bfloat16, "x").shape
     codes = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     scales = torch.empty((-(-K // 128), M), dtype=torch.float32, device=x.device)
-    with _on(x.device):
-        _check("moe_block_quantize", lib().moe_block_quantize(
-            M, K, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _raw_stream(x.device)))
+    _launch("moe_block_quantize", lib().moe_block_quantize, x.device.index,
+            M, K, x.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -779,15 +780,13 @@ def _block_operands(rows: torch.Tensor, weight: BlockWeight, y: Optional[torch.T
     N = weight.shape[0]
     if weight.shape[1] != K:
         raise ValueError(f"weight: K is {weight.shape[1]}, the rows have {K}")
-    _dev(weight.codes, torch.uint8, "weight.codes", ((N + 15) // 16 * -(-K // 128) * 2048,))
-    _dev(weight.scales, torch.float32, "weight.scales", (-(-N // 128), -(-K // 128)))
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=rows.device)
-    else:
-        _dev(y, torch.bfloat16, "y", (M, N))
     dev = rows.device
-    if weight.codes.device != dev or weight.scales.device != dev or y.device != dev:
-        _same_device(dev, **{"weight.codes": weight.codes, "weight.scales": weight.scales, "y": y})
+    _arg(weight.codes, torch.uint8, "weight.codes", ((N + 15) // 16 * -(-K // 128) * 2048,), dev)
+    _arg(weight.scales, torch.float32, "weight.scales", (-(-N // 128), -(-K // 128)), dev)
+    if y is None:
+        y = rows.new_empty((M, N), dtype=torch.bfloat16)
+    else:
+        _arg(y, torch.bfloat16, "y", (M, N), dev)
     return M, N, K, y
 
 
@@ -798,15 +797,19 @@ def block_matmul(codes: torch.Tensor, scales: torch.Tensor, weight: BlockWeight,
     M, N, K, y = _block_operands(codes, weight, y)
     _dev(scales, torch.float32, "scales", (-(-K // 128), M))
     _same_device(codes.device, scales=scales)
-    with _on(codes.device):
-        _check("moe_block_matmul", lib().moe_block_matmul(
+    _launch("moe_block_matmul", lib().moe_block_matmul, codes.device.index,
             M, N, K, codes.data_ptr(), scales.data_ptr(), weight.codes.data_ptr(),
-            weight.scales.data_ptr(), y.data_ptr(), _raw_stream(codes.device)))
+            weight.scales.data_ptr(), y.data_ptr())
     return y
 
 
+@functools.lru_cache(maxsize=256)
+def _block_linear_bytes(max_rows: int, K: int) -> int:
+    return int(lib().moe_block_linear_workspace_size(max_rows, K))
+
+
 def block_linear_workspace(max_rows: int, K: int, device="cuda") -> torch.Tensor:
-    n = int(lib().moe_block_linear_workspace_size(int(max_rows), int(K)))
+    n = _block_linear_bytes(int(max_rows), int(K))
     if n == 0:
         raise ValueError(f"moe_block_linear_workspace_size: invalid rows {max_rows} or K {K}")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -822,8 +825,7 @@ def block_linear(x: torch.Tensor, weight: BlockWeight, y: Optional[torch.Tensor]
         _same_device(x.device, ws=ws)
     elif M > BLOCK_FEW_ROWS:
         ws = block_linear_workspace(M, K, x.device)
-    with _on(x.device):
-        _check("moe_block_linear", lib().moe_block_linear(
+    _launch("moe_block_linear", lib().moe_block_linear, x.device.index,
             M, N, K, x.data_ptr(), weight.codes.data_ptr(), weight.scales.data_ptr(), y.data_ptr(),
-            _p(ws), 0 if ws is None else ws.numel(), _raw_stream(x.device)))
+            _p(ws), 0 if ws is None else ws.numel())
     return y
