@@ -563,7 +563,10 @@ __host__ __device__ constexpr int chunks_of(int K) {
 
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
-  constexpr int P = FMT == kBF16 ? 4 : 3;  // units in flight per wave
+  // units in flight per wave: 16 waves keep 32 KB to 64 KB of loads under way per
+  // CU; 3 and 4 are 1 % slower, 5 and 6 up to 10 % (loads past a stream's end
+  // touch no memory but are issued)
+  constexpr int P = 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   Shared& sm = *reinterpret_cast<Shared*>(dyn);
   uint8_t* const stage = dyn + (sizeof(Shared) + 15) / 16 * 16;  // tokens, later rows of a
