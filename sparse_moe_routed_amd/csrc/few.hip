@@ -540,7 +540,8 @@ __device__ __forceinline__ void stage_rows(int rows, int chunks, Get get, Put pu
     int r[kBatch], c[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int i = min(i0 + j * kThreads, n - 2 + (me & 1));
+      const int i = i0 + j * kThreads;
+      if (i >= n) break;
       // i / chunks: i < 2^14 here, so the quotient is off by less than the
       // distance of (i + 1/2) / chunks from a whole number
       r[j] = static_cast<int>((static_cast<float>(i) + 0.5f) * inv);
@@ -549,8 +550,8 @@ __device__ __forceinline__ void stage_rows(int rows, int chunks, Get get, Put pu
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const u32x4 o = make(v[j]);
-      if (i0 + j * kThreads < n) *reinterpret_cast<u32x4*>(put(r[j], c[j])) = o;
+      if (i0 + j * kThreads >= n) break;  // both threads of a pair, or neither
+      *reinterpret_cast<u32x4*>(put(r[j], c[j])) = make(v[j]);
     }
   }
 }
