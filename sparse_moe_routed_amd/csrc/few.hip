@@ -433,15 +433,16 @@ __device__ __forceinline__ void clear_routing(Shared& sm) {
   if (threadIdx.x < kMaxRows / 2) sm.rt.key[threadIdx.x] = 0xffffffffu;
 }
 
-// top-k and gates of the tokens wave, wave + kWaves, ...
+// top-k and gates of the tokens wave, wave + kWaves, ... of up to 64 N experts
+template <int N>
 __device__ __forceinline__ void select_experts(const FewArgs& g, Shared& sm) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Routing& rt = sm.rt;
   for (int t = wave; t < g.T; t += kWaves) {
-    float v[kMaxE / 64];
-    uint32_t key[kMaxE / 64];
+    float v[N];
+    uint32_t key[N];
 #pragma unroll
-    for (int i = 0; i < kMaxE / 64; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int e = lane + 64 * i;
       v[i] = -INFINITY;
       key[i] = 0u;
@@ -581,7 +582,8 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
   if (tid == 0) sm.next = static_cast<int>(atomicAdd(&g.ctr[kFewTicket], 1u));
   clear_routing(sm);
   __syncthreads();
-  select_experts(g, sm);
+  if (g.E <= 128) select_experts<2>(g, sm);
+  else select_experts<kMaxE / 64>(g, sm);
   // The tokens as the operand: chunk ch of token t at (ch * T + t) * 16, so the
   // lanes of one MFMA read consecutive addresses.
   const int T16 = T * 16;
@@ -614,8 +616,9 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
   const uint8_t* const col = stage + min(c, T - 1) * 16;
   while (ticket < up_items) {
     float local = 0.f;
-    const int t1 = static_cast<int>(static_cast<int64_t>(up_tiles) * (ticket + 1) / up_items);
-    int t0 = static_cast<int>(static_cast<int64_t>(up_tiles) * ticket / up_items);
+    // (up_tiles * up_items < 2^31: at most 128 experts, 256 items, F < 2^16)
+    const int t1 = static_cast<int>(static_cast<uint32_t>(up_tiles * (ticket + 1)) / static_cast<uint32_t>(up_items));
+    int t0 = static_cast<int>(static_cast<uint32_t>(up_tiles * ticket) / static_cast<uint32_t>(up_items));
     const int U = units_of<FMT>(H);
     Tile<FMT, false> w;
     int ksl = 0, e = 0, n0 = 0, u0 = 0, n = 0;  // of the round that is streaming

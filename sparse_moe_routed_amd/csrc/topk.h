@@ -30,13 +30,14 @@ __device__ __forceinline__ uint32_t float_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// The k largest of the logits v over the wave (lane l holds experts l + 64 i;
+// The k largest of the logits v over the wave (lane l holds experts l + 64 i, i < N;
 // key is float_key(v), 0 past E, and is used up): sel_i in order of (logit
 // desc, index asc), sel_v their logits.  Each of the k rounds takes the largest
 // key over the wave, then the lowest expert index holding it (ballots over the
 // slots in index order), and retires that expert.
-__device__ __forceinline__ void wave_topk(const float (&v)[kMaxE / 64], uint32_t (&key)[kMaxE / 64],
-                                          int k, float (&sel_v)[8], int (&sel_i)[8]) {
+template <int N>
+__device__ __forceinline__ void wave_topk(const float (&v)[N], uint32_t (&key)[N], int k,
+                                          float (&sel_v)[8], int (&sel_i)[8]) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -45,18 +46,18 @@ __device__ __forceinline__ void wave_topk(const float (&v)[kMaxE / 64], uint32_t
     if (j >= k) continue;
     uint32_t m = key[0];
 #pragma unroll
-    for (int i = 1; i < kMaxE / 64; ++i) m = max(m, key[i]);
+    for (int i = 1; i < N; ++i) m = max(m, key[i]);
     const uint32_t best = wave_umax(m);
     int win = -1;
 #pragma unroll
-    for (int i = 0; i < kMaxE / 64; ++i) {
+    for (int i = 0; i < N; ++i) {
       const uint64_t b = __ballot(key[i] == best && key[i] != 0u);
       if (win < 0 && b) win = 64 * i + __ffsll(static_cast<unsigned long long>(b)) - 1;
     }
     // the winner's logit, from the lane that holds it
     float wv = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kMaxE / 64; ++i)
+    for (int i = 0; i < N; ++i)
       if (lane + 64 * i == win) {
         wv = v[i];
         key[i] = 0u;
