@@ -432,7 +432,7 @@ int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const v
  * MOE_FEW_TOKENS tokens in two kernels (decode, where the six to nine launches
  * of the two calls cost more than the weights of one token), or as the two calls
  * where those are faster or the two kernels do not apply: FP8_BLOCK banks; more
- * than 100000 (BF16) or 50000 (NVFP4) values in the T*k rows of the
+ * than 140000 (BF16) or 60000 (NVFP4) values in the T*k rows of the
  * intermediate; T rows of H or F + 8 bf16 values, H and F rounded up to 128,
  * beyond 120 KiB; expert matrices of 2^30 values and more.  Formulas, routing
  * order and quantisation are those of the two calls; the two kernels sum in

@@ -8,11 +8,11 @@
 // per expert at the full width) and computes next to nothing, so the bound is
 // HBM, and below it the latency of the chain router -> selection -> up ->
 // (tensor scale of a) -> down, which as separate launches costs more than the
-// weights of one token.  Full layer, T = 1 and T = 4: BF16 37 and 82 us, FP8 29
-// and 55, NVFP4 30 and 49 (as separate launches 55 and 81, 47 and 65, 43 and 54).
-// Of NVFP4's 30 us the router's kernel takes 5, the selection 4 to 5, the up
-// projection 8, the wait for it 3, fetching a 3.6 and the down projection 2.3;
-// with more tokens the products stream at 5 to 5.5 TB/s.
+// weights of one token.  Full layer, T = 1 and T = 4: BF16 37 and 82 us, FP8 28
+// and 54, NVFP4 28 and 49 (as separate launches 55 and 81, 47 and 65, 43 and 54).
+// Of NVFP4's 28 us the router's kernel takes 5, the start of 256 workgroups 3, the
+// selection 4, the up projection 7, the wait for it 2, fetching a 2 and the down
+// projection 2.5; with more tokens the products stream at 5 to 5.7 TB/s.
 //
 // few_router_kernel writes partial logits.  few_layer_kernel does the rest: its
 // workgroups each redo the selection (a few KB of partial logits), then take
@@ -857,12 +857,12 @@ hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
 // kernels are not slower than moe_route and moe_forward.  What they save is
 // launches, about 20 us; what they cost grows with the rows of a that every
 // workgroup stages, and for NVFP4 quantises, T k F values.  Full layer (k F =
-// 11136), these against the two calls: BF16 T = 1 37 us (55), 8 120 (119),
-// 16 192 (183); NVFP4 T = 1 30 (42), 4 48 (50), 8 68 (61), 16 105 (81); FP8
-// T = 1 29 (48), 8 78 (89), 16 116 (122).
+// 11136), us of these against the two calls: BF16 T = 1 37 (55), 8 122 (126), 12
+// 158 (160), 16 189 (182); NVFP4 T = 1 28 (43), 5 53 (54), 6 59 (57), 16 103 (84);
+// FP8 T = 1 28 (47), 8 78 (87), 16 113 (119).
 bool few_pays(int fmt, int T, int H, int F, int k) {
   const size_t staged = static_cast<size_t>(T) * k * F;
-  if (fmt == kFP8Block || (fmt == kBF16 && staged > 100000) || (fmt == kNVFP4 && staged > 50000)) return false;
+  if (fmt == kFP8Block || (fmt == kBF16 && staged > 140000) || (fmt == kNVFP4 && staged > 60000)) return false;
   return stage_need(T, H, F) <= kMaxStage &&
          static_cast<size_t>(H) * F * 2 < (static_cast<size_t>(1) << 31);
 }
