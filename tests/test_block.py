@@ -367,10 +367,12 @@ def test_forward_matches_oracle(name, T):
     for b in range(kb):
         w, e = want[:, b * 128:b * 128 + 128].max(1), e_a[:, b * 128:b * 128 + 128].max(1)
         assert (np.abs(448 * scales[:, b].astype(np.float64) - w) <= e + 2.0 ** -23 * w).all()
-    # One bf16 value in twenty at most lies near enough to a border to fall on its
-    # other side: a code differs where its value does, or its block's maximum.
+    # The sums are fp32 of exact products, off by some 2^-24 sqrt(n) = 2^-18 of
+    # their size: one bf16 value in 500 falls on the other side of a border (step
+    # 2^-8), and a code differs where that crosses one of its own, or where its
+    # block's maximum did and 6 % of the block's codes with it.
     qo, so = codecs.fp8_block_quantize(want)
-    assert (codes != qo).mean() <= 0.1
+    assert (codes != qo).mean() <= 0.002
     # The output, against the oracle's: one value of the intermediate on the
     # other side of a border moves its code by a whole step, whatever its
     # distance, so the difference of the two intermediates is carried through
