@@ -326,7 +326,7 @@ typedef struct {
   int64_t out_rows;   /* fp32 [T*k, H]: gate * W_down a~, sorted row order   */
   int64_t x_q;        /* [T, H] dequantised token values without the tensor
                          scale: FP8 bf16 dec(q); NVFP4 fp16 dec(q)*dec(sb);
-                         FP8_BLOCK fp16 dec(q), fp32 scales [ceil(H/128), T]
+                         FP8_BLOCK u8 codes, fp32 scales [ceil(H/128), T]
                          behind them at the next multiple of 256 bytes       */
   int64_t act_q;      /* FP8: u8 [T*k, F] codes; NVFP4: fp16 dec(q)*dec(sb)
                          in place over act; FP8_BLOCK: u8 [T*k, F] codes,

@@ -15,12 +15,11 @@
 //
 // The experts' up projection is the exception: its sums become codes again, and
 // there a sum that is cut short moves a whole E4M3 step, or a block's scale.  Its
-// products are exact: rows come as the codes' values in fp16, the weights' codes
-// become fp16 in registers (both exact), and four 16x16x32 products in fp32 take
-// the place of the one.  Against exact sums the layer's bf16 output is then off by
-// 1.7e-3, its own rounding (with the short sums 2.0e-3 to 2.9e-3).  Batches that
-// read weights from memory do not notice (T = 5 52 us, T = 64 160); at T = 4096 the
-// up projection takes 339 us instead of 226.
+// products are exact: both operands' codes become fp16 in registers, and four
+// 16x16x32 products in fp32 take the place of the one.  Against exact sums the
+// layer's bf16 output is then off by 1.7e-3, its own rounding (with the short sums
+// 2.0e-3 to 2.9e-3).  Batches that read weights from memory do not notice (T = 5
+// 52 us, T = 64 160); at T = 4096 the up projection takes 327 us instead of 226.
 //
 // Weight codes are packed in operand order: for each group of 16 rows and each
 // K block 2 KB, [half h][lane l][16 bytes] = row l % 16, values 32 (l / 16) + 16 h
@@ -402,9 +401,8 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   constexpr int NW = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int MS = WTM / 16, NS = WTN / 16;  // 16 x 16 products of a wave
-  constexpr bool kHalf = MODE == kBlockUp;     // rows hold the codes' values in fp16
-  constexpr int kRowB = kHalf ? 256 : 128;     // bytes of a row and step
-  constexpr int QA = BM * kRowB / 1024 / NW;   // 1 KB loads of rows per wave and step
+  constexpr bool kHalf = MODE == kBlockUp;     // exact products, in fp16
+  constexpr int QA = BM / 8 / NW;              // loads of 8 rows per wave and step
   constexpr int kRowLoads = QA + 1;            // and one of 64 scales
   constexpr int kRowsAhead = (NBUF - 2) * kRowLoads;         // loads that may be under way: of rows,
   // Loads go between the products, weights first, so that the matrix unit starts
@@ -415,12 +413,13 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   // with the weights': those of steps from this one on that were issued after
   // the rows of this one
   constexpr int kAhead = kRowsAhead + (kSpread ? WBUF / 2 : WBUF - 1) * 2 * NS;
-  constexpr int SOFF = BM * kRowB;
+  constexpr int SOFF = BM * 128;
   constexpr int kParts = BM < 64 ? 1 : BM / 64;  // loads of 64 rows' scales
   constexpr int WOFF = SOFF + kParts * 256;
   constexpr int BUF = WOFF + 256;
-  static_assert(QA * 1024 * NW == BM * kRowB && 128 % WTN == 0 && BN % WTN == 0, "tile");
+  static_assert(QA * 8 * NW == BM && 128 % WTN == 0 && BN % WTN == 0, "tile");
   static_assert(BM % 64 == 0 || BM == 32, "scales come 64 at a time");
+  static_assert(NS == 1 || NS == 2 || NS == 4, "columns of a wave");
   static_assert((NBUF == 2 || NBUF == 4) && (WBUF == 2 || WBUF == 4) && kAhead < 64, "buffers");
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[BUF];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[BUF];
@@ -437,22 +436,15 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   // 2^32 bytes, checked by the caller), others from the tile's first.
   const bool gather = MODE == kBlockUp;
   const size_t first = gather ? 0 : static_cast<size_t>(t.row0);
-  constexpr int kSize = kHalf ? 2 : 1;  // bytes of a value
-  const uint32_t a_bytes = static_cast<uint32_t>(static_cast<size_t>(gather ? g.a_rows : t.rows) * K * kSize);
-  const uint8_t* const a = g.a + first * K * kSize;
-  // this lane's row of a 1 KB piece, and its chunk of that row (see swz)
-  const auto row_of = [&](int piece) __attribute__((always_inline)) {
-    return kHalf ? piece * 4 + (lane >> 4) : piece * 8 + (lane >> 3);
-  };
-  const auto chunk_of = [&](int row) __attribute__((always_inline)) {
-    return kHalf ? (lane & 15) ^ (row & 15) : (lane & 7) ^ swz(row);
-  };
+  const uint32_t a_bytes = static_cast<uint32_t>(static_cast<size_t>(gather ? g.a_rows : t.rows) * K);
+  const uint8_t* const a = g.a + first * K;
   uint32_t ar[QA];
 #pragma unroll
   for (int i = 0; i < QA; ++i) {
-    const int r = row_of(wave * QA + i);
+    const int r = (wave * QA + i) * 8 + (lane >> 3);
+    const int ch = ((lane & 7) ^ swz(r)) * 16;
     const uint32_t row = static_cast<uint32_t>(source_row<MODE>(g, t.row0 + min(r, t.rows - 1)) - first);
-    ar[i] = row * K * kSize + chunk_of(r) * 16;
+    ar[i] = row * K + ch;
   }
   // Scales: wave p < kParts loads those of 64 rows, the others those of the
   // weights' 128-row blocks (all the same words to the same place), so that
@@ -471,9 +463,9 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
     const bool in = step < steps;
     if (i < QA) {
       const Buffer b = buffer_of(a, in ? a_bytes : 0u);
-      const int chunks = K * kSize / 16 - step * (kRowB / 16);  // a last block may be short
-      const int ch = chunk_of(row_of(wave * QA + i));
-      load16_to_lds(b, ch < chunks ? ar[i] : kPastEnd, in ? step * kRowB : 0, buf + (wave * QA + i) * 1024);
+      const int chunks = min(K / 16 - step * 8, 8);  // a last block may be short
+      const int ch = (lane & 7) ^ swz((wave * QA + i) * 8 + (lane >> 3));
+      load16_to_lds(b, ch < chunks ? ar[i] : kPastEnd, in ? step * 128 : 0, buf + (wave * QA + i) * 1024);
     } else {
       const Buffer sb = buffer_of(s_from + static_cast<size_t>(in ? step : 0) * s_step, in ? s_bytes : 0u);
       load4_to_lds(sb, s_at, 0, buf + s_to);
@@ -549,18 +541,25 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // The same with rows of fp16: four products of 32 values a block, chained in
-  // fp32, over the lane's 32 values of k in the order of its weights' codes.
-  const auto compute_half = [&](const uint8_t* buf, const Weights& w, auto live_c) __attribute__((always_inline)) {
+  // The same with codes turned into fp16, which is exact: four products of 32
+  // values a block, chained in fp32, over the lane's 32 values of k in their order.
+  const auto compute_half = [&](const uint8_t* buf, const Weights& w, auto live_c, auto issue)
+                                __attribute__((always_inline)) {
     constexpr int ML = decltype(live_c)::value;
-    const uint8_t* const xrow = buf + m0 * kRowB + c * kRowB;
+    const uint8_t* const xrow = buf + m0 * 128;
     const float* const srow = reinterpret_cast<const float*>(buf + SOFF) + m0 + c;
     const float sw = reinterpret_cast<const float*>(buf + WOFF)[nw0 / 128];
-    u32x4 x[2][4];
-    const auto read = [&](u32x4 (&to)[4], int j) __attribute__((always_inline)) {
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        to[h] = *reinterpret_cast<const u32x4*>(xrow + j * 16 * kRowB + (((4 * q + h) ^ c) << 4));
+    const auto half = [&](uint32_t lo, uint32_t hi) __attribute__((always_inline)) {
+      const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+      const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+      const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+      const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+      return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+    };
+    u32x4 x[2][2];
+    const auto read = [&](u32x4 (&to)[2], int j) __attribute__((always_inline)) {
+      to[0] = *reinterpret_cast<const u32x4*>(xrow + j * 2048 + off0);
+      to[1] = *reinterpret_cast<const u32x4*>(xrow + j * 2048 + off1);
     };
     read(x[0], 0);
     f16x8 wf[NS][4];
@@ -568,12 +567,7 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
     for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const uint32_t lo = w[i][h >> 1][(h & 1) * 2], hi = w[i][h >> 1][(h & 1) * 2 + 1];
-        const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-        const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-        const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-        const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-        wf[i][h] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+        wf[i][h] = half(w[i][h >> 1][(h & 1) * 2], w[i][h >> 1][(h & 1) * 2 + 1]);
       }
     f32x4 p[2][NS];
     float s[2];
@@ -583,13 +577,16 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
         if (j + 1 < ML) read(x[(j + 1) & 1], j + 1);
         s[j & 1] = srow[j * 16] * sw;
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < 4; ++h) {
+          const f16x8 xf = half(x[j & 1][h >> 1][(h & 1) * 2], x[j & 1][h >> 1][(h & 1) * 2 + 1]);
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
             const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            p[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                wf[i][h], __builtin_bit_cast(f16x8, x[j & 1][h]), h == 0 ? zero : p[j & 1][i], 0, 0, 0);
+            p[j & 1][i] =
+                __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[i][h], xf, h == 0 ? zero : p[j & 1][i], 0, 0, 0);
           }
+          if (h * NS % 4 == 0) issue(j * NS + h * NS / 4);
+        }
       }
       if (j > 0) {
 #pragma unroll
@@ -614,18 +611,20 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
     __asm__ volatile("s_barrier" ::: "memory");
     if constexpr (kAny && !TAIL && kSpread) {
       constexpr int kLoads = kRowLoads + NS, kProducts = decltype(live_c)::value * NS;
-      compute(cur, now, live_c, [&](int u) __attribute__((always_inline)) {
+      const auto issue = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
         for (int l = 0; l < kLoads; ++l) {
           if (l * kProducts / kLoads != u) continue;
           if (l < NS) load_w1(next, step + WBUF - 1, l);
           else load_row(step + NBUF - 1, ahead, l - NS);
         }
-      });
+      };
+      if constexpr (kHalf) compute_half(cur, now, live_c, issue);
+      else compute(cur, now, live_c, issue);
     } else {
       if (!TAIL || NBUF == 2) load_rows(step + NBUF - 1, ahead);
       if (kAny && (!TAIL || WBUF == 2)) load_w(next, step + WBUF - 1);
-      if constexpr (kAny && kHalf) compute_half(cur, now, live_c);
+      if constexpr (kAny && kHalf) compute_half(cur, now, live_c, [](int) {});
       else if constexpr (kAny) compute(cur, now, live_c, [](int) {});
     }
   };
@@ -805,14 +804,15 @@ int block_tile_rows(int R, int E) { return R < (16 * E > 256 ? 16 * E : 256) ? 3
 // dealt round the XCDs 605 and 340).  There matrix unit, LDS and vector unit are
 // each busy a quarter to a third of the time and HBM runs at 3.4 TB/s: the steps'
 // latencies are what is left.
-// (These are of E4M3 products in both projections.  With the up projection's in
-// fp16, T = 4096: 688 us, 128 x 256 in 8 waves 685, 128 x 128 in 8 waves 717, 2 x 4
-// waves 755, 2 x 2 waves 837; T = 1024 374, 378, 385, 416, 438.)
+// (These are of E4M3 products in both projections.  The up projection's in fp16
+// are bound by the matrix unit: 128 x 128 in 2 x 2 waves T = 4096 669 us, in a row of
+// 4 waves 684, 128 x 256 in 8 waves 677, 2 x 4 waves 709; tokens handed over in fp16
+// instead of codes, which is half the conversions and twice the LDS reads, 688.)
 hipError_t launch_block_experts(int stage, const BlockArgs& g, hipStream_t stream, const KernelEvents& ev) {
   if (block_tile_rows(g.M, g.E) == 32)
     return stage == 0 ? launch_large<kBlockUp, 32, 128, 1, 4, 4, 4, true>(g, stream, ev)
                       : launch_large<kBlockDown, 32, 64, 1, 4, 4, 4, true>(g, stream, ev);
-  return stage == 0 ? launch_large<kBlockUp, 128, 128, 1, 4, 2, 2>(g, stream, ev)
+  return stage == 0 ? launch_large<kBlockUp, 128, 128, 2, 2, 4, 2>(g, stream, ev)
                     : launch_large<kBlockDown, 128, 128, 1, 4, 2, 2>(g, stream, ev);
 }
 

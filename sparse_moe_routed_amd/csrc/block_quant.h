@@ -70,18 +70,8 @@ __device__ __forceinline__ void block_quantise(const BlockQuantArgs& q, int grou
     if (k < q.cols) v = *reinterpret_cast<const u32x4*>(q.x + at);
     const float amax = row16_max(amax8(v));
     const bool live = amax >= kTinyAmax;
-    const uint2 code = encode8(v, live ? __fdiv_rn(448.f, amax) : 0.f);
-    if (k < q.cols && q.half) {
-      const f16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code.x, 1.0f, false);
-      const f16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code.x, 1.0f, true);
-      const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code.y, 1.0f, false);
-      const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code.y, 1.0f, true);
-      *reinterpret_cast<u32x4*>(q.codes + 2 * at) =
-          u32x4{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
-                __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
-    } else if (k < q.cols) {
-      *reinterpret_cast<uint2*>(q.codes + at) = code;
-    }
+    if (k < q.cols)
+      *reinterpret_cast<uint2*>(q.codes + at) = encode8(v, live ? __fdiv_rn(448.f, amax) : 0.f);
     if (l16 == 0) q.scales[static_cast<size_t>(kb) * q.rows + r] = live ? __fdiv_rn(amax, 448.f) : 0.f;
   }
 }

@@ -111,7 +111,7 @@ Layout make_layout(const moe_dims* d, int32_t fmt, int32_t T) {
   L.has_actq = fmt != kBF16;
   L.actq_inplace = fmt == kNVFP4;
   if (fmt == kFP8Block) {  // codes and block scales
-    L.x_q = alloc(static_cast<size_t>(T) * H * 2);
+    L.x_q = alloc(static_cast<size_t>(T) * H);
     L.x_s = alloc(kblocks(H) * T * 4);
     L.act_q = alloc(R * F);
     L.act_s = alloc(kblocks(F) * R * 4);
@@ -489,7 +489,7 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
       !bank_aligned(ex))
     return MOE_EINVAL;
   // the block-scaled products address the tokens' codes by 32 bits
-  if (ex->fmt == kFP8Block && static_cast<size_t>(T) * dims->hidden * 2 >= moe::kBlockMaxBytes)
+  if (ex->fmt == kFP8Block && static_cast<size_t>(T) * dims->hidden >= moe::kBlockMaxBytes)
     return MOE_EUNSUPPORTED;
   const Layout L = make_layout(dims, ex->fmt, T);
   if (!ws || ws_bytes < L.total) return MOE_EWORKSPACE;
@@ -521,7 +521,7 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   p.zero_words = amax_x;  // amax slots of x and of the intermediate
   p.n_zero = 2 * moe::kAmaxSlots;
   if (fmt == kFP8Block)
-    p.quant = {static_cast<const uint16_t*>(x), T, H, at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s), true};
+    p.quant = {static_cast<const uint16_t*>(x), T, H, at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s)};
   marks.mark(0);
   hipError_t err = shared ? moe::launch_permute_identity(R, p, st)
                           : moe::launch_permute(ids, gates, T, E, k, p, st);
@@ -789,7 +789,7 @@ int32_t moe_quantize_activation(int32_t fmt, int32_t rows, int32_t cols, const v
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (fmt == kFP8Block)
     return hip_status(moe::launch_block_quant({static_cast<const uint16_t*>(x), rows, cols,
-                                               static_cast<uint8_t*>(codes), scale, false}, st));
+                                               static_cast<uint8_t*>(codes), scale}, st));
   uint32_t* amax = static_cast<uint32_t*>(ws);  // kAmaxSlots words
   hipError_t err = moe::launch_zero_u32(amax, moe::kAmaxSlots, st);
   if (err == hipSuccess)
@@ -963,7 +963,7 @@ int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, flo
   if (!x || !codes || !scales) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
   return hip_status(moe::launch_block_quant({static_cast<const uint16_t*>(x), M, K,
-                                             static_cast<uint8_t*>(codes), scales, false},
+                                             static_cast<uint8_t*>(codes), scales},
                                             static_cast<hipStream_t>(stream)));
 }
 

@@ -39,7 +39,6 @@ struct BlockQuantArgs {
   int rows, cols;
   uint8_t* codes;
   float* scales;
-  bool half;  // the codes' values in fp16 (exact) instead of the codes
 };
 
 struct PermBufs {
@@ -209,7 +208,7 @@ enum BlockMode { kBlockDense = 0, kBlockUp = 1, kBlockDown = 2 };
 constexpr uint32_t kBlockMaxBytes = 0xf0000000u;  // gathered activation rows stay below
 struct BlockArgs {
   int M, N, K;
-  const uint8_t* a;   // codes [rows, K]; up: their values in fp16; launch_block_few_linear: bf16
+  const uint8_t* a;   // codes [rows, K]; launch_block_few_linear: bf16 [M, K]
   const float* a_s;   // [ceil(K / 128), a_rows]
   int a_rows;
   const uint8_t* w;   // codes of E matrices [N, K], packed (block.hip)
