@@ -344,7 +344,7 @@ int32_t moe_workspace_layout(const moe_dims* dims, int32_t fmt, int32_t T,
  * for FP8 and, over each 128 x 128 block, FP8_BLOCK (scales as in moe_experts;
  * a block whose amax is below 2^-100 becomes zero); S = f32(amax/2688), block scale sb = E4M3(f32(amax_b/f32(6S))),
  * code = E2M1(f32(w*f32(1/f32(sb*S)))) for NVFP4; amax == 0 -> zero codes and
- * scale).  Layouts as in moe_experts.
+ * scale; 448/amax or 1/(sb*S) past the range of fp32 counts as 0: zero codes).  Layouts as in moe_experts.
  *   up_bf16 [dev] [E, F, H], down_bf16 [dev] [E, H, F]
  *   up_q, down_q [dev] out; up_bs, down_bs [dev] out (NVFP4 only, else NULL);
  *   up_s, down_s [dev] fp32 [E] out. */

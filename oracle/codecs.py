@@ -29,7 +29,9 @@ codes from identical inputs:
                     per 16-block along K: sb = E4M3(f32(amax_b / f32(6 * S)))
                     sb == 0 -> block all zero; else r = f32(1 / f32(dec(sb) * S))
                     q = E2M1(f32(v * r));             value = dec(q) * dec(sb) * S
-  amax == 0 gives all-zero codes and a zero scale.
+  amax == 0 gives all-zero codes and a zero scale.  A reciprocal past the
+  range of float32 (of amax below 1.32e-36, or of sb * S below 2.94e-39) counts
+  as 0: zero codes, where an infinite one would make 0 * inf of every zero.
 
 Parity pins (tests/test_codecs.py): exhaustive decode tables against
 hand-written tables in tests/golden, every rounding midpoint, saturation,
@@ -151,6 +153,13 @@ def e2m1_encode(v) -> np.ndarray:
 
 
 # --------------------------------------------------------------------------- recipes
+def _over32(num: float, den) -> np.ndarray:
+    """f32(num / den) of positive float32 den, 0 where that is past float32's range."""
+    with np.errstate(over="ignore"):
+        q = (np.float32(num) / np.asarray(den, np.float32)).astype(np.float32)
+    return np.where(np.isinf(q), np.float32(0.0), q).astype(np.float32)
+
+
 def _amax32(v: np.ndarray) -> np.float32:
     return np.float32(np.max(np.abs(v))) if v.size else np.float32(0.0)
 
@@ -164,7 +173,7 @@ def fp8_quantize(v):
     if amax == 0:
         return np.zeros(v32.shape, np.uint8), np.float32(0.0)
     s = np.float32(amax / np.float32(E4M3_MAX))
-    inv = np.float32(np.float32(E4M3_MAX) / amax)
+    inv = _over32(E4M3_MAX, amax)
     prod = (v32 * inv).astype(np.float32)
     return e4m3_encode(prod), s
 
@@ -224,7 +233,7 @@ def nvfp4_quantize(v, amax=None):
     den = (sb * S).astype(np.float32)
     live = sb != 0
     r = np.zeros_like(den)
-    r[live] = (np.float32(1.0) / den[live]).astype(np.float32)
+    r[live] = _over32(1.0, den[live])
     prod = (blocks * r[..., None]).astype(np.float32)
     q = e2m1_encode(prod)
     q[~live] = 0

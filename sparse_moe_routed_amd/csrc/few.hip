@@ -53,11 +53,11 @@ __device__ __forceinline__ bf16x8 fp8_frag(uint32_t w0, uint32_t w1) {
 template <int FMT>
 struct TensorScale {
   float s = 1.f;  // value = stored * s
-  float a = 0.f;  // FP8: 448 / amax; NVFP4: 6 s
+  float a = 0.f;  // FP8: 448 / amax (0 where infinite); NVFP4: 6 s
   __device__ explicit TensorScale(float amax) {
     if constexpr (FMT == kFP8) {
       s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
-      a = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
+      a = quotient_or_zero(448.f, amax);
     } else if constexpr (FMT == kNVFP4) {
       s = amax > 0.f ? __fdiv_rn(amax, 2688.f) : 0.f;
       a = 6.f * s;
@@ -115,9 +115,10 @@ __device__ __forceinline__ u32x4 quantise8(u32x4 v, const TensorScale<FMT>& ts) 
       const uint32_t sb = ts.s > 0.f ? e4m3_encode(__fdiv_rn(fmaxf(m, mo), ts.a)) : 0u;
       const f16x2 s2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb | (sb << 8), 1.0f, false);
       const float sbf = static_cast<float>(s2[0]);
-      const float r = sbf > 0.f ? __fdiv_rn(1.f, sbf * ts.s) : 0.f;
-      // |f r| is at most 6 * (1 + 2^-4) / (1 - 2^-4) (0 for a zero scale): the
-      // hardware conversion saturates it to 6
+      const float r = quotient_or_zero(1.f, sbf * ts.s);
+      // |f r| is below 6 (1 + 2^-4) for a normal block scale and below 9 for a
+      // subnormal one, which may be two thirds of what it rounds: the hardware
+      // conversion saturates it to 6
       uint32_t q = 0u;
       q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[0] * r, f[1] * r, 1.0f, 0);
       q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[2] * r, f[3] * r, 1.0f, 1);

@@ -134,6 +134,14 @@ __device__ __forceinline__ float e2m1_decode(uint32_t c) {
   return (c & 8u) ? -mag : mag;
 }
 
+// num / den of a quantiser (num > 0, den >= 0), 0 where that is infinite: den 0,
+// or so small (amax below 1.32e-36 for FP8) that the quotient is past fp32's
+// range.  Values times 0 become code 0; times infinity a zero would be NaN.
+__device__ __forceinline__ float quotient_or_zero(float num, float den) {
+  const float q = __fdiv_rn(num, den);
+  return q <= __FLT_MAX__ ? q : 0.f;
+}
+
 // ----------------------------------------------------------------- wave helpers
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll

@@ -7,7 +7,8 @@
 //   NVFP4 S = amax / 2688 (= 6 * 448),  per 16-element block along K:
 //         sb = E4M3(amax_b / (6 * S)); sb == 0 -> zero block;
 //         r = 1 / (dec(sb) * S),  code = E2M1(v * r)
-//   amax == 0 -> zero codes and a zero scale.
+//   amax == 0 -> zero codes and a zero scale; inv or r past the range of
+//   float32 counts as 0 (zero codes).
 // The same kernels pack expert weights (one scale per expert projection) and
 // quantise activations inside the forward pass (one scale per tensor).
 #include "moe_common.h"
@@ -87,8 +88,8 @@ __global__ __launch_bounds__(FUSED ? kFusedThreads : kQThreads) void quant_fp8_k
   if constexpr (FUSED) amax = block_amax_bf16(x, n8);
   else amax = read_amax_slots(amax_p);
   if (blockIdx.x == 0 && threadIdx.x == 0) *scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
-  // amax == 0: inv = 0, every product is +-0 and every code 0
-  const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
+  // inv = 0 (amax 0 or tiny): every product is +-0 and every code 0
+  const float inv = quotient_or_zero(448.f, amax);
   for (size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8;
        i += static_cast<size_t>(gridDim.x) * blockDim.x) {
     const u32x4 v = reinterpret_cast<const u32x4*>(x)[i];
@@ -157,8 +158,8 @@ __global__ __launch_bounds__(FUSED ? kFusedThreads : kQThreads) void quant_nvfp4
       sb = e4m3_encode(__fdiv_rn(amax_b, sixS));
       sbf = e4m3_decode(sb);
     }
-    // sb == 0: r = 0, every product is +-0 and every code 0
-    const float r = sbf > 0.f ? __fdiv_rn(1.f, sbf * S) : 0.f;
+    // r = 0 (sb == 0, or sb S tiny): every product is +-0 and every code 0
+    const float r = quotient_or_zero(1.f, sbf * S);
     float t[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) t[j] = v[j] * r;
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(kQThreads) void weight_codes_kernel(
   const uint16_t* base = w + static_cast<size_t>(e) * per_expert;
   const size_t n16 = per_expert / 16;
   if (fmt == kFP8) {
-    const float inv = a > 0.f ? __fdiv_rn(448.f, a) : 0.f;
+    const float inv = quotient_or_zero(448.f, a);
     uint8_t* qe = q + static_cast<size_t>(e) * per_expert;
     for (size_t i = static_cast<size_t>(blockIdx.x) * kQThreads + threadIdx.x; i < n16;
          i += static_cast<size_t>(gridDim.x) * kQThreads) {
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(kQThreads) void weight_codes_kernel(
         const uint32_t x0 = ww < 2 ? v0[2 * ww] : v1[2 * (ww - 2)];
         const uint32_t x1 = ww < 2 ? v0[2 * ww + 1] : v1[2 * (ww - 2) + 1];
         uint32_t c[4] = {0u, 0u, 0u, 0u};
-        if (a > 0.f) {
+        if (inv > 0.f) {
           c[0] = e4m3_encode(bf16_to_f32(x0 & 0xffffu) * inv);
           c[1] = e4m3_encode(bf16_to_f32(x0 >> 16) * inv);
           c[2] = e4m3_encode(bf16_to_f32(x1 & 0xffffu) * inv);
@@ -272,8 +273,8 @@ __global__ __launch_bounds__(kQThreads) void weight_codes_kernel(
         sbf = e4m3_decode(sb);
       }
       uint32_t p0 = 0u, p1 = 0u;
-      if (sbf > 0.f) {
-        const float r = __fdiv_rn(1.f, sbf * S);
+      const float r = quotient_or_zero(1.f, sbf * S);
+      if (r > 0.f) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           p0 |= (e2m1_encode(v[2 * j] * r) | (e2m1_encode(v[2 * j + 1] * r) << 4)) << (8 * j);

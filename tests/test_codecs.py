@@ -216,3 +216,20 @@ def test_codecs_reject_non_finite():
         codecs.e4m3_encode(np.array([np.nan]))
     with pytest.raises(ValueError):
         codecs.e2m1_encode(np.array([np.inf]))
+
+
+def test_tiny_tensors_become_zero():
+    """448 / amax and 1 / (sb S) past the range of float32 count as 0: the codes
+    are zero instead of 0 * inf.  Above that the recipes hold as they are."""
+    big = np.float32(np.finfo(np.float32).max)
+    for amax in (1e-37, 1e-39, float(np.float32(448.0) / big) * 0.99):
+        q, s = codecs.fp8_quantize(np.array([amax, 0.0, -0.5 * amax]))
+        assert not q.any() and s == np.float32(np.float32(amax) / np.float32(448.0))
+    q, s = codecs.fp8_quantize(np.array([1.5e-36, 0.0, -1.5e-36]))
+    assert list(q) == [0x7E, 0, 0xFE]
+    # NVFP4: S = 2^-124, so a block scale of 2^-9 has no reciprocal and one of 448 has
+    v = np.zeros((1, 32), np.float32)
+    v[0, 0], v[0, 16], v[0, 17] = 2688 * 2.0 ** -124, 6 * 2.0 ** -133, -3 * 2.0 ** -133
+    q, sb, S = codecs.nvfp4_quantize(v)
+    assert S == np.float32(2.0 ** -124) and q[0, 0] == 7 and sb[0, 1] == 1
+    assert not q[0, 1:].any()

@@ -1197,3 +1197,31 @@ def test_forward_timed_equals_forward(full, fmt):
                     assert hip.ms(ev[st], ev[j]) >= -slack, (fmt, T, st)
                     assert hip.ms(ev[j + 1], ev[st + 1]) >= -slack, (fmt, T, st)
             hip.destroy(ev)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [2, 300])
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_activation_codes_of_tiny_tensors(fmt, rows):
+    """Tensors around the smallest amax whose scale has a reciprocal in fp32, in
+    one workgroup and in several: the oracle's codes and scale, and so for weights."""
+    rng = np.random.default_rng(rows)
+    for amax in (1e-30, 4e-33, 1e-34, 2e-36, 1.2e-36, 1e-37, 1e-39):
+        v = rng.standard_normal((rows, 256)) * rng.choice([1.0, 2.0 ** -8], (rows, 256))
+        v[:, ::7] = 0.0
+        x = torch.from_numpy(v / np.abs(v).max() * amax).float().bfloat16()
+        codes, bs, s = moe.quantize_activation(x.cuda(), fmt)
+        if fmt == "fp8":
+            q, s_o = codecs.fp8_quantize(x.float().numpy())
+        else:
+            q, sb, s_o = codecs.nvfp4_quantize(x.float().numpy())
+            q = codecs.nvfp4_pack(q)
+            assert np.array_equal(bs.cpu().numpy(), sb), amax
+        print(f"{fmt} rows {rows} amax {amax}: {(codes.cpu().numpy() != q).mean():.3f} differ", flush=True)
+        assert np.array_equal(codes.cpu().numpy(), q) and s.item() == s_o, amax
+        if rows == 300 and fmt == "fp8":
+            w = x[:192].unsqueeze(0)
+            bank = moe.quantize_experts(w.cuda(), w.transpose(1, 2).contiguous().cuda(), fmt,
+                                        moe.LayerDims(256, 192, 1, 1))
+            q, s_o = codecs.fp8_quantize(w[0].float().numpy())
+            assert np.array_equal(bank.up[0].cpu().numpy(), q) and bank.up_s.item() == s_o, amax

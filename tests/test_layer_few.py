@@ -309,3 +309,29 @@ def test_both_ways_captured(fmt, T):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, ids, gates), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 16])
+@pytest.mark.parametrize("fmt,e", [("fp8", -62), ("fp8", -67), ("nvfp4", -58), ("nvfp4", -59)])
+def test_tiny_intermediate(fmt, e, T):
+    """Tokens of about 2^e, so that the intermediate (about 2^2e; a block of it
+    2^-16 of that) has a scale whose reciprocal is past the range of fp32: it
+    counts as zero, in both ways alike, and y is finite."""
+    L = layer(SMALL)
+    up = L.up.clone()
+    up[:, 16:32] *= 2.0 ** -8
+    dev = moe.quantize_experts(up.cuda(), L.down_d, fmt, L.ld)
+    x = (synth.make_tokens(T, SMALL).float() * 2.0 ** e).bfloat16()
+    y, ids, gates = moe.layer_few(x.cuda(), L.router, dev, L.ld)
+    i2, g2 = moe.route(x.cuda(), L.router, L.ld)
+    assert torch.equal(ids, i2)
+    y2 = moe.forward(x.cuda(), i2, g2, dev, L.ld)
+    bank = om.ExpertBank(up, L.down, fmt).preload(np.unique(ids.cpu().numpy()), threads=8)
+    ref, a = om.forward(x.float().numpy(), ids.cpu().numpy(), gates.double().cpu().numpy(), bank, return_a=True)
+    rms = np.sqrt(np.mean(ref ** 2))
+    print(f"{fmt} 2^{e} T={T}: amax of a {a.max():.2e} rms of y {rms:.2e} NaN {int(y.isnan().sum())}", flush=True)
+    # the product of the intermediate's and the weights' scale is subnormal, with
+    # 10 bits and more: inside TOL
+    assert np.abs(y.double().cpu().numpy() - ref).max() <= TOL[fmt] * rms
+    assert np.abs(y2.double().cpu().numpy() - ref).max() <= TOL[fmt] * rms
