@@ -413,9 +413,10 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  * NULL, with the codes in the workspace past that.  K % 16 == 0
  * (MOE_EUNSUPPORTED otherwise), any N, M from 0 (a no-op) to 1 << 20, N and K up
  * to 1 << 20; x, y, w and codes 16-byte aligned, scales 4-byte; ws 256-byte
- * aligned, ws_bytes >= moe_block_linear_workspace_size(M, K).  A NaN or infinity becomes a NaN code;
- * a NaN code (0x7f, 0xff) spreads to the row or column of y that reads it and no
- * further. */
+ * aligned, ws_bytes >= moe_block_linear_workspace_size(M, K).  A NaN or
+ * infinity becomes a NaN code (of a weight it is no part of its block's amax; a
+ * row of x with an infinity has an infinite scale); a NaN code (0x7f, 0xff)
+ * spreads to the row or column of y that reads it and no further. */
 #define MOE_BLOCK_FEW_ROWS 32
 int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales, void* stream);
 size_t moe_block_packed_size(int32_t N, int32_t K);

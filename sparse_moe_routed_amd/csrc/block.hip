@@ -56,6 +56,17 @@ __device__ __forceinline__ size_t packed_at(int n, int k, int kb_n) {
          ((in >> 5) * 16 + (n & 15)) * 16 + (k & 15);
 }
 
+// bf16 pairs with infinities turned into NaN: a NaN is no part of a block's
+// amax, so the block's other values keep their codes
+__device__ __forceinline__ u32x4 inf_to_nan(u32x4 v) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if ((v[w] & 0x7fffu) == 0x7f80u) v[w] |= 0x40u;
+    if ((v[w] & 0x7fff0000u) == 0x7f800000u) v[w] |= 0x400000u;
+  }
+  return v;
+}
+
 // ---- weights: a workgroup per 128 x 128 block; rows of 16 lanes
 __global__ __launch_bounds__(kQThreads) void block_pack_kernel(const uint16_t* __restrict__ w, int N,
                                                                int K, uint8_t* __restrict__ codes,
@@ -72,7 +83,7 @@ __global__ __launch_bounds__(kQThreads) void block_pack_kernel(const uint16_t* _
   for (int j = 0; j < 8; ++j) {
     const int n = nb * 128 + r0 + 16 * j;
     v[j] = u32x4{0u, 0u, 0u, 0u};
-    if (n < N && k < K) v[j] = *reinterpret_cast<const u32x4*>(src + static_cast<size_t>(n) * K + k);
+    if (n < N && k < K) v[j] = inf_to_nan(*reinterpret_cast<const u32x4*>(src + static_cast<size_t>(n) * K + k));
     m = fmaxf(m, amax8(v[j]));
   }
   m = wave_max(m);

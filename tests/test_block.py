@@ -604,3 +604,25 @@ def test_linear_captured(M):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [5, 40, 300])
+def test_infinite_weight_stays_in_its_column(M):
+    """An infinite or NaN weight makes its own row's column of y NaN; the others are
+    as with a 0 in its place, the scale of its block included."""
+    x, w = _rows(M, 144, M), _weight(130, 144, M)
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        w2, w0 = w.clone(), w.clone()
+        for n, k in ((5, 7), (9, 130), (129, 3)):
+            w2[n, k], w0[n, k] = bad, 0.0
+        V, W = moe.block_pack(w2.cuda()), moe.block_pack(w0.cuda())
+        assert torch.equal(V.scales, W.scales)
+        got, want = moe.block_linear(x.cuda(), V), moe.block_linear(x.cuda(), W)
+        cols = [n for n in range(130) if n not in (5, 9, 129)]
+        assert torch.equal(got[:, cols], want[:, cols]) and got[:, [5, 9, 129]].isnan().all()
+    # and no other value in its block
+    w2 = torch.zeros((130, 144))
+    w2[5, 7] = float("inf")
+    got = moe.block_linear(x.cuda(), moe.block_pack(w2.bfloat16().cuda()))
+    assert got[:, 5].isnan().all() and not got[:, :5].any() and not got[:, 6:].any()
