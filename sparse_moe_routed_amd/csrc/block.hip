@@ -307,8 +307,10 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
   // 16 rows of 128 bytes: chunk x of row r lies at x ^ (r % 8)
   const auto put = [&](int piece, u32x4 a, u32x4 b) {
     u32x4* p = reinterpret_cast<u32x4*>(mine + piece * 2048 + lr * 128 + ((ch ^ lr) << 4));
+    wave_lds_order();  // what was there has been read
     p[0] = a;
     p[64] = b;
+    wave_lds_order();
   };
   const auto get = [&](int piece) {
     const uint8_t* p = mine + piece * 2048 + c * 128;

@@ -358,8 +358,10 @@ __device__ __forceinline__ f32x4 mul_unit(const Unit<FMT>& w, const uint8_t* x, 
   } else {
     const int row = lane >> 3, r = lane & 15;
     u32x4* const put = reinterpret_cast<u32x4*>(turn + row * 128 + (((lane & 7) ^ row) << 4));
+    wave_lds_order();  // the unit before this one has been read
     put[0] = w.v[0];
     put[64] = w.v[1];  // 8 rows on, the same row % 8
+    wave_lds_order();
     const auto get = [&](int c) {
       return *reinterpret_cast<const u32x4*>(turn + r * 128 + ((c ^ (r & 7)) << 4));
     };

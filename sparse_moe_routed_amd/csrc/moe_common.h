@@ -143,6 +143,14 @@ __device__ __forceinline__ float quotient_or_zero(float num, float den) {
 }
 
 // ----------------------------------------------------------------- wave helpers
+// Between a wave's LDS accesses where lanes read what other lanes of the wave
+// wrote, or write over what they read.  The hardware keeps one wave's LDS accesses
+// in order; this keeps the compiler from moving them.  It issues nothing.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
