@@ -440,7 +440,8 @@ int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const v
  * another fixed order (a token's experts by index instead of by slot), so y
  * agrees with moe_forward's to fp32 summation order and repeats bit for bit.
  *   x [dev] bf16 [T, H]; router, experts as moe_route and moe_forward
- *   ids [dev] int32 [T, k], gates [dev] fp32 [T, k], y [dev] [T, H]: written
+ *   ids [dev] int32 [T, k], gates [dev] fp32 [T, k], y [dev] [T, H]: written;
+ *      y may be x or overlap it, as in the two calls
  *   ws [dev] workspace of ws_bytes >= moe_layer_few_workspace_size(dims, fmt, T),
  *      256-byte aligned; its contents need no initialisation
  * MOE_EUNSUPPORTED for T > MOE_FEW_TOKENS.  Errors otherwise as moe_route and

@@ -138,7 +138,9 @@ __device__ __forceinline__ u32x4 quantise8(u32x4 v, const TensorScale<FMT>& ts) 
 // 16 experts over one K slice each, its K steps dealt to the 4 waves in
 // contiguous ranges, the waves' sums added in wave order.  The others (FP8,
 // NVFP4) quantise a part of the tokens each, the tensor's amax taken by every
-// one of them.  Workgroup 0 clears the counters of the second kernel.
+// one of them; BF16 copies them where y overlaps x, since the second kernel's
+// first workgroups write y while its last ones may not have read their tokens.
+// Workgroup 0 clears the counters of the second kernel.
 constexpr int kQuantGroups = 16;
 
 template <int FMT>
@@ -150,25 +152,26 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(FewArgs g) {
   const int n_router = E / 16 * kFewSlices;
   if (blockIdx.x == 0)
     for (int j = threadIdx.x; j < kFewCounters; j += kRouterThreads) g.ctr[j] = 0u;
-  if constexpr (FMT != kBF16) {
-    if (static_cast<int>(blockIdx.x) >= n_router) {
+  if (static_cast<int>(blockIdx.x) >= n_router) {
+    const u32x4* x = reinterpret_cast<const u32x4*>(g.x);
+    const int n8 = T * H / 8;
+    float amax = 0.f;
+    if constexpr (FMT != kBF16) {
       float* part = reinterpret_cast<float*>(red);
-      const u32x4* x = reinterpret_cast<const u32x4*>(g.x);
-      const int n8 = T * H / 8;
-      float m = 0.f;
 #pragma unroll 8
-      for (int i = threadIdx.x; i < n8; i += kRouterThreads) m = fmaxf(m, amax8(x[i]));
-      m = wave_max(m);
-      if (lane == 0) part[wave] = m;
+      for (int i = threadIdx.x; i < n8; i += kRouterThreads) amax = fmaxf(amax, amax8(x[i]));
+      amax = wave_max(amax);
+      if (lane == 0) part[wave] = amax;
       __syncthreads();
-      const TensorScale<FMT> ts(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
-      const int b = static_cast<int>(blockIdx.x) - n_router;
-      if (b == 0 && threadIdx.x == 0) *g.x_scale = ts.s;
-      // pairs of chunks (a block's halves) stay together: the stride is even
-      for (int i = b * kRouterThreads + threadIdx.x; i < n8; i += kQuantGroups * kRouterThreads)
-        reinterpret_cast<u32x4*>(g.x_q)[i] = quantise8<FMT>(x[i], ts);
-      return;
+      amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
     }
+    const TensorScale<FMT> ts(amax);
+    const int b = static_cast<int>(blockIdx.x) - n_router;
+    if (b == 0 && threadIdx.x == 0) *g.x_scale = ts.s;
+    // pairs of chunks (a block's halves) stay together: the stride is even
+    for (int i = b * kRouterThreads + threadIdx.x; i < n8; i += kQuantGroups * kRouterThreads)
+      reinterpret_cast<u32x4*>(g.x_q)[i] = quantise8<FMT>(x[i], ts);
+    return;
   }
   const int eb = blockIdx.x / kFewSlices, s = blockIdx.x % kFewSlices;
   const int row = lane & 15;
@@ -840,8 +843,8 @@ size_t stage_need(int T, int H, int F) {
 template <int FMT>
 hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
   FewArgs g = a;
-  g.tokens = FMT == kBF16 ? g.x : g.x_q;
-  const int blocks = g.E / 16 * kFewSlices + (FMT == kBF16 ? 0 : kQuantGroups);
+  g.tokens = FMT == kBF16 && !g.y_over_x ? g.x : g.x_q;
+  const int blocks = g.E / 16 * kFewSlices + (g.tokens == g.x ? 0 : kQuantGroups);
   hipLaunchKernelGGL(few_router_kernel<FMT>, dim3(blocks), dim3(kRouterThreads), 0, stream, g);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;

@@ -63,6 +63,12 @@ size_t kblocks(size_t n) { return (n + 127) / 128; }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// whether the n bytes at p and the m bytes at q share any
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
+
 // The kernels move token rows, weight rows and output rows in 16-byte
 // vectors and routing entries, scales and block scales as 4-byte words.
 bool bank_aligned(const moe_experts* ex) {
@@ -929,6 +935,8 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   g.gates = gates;
   g.y = y;
   g.y_bf16 = y_dtype == MOE_Y_BF16;
+  const size_t n = static_cast<size_t>(T) * dims->hidden;
+  g.y_over_x = overlap(x, n * 2, y, n * (g.y_bf16 ? 2 : 4));
   return hip_status(moe::launch_few(experts->fmt, g, static_cast<hipStream_t>(stream)));
 }
 

@@ -190,7 +190,7 @@ struct FewArgs {
   const float *up_s, *down_s;
   float* part;     // [kFewSlices, T, E]
   uint32_t* ctr;   // [kFewCounters]
-  uint16_t* x_q;   // FP8, NVFP4: [T, H] code values (the GEMM operand)
+  uint16_t* x_q;   // [T, H] code values (FP8, NVFP4: the GEMM operand), or x's copy
   float* x_scale;  // and their tensor scale
   const uint16_t* tokens;  // x or x_q (set by the launch)
   uint16_t* act;   // [T * k, F]
@@ -198,6 +198,7 @@ struct FewArgs {
   float* gates;
   void* y;
   int y_bf16;
+  int y_over_x;    // y overlaps x
   int stage_rows;  // rows of a that the LDS stage holds (set by the launch)
 };
 bool few_pays(int fmt, int T, int H, int F, int k);

@@ -335,3 +335,25 @@ def test_tiny_intermediate(fmt, e, T):
     # 10 bits and more: inside TOL
     assert np.abs(y.double().cpu().numpy() - ref).max() <= TOL[fmt] * rms
     assert np.abs(y2.double().cpu().numpy() - ref).max() <= TOL[fmt] * rms
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("T", [1, 5, 12, 16])
+def test_output_over_the_tokens(fmt, T):
+    """y in place of x, and fp32 y whose first or last half is x: the bits of a
+    call with buffers apart, every time."""
+    L = layer(FULL)
+    bank, n = L.bank(fmt), T * 2688
+    x = synth.make_tokens(T, FULL).cuda()
+    want = {t: moe.layer_few(x, L.router, bank, L.ld, y_dtype=t)[0] for t in (torch.bfloat16, torch.float32)}
+    for _ in range(5):
+        a = x.clone()
+        y, ids, gates = moe.layer_few(a, L.router, bank, L.ld, y=a, y_dtype=torch.bfloat16)
+        assert y is a and torch.equal(a, want[torch.bfloat16])
+        for at in (0, n):
+            store = torch.empty(n, device="cuda")
+            a = store.view(torch.bfloat16)[at:at + n].view(T, 2688)
+            a.copy_(x)
+            moe.layer_few(a, L.router, bank, L.ld, y=store.view(T, 2688))
+            assert torch.equal(store.view(T, 2688), want[torch.float32])
