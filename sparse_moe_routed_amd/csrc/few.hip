@@ -20,7 +20,9 @@
 // down projection's column tiles.  A down item waits until every up round is
 // done.  The wait ends: tickets are handed out in order, so all up rounds
 // belong to workgroups that are running, and none of those waits before its
-// round is done, however few workgroups the GPU runs at a time.
+// round is done, however few workgroups the GPU runs at a time.  It is bounded
+// all the same: if another call wrote to the workspace meanwhile, which the header
+// forbids, tickets and done words are lost, and y is NaN instead of a hang.
 //
 // Weights go from HBM straight into registers in MFMA operand order.  The
 // matrix instruction takes 16 weight rows x 16 tokens: with at most 16 tokens
@@ -40,6 +42,7 @@ constexpr int kThreads = kWaves * kWave;
 constexpr int kTok = kFewTokens;        // MFMA columns
 constexpr int kMaxRows = kTok * 8;      // (token, slot) pairs
 constexpr int kRouterThreads = 256;
+constexpr int kMaxPolls = 1 << 22;      // some seconds; an up projection takes milliseconds at most
 
 __device__ __forceinline__ bf16x8 fp8_frag(uint32_t w0, uint32_t w1) {
   const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
@@ -620,7 +623,7 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
   // before it are joined.  A last round may hold fewer than n tiles, down to
   // 5/8: idle waves cost less there than one more round.
   const uint8_t* const col = stage + min(c, T - 1) * 16;
-  while (ticket < up_items) {
+  while (static_cast<uint32_t>(ticket) < static_cast<uint32_t>(up_items)) {
     float local = 0.f;
     // (up_tiles * up_items < 2^31: at most 128 experts, 256 items, F < 2^16)
     const int t1 = static_cast<int>(static_cast<uint32_t>(up_tiles * (ticket + 1)) / static_cast<uint32_t>(up_items));
@@ -716,6 +719,7 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
   const int stride = cF * 16 + 16;  // LDS row of a: padded against bank conflicts
   const int U = units_of<FMT>(F);
   bool ready = false;
+  bool late = false;  // wave 0: the wait was given up
   TensorScale<FMT> ts(0.f);
   for (int item = blockIdx.x; item < H / 16; item += groups) {
     const int n0 = item * 16;
@@ -749,14 +753,17 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
         // every up item is done; the largest a gives the tensor scale
         if (wave == 0) {
           float amax = 0.f;
-          for (int i = lane; i < up_items; i += kWave) {
+          for (int i = lane; i < up_items && !late; i += kWave) {
             uint32_t v;
+            int polls = 0;
             while (!((v = __hip_atomic_load(&g.ctr[kFewDone + i], __ATOMIC_RELAXED,
-                                            __HIP_MEMORY_SCOPE_AGENT)) & kFewDoneBit))
+                                            __HIP_MEMORY_SCOPE_AGENT)) & kFewDoneBit) && ++polls < kMaxPolls)
               __builtin_amdgcn_s_sleep(4);
+            late = polls == kMaxPolls;
             amax = fmaxf(amax, __uint_as_float(v & ~kFewDoneBit));
           }
           amax = wave_max(amax);
+          late = __any(late);
           // what the other workgroups stored is read from memory from here on
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
           if (lane == 0) sm.wave_part[0] = amax;
@@ -812,6 +819,7 @@ __global__ __launch_bounds__(kThreads) void few_layer_kernel(FewArgs g) {
     if (wave == 0 && c < T) {
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) tot += *part_of(w);
+      if (late) tot = f32x4{NAN, NAN, NAN, NAN};
       const size_t at = static_cast<size_t>(c) * H + n0 + 4 * q;
       if (g.y_bf16) {
         const uint32_t lo = f32_to_bf16(tot[0]) | (static_cast<uint32_t>(f32_to_bf16(tot[1])) << 16);
