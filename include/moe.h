@@ -407,7 +407,7 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  *   y        [dev] bf16 [M, N], written in full
  * moe_block_pack quantises and packs a weight (once), moe_block_pack_codes packs
  * the row-major codes [N, K] of a checkpoint whose block scales are used as they
- * are (packed must not be codes); moe_block_quantize quantises activations;
+ * are; moe_block_quantize quantises activations;
  * moe_block_linear is moe_block_quantize followed by moe_block_matmul: in one
  * kernel up to MOE_BLOCK_FEW_ROWS rows, where no workspace is used and ws may be
  * NULL, with the codes in the workspace past that.  K % 16 == 0
@@ -416,7 +416,8 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  * aligned, ws_bytes >= moe_block_linear_workspace_size(M, K).  A NaN or
  * infinity becomes a NaN code (of a weight it is no part of its block's amax; a
  * row of x with an infinity has an infinite scale); a NaN code (0x7f, 0xff)
- * spreads to the row or column of y that reads it and no further. */
+ * spreads to the row or column of y that reads it and no further.  No output, and
+ * not the workspace, may lie over another buffer of the call (MOE_EINVAL). */
 #define MOE_BLOCK_FEW_ROWS 32
 int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales, void* stream);
 size_t moe_block_packed_size(int32_t N, int32_t K);
@@ -467,10 +468,10 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
  *         MOE_GATE_NONE
  *   post_weight, pre_weight  [dev] fp32 [H], NULL: no weight
  *   x_out [dev] bf16 [T, H]: x', may be x itself (in place)
- *   out   [dev] bf16 [T, H], or NULL: no pre-norm (after the last block); must
- *         not be x, x_out or y
+ *   out   [dev] bf16 [T, H], or NULL: no pre-norm (after the last block)
  *   scale any float; eps >= 0 and finite; post_norm 0 or 1
- * Any H from 1 to 49152 (MOE_EUNSUPPORTED above), and pointers aligned to
+ * x_out, unless it is x, lies over no input and out over no other buffer
+ * (MOE_EINVAL).  Any H from 1 to 49152 (MOE_EUNSUPPORTED above), and pointers aligned to
  * their elements only.  A row depends on nothing but itself: rows with
  * infinities or NaN leave the others as they are. */
 typedef enum {

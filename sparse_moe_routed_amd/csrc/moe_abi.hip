@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <limits>
 #include <mutex>
 
@@ -63,10 +64,22 @@ size_t kblocks(size_t n) { return (n + 127) / 128; }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// whether the n bytes at p and the m bytes at q share any
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + m && b < a + n;
+// a buffer's bytes; those of a null pointer are none
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+
+bool overlap(Bytes u, Bytes v) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(u.p), b = reinterpret_cast<uintptr_t>(v.p);
+  return u.p && v.p && a < b + v.n && b < a + u.n;
+}
+
+// whether an output lies over any of the call's other buffers
+bool overlaps_any(Bytes out, std::initializer_list<Bytes> others) {
+  for (const Bytes& o : others)
+    if (overlap(out, o)) return true;
+  return false;
 }
 
 // The kernels move token rows, weight rows and output rows in 16-byte
@@ -860,6 +873,15 @@ int32_t moe_residual_norm(int32_t T, int32_t H, const void* x, const void* y, in
   if (!aligned(x, 2) || !aligned(y, y_dtype == MOE_Y_F32 ? 4 : 2) || !aligned(gate, 4) ||
       !aligned(post_weight, 4) || !aligned(pre_weight, 4) || !aligned(x_out, 2) || !aligned(out, 2))
     return MOE_EINVAL;
+  // rows go to workgroups in any order; a row's own x may be replaced
+  const size_t values = static_cast<size_t>(T) * H, width = static_cast<size_t>(H) * 4;
+  const size_t gates = gate_kind == MOE_GATE_TOKEN ? static_cast<size_t>(T) * 4
+                       : gate_kind == MOE_GATE_CHANNEL ? width : values * 4;
+  const Bytes bx{x, values * 2}, by{y, values * (y_dtype == MOE_Y_F32 ? 4 : 2)};
+  const Bytes bg{gate_kind == MOE_GATE_NONE ? nullptr : gate, gates};
+  const Bytes bpost{post_weight, width}, bpre{pre_weight, width}, bxo{x_out, values * 2};
+  if (overlaps_any(bxo, {by, bg, bpost, bpre}) || (x_out != x && overlap(bxo, bx))) return MOE_EINVAL;
+  if (overlaps_any({out, values * 2}, {bx, bxo, by, bg, bpost, bpre})) return MOE_EINVAL;
   moe::ResidualNormArgs a{};
   a.T = T;
   a.H = H;
@@ -936,7 +958,7 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   g.y = y;
   g.y_bf16 = y_dtype == MOE_Y_BF16;
   const size_t n = static_cast<size_t>(T) * dims->hidden;
-  g.y_over_x = overlap(x, n * 2, y, n * (g.y_bf16 ? 2 : 4));
+  g.y_over_x = overlap({x, n * 2}, {y, n * (g.y_bf16 ? 2 : 4)});
   return hip_status(moe::launch_few(experts->fmt, g, static_cast<hipStream_t>(stream)));
 }
 
@@ -945,6 +967,8 @@ int32_t moe_block_pack(int32_t N, int32_t K, const void* w, void* codes, float* 
   if (const moe_status cs = block_dims_check(0, N, K)) return cs;
   if (!w || !codes || !scales) return MOE_EINVAL;
   if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
+  const Bytes from{w, static_cast<size_t>(N) * K * 2}, to{codes, expert_code_bytes(kFP8Block, N, K)};
+  if (overlap(to, from) || overlaps_any({scales, kblocks(N) * kblocks(K) * 4}, {from, to})) return MOE_EINVAL;
   return hip_status(moe::launch_block_pack(static_cast<const uint16_t*>(w), 1, N, K,
                                            static_cast<uint8_t*>(codes), scales,
                                            static_cast<hipStream_t>(stream)));
@@ -957,8 +981,10 @@ size_t moe_block_packed_size(int32_t N, int32_t K) {
 
 int32_t moe_block_pack_codes(int32_t N, int32_t K, const void* codes, void* packed, void* stream) {
   if (const moe_status cs = block_dims_check(0, N, K)) return cs;
-  if (!codes || !packed || codes == packed) return MOE_EINVAL;
+  if (!codes || !packed) return MOE_EINVAL;
   if (!aligned(codes, 16) || !aligned(packed, 16)) return MOE_EINVAL;
+  if (overlap({codes, static_cast<size_t>(N) * K}, {packed, expert_code_bytes(kFP8Block, N, K)}))
+    return MOE_EINVAL;
   return hip_status(moe::launch_block_pack_codes(static_cast<const uint8_t*>(codes), N, K,
                                                  static_cast<uint8_t*>(packed),
                                                  static_cast<hipStream_t>(stream)));
@@ -970,6 +996,9 @@ int32_t moe_block_quantize(int32_t M, int32_t K, const void* x, void* codes, flo
   if (M == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
+  const size_t values = static_cast<size_t>(M) * K;
+  const Bytes from{x, values * 2}, to{codes, values};
+  if (overlap(to, from) || overlaps_any({scales, kblocks(K) * M * 4}, {from, to})) return MOE_EINVAL;
   return hip_status(moe::launch_block_quant({static_cast<const uint16_t*>(x), M, K,
                                              static_cast<uint8_t*>(codes), scales},
                                             static_cast<hipStream_t>(stream)));
@@ -982,6 +1011,11 @@ int32_t moe_block_matmul(int32_t M, int32_t N, int32_t K, const void* codes, con
   if (!codes || !scales || !w_codes || !w_scales || !y) return MOE_EINVAL;
   if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(w_codes, 16) || !aligned(w_scales, 4) ||
       !aligned(y, 16))
+    return MOE_EINVAL;
+  if (overlaps_any({y, static_cast<size_t>(M) * N * 2},
+                   {{codes, static_cast<size_t>(M) * K}, {scales, kblocks(K) * M * 4},
+                    {w_codes, expert_code_bytes(kFP8Block, N, K)},
+                    {w_scales, kblocks(N) * kblocks(K) * 4}}))
     return MOE_EINVAL;
   moe::BlockArgs g{};
   g.M = M;
@@ -1009,7 +1043,10 @@ int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const v
   if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(y, 16))
     return MOE_EINVAL;
   static_assert(moe::kBlockFewRows == MOE_BLOCK_FEW_ROWS, "the header's limit");
+  const Bytes bx{x, static_cast<size_t>(M) * K * 2}, by{y, static_cast<size_t>(M) * N * 2};
+  const Bytes bw{w_codes, expert_code_bytes(kFP8Block, N, K)}, bs{w_scales, kblocks(N) * kblocks(K) * 4};
   if (M <= moe::kBlockFewRows) {
+    if (overlaps_any(by, {bx, bw, bs})) return MOE_EINVAL;
     moe::BlockArgs g{};
     g.M = M;
     g.N = N;
@@ -1022,6 +1059,7 @@ int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const v
   }
   const BlockLinearLayout L = block_linear_layout(M, K);
   if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
+  if (overlaps_any(by, {bx, bw, bs}) || overlaps_any({ws, L.total}, {bx, by, bw, bs})) return MOE_EINVAL;
   uint8_t* codes = at<uint8_t>(ws, 0);
   float* scales = at<float>(ws, L.scales);
   const int32_t qs = moe_block_quantize(M, K, x, codes, scales, stream);

@@ -626,3 +626,26 @@ def test_infinite_weight_stays_in_its_column(M):
     w2[5, 7] = float("inf")
     got = moe.block_linear(x.cuda(), moe.block_pack(w2.bfloat16().cuda()))
     assert got[:, 5].isnan().all() and not got[:, :5].any() and not got[:, 6:].any()
+
+
+def test_overlapping_buffers_are_refused():
+    """An output over an operand would be read by one workgroup after another has
+    written it."""
+    L = moe.lib()
+    M, N, K = 40, 64, 256
+    x, c, s, w, ws, y = (FAKE + (i << 20) for i in range(6))  # 1 MiB apart
+    wb, yb = L.moe_block_packed_size(N, K), M * N * 2
+    for bad in ((x, x, s), (x, x + 2 * M * K - 16, s), (x, c, x + 4), (x, c, c + M * K - 4)):
+        assert L.moe_block_quantize(M, K, *bad, None) == moe.EINVAL, bad
+    for bad in ((x, x + 2 * N * K - 16, s), (x, c, x + 2 * N * K - 4), (x, c, c + wb - 4)):
+        assert L.moe_block_pack(N, K, *bad, None) == moe.EINVAL, bad
+    for bad in ((c, c + N * K - 16), (c + wb - 16, c)):
+        assert L.moe_block_pack_codes(N, K, *bad, None) == moe.EINVAL, bad
+    for bad in (c, c + M * K - 16, s, s + 2 * M * 4 - 16, w + wb - 16, ws, w - yb + 16):
+        assert L.moe_block_matmul(M, N, K, c, s, w, ws, bad, None) == moe.EINVAL, hex(bad)
+    need = L.moe_block_linear_workspace_size(M, K)
+    for m in (M, 4):  # the two kernels, the one
+        for bad in (x, x + 2 * m * K - 16, w + wb - 16, s):
+            assert L.moe_block_linear(m, N, K, x, w, s, bad, ws, need, None) == moe.EINVAL, hex(bad)
+    assert L.moe_block_linear(M, N, K, x, w, s, ws + 256, ws, need, None) == moe.EINVAL
+    assert L.moe_block_linear(M, N, K, ws + 256, w, s, y, ws, need, None) == moe.EINVAL

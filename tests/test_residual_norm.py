@@ -191,3 +191,21 @@ def test_stream_and_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(xo, want[0]) and torch.equal(out, want[1])
+
+
+def test_overlapping_buffers_are_refused():
+    """Rows go to workgroups in any order, so an output that lies over another row's
+    input is refused; x_out may be x itself, and neighbours may touch."""
+    f = moe.lib().moe_residual_norm
+    n = 4 * 64 * 2  # bytes of a bf16 operand
+
+    def call(x=FAKE, y=FAKE + 4096, yd=1, gate=None, kind=0, post=None, pre=None, xo=FAKE, out=FAKE + 8192):
+        return f(4, 64, x, y, yd, gate, kind, post, pre, 1.0, 1e-6, 1, xo, out, None)
+
+    for bad in (dict(xo=FAKE + 2), dict(xo=FAKE + n - 2), dict(xo=FAKE - n + 2), dict(xo=FAKE + 4096 + 2),
+                dict(xo=FAKE + 4096 + 2 * n - 2), dict(out=FAKE + 128), dict(out=FAKE + 4096 + 2 * n - 2),
+                dict(xo=FAKE + 2048, out=FAKE + 2048 + n - 2), dict(y=None, xo=None, out=FAKE + 2),
+                dict(kind=1, gate=FAKE + 8192 + 4), dict(kind=2, gate=FAKE + n - 4),
+                dict(kind=3, gate=FAKE + 8192 - 2 * n + 4), dict(post=FAKE + n - 4), dict(pre=FAKE + 8192 - 252),
+                dict(yd=0, xo=FAKE + 2048, y=FAKE + 2048 + n - 2)):
+        assert call(**bad) == moe.EINVAL, bad
