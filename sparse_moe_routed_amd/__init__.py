@@ -660,6 +660,39 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torc
     return (x if y is None else x_out), out
 
 
+def _bank_part(t, name: str, device: torch.device, dtype, n_bytes: int):
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous tensor on {device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if t.numel() * t.element_size() < n_bytes:
+        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, the layer's dims need {n_bytes}")
+
+
+def _check_bank(bank: ExpertBank, dims: LayerDims, device: torch.device):
+    """The bank's tensors are on the device and hold the layer's experts: the
+    kernels read them by the dims alone."""
+    E, H, F, fmt = dims.n_experts, dims.hidden, dims.ffn, bank.fmt
+    n = E * H * F
+    if fmt == "bf16":
+        _bank_part(bank.up, "up", device, torch.bfloat16, 2 * n)
+        _bank_part(bank.down, "down", device, torch.bfloat16, 2 * n)
+        return
+    scales = 4 * E
+    up = down = n // 2 if fmt == "nvfp4" else n
+    if fmt == "fp8_block":
+        kh, kf = -(-H // 128), -(-F // 128)
+        up, down = E * (-(-F // 16) * kh) * 2048, E * (-(-H // 16) * kf) * 2048
+        scales *= kh * kf
+    _bank_part(bank.up, "up", device, None, up)
+    _bank_part(bank.down, "down", device, None, down)
+    _bank_part(bank.up_s, "up_s", device, torch.float32, scales)
+    _bank_part(bank.down_s, "down_s", device, torch.float32, scales)
+    if fmt == "nvfp4":
+        _bank_part(bank.up_bs, "up_bs", device, None, n // 16)
+        _bank_part(bank.down_bs, "down_bs", device, None, n // 16)
+
+
 FEW_TOKENS = 16  # MOE_FEW_TOKENS of include/moe.h
 
 
@@ -700,8 +733,10 @@ def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
         ws = layer_few_workspace(dims, experts.fmt, min(T, FEW_TOKENS), dev)
     else:
         _dev(ws, torch.uint8, "ws")
-    _same_device(dev, w_packed=router.w_packed, bias=router.bias, up=experts.up, down=experts.down,
-                 ids=ids, gates=gates, y=y, ws=ws)
+    if router.bias is not None:
+        _dev(router.bias, torch.float32, "bias", (dims.n_experts,))
+    _check_bank(experts, dims, dev)
+    _same_device(dev, w_packed=router.w_packed, bias=router.bias, ids=ids, gates=gates, y=y, ws=ws)
     yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}[y_dtype]
     d = dims.c()
     r = Router(router.w_packed.data_ptr(),

@@ -357,3 +357,58 @@ def test_output_over_the_tokens(fmt, T):
             a.copy_(x)
             moe.layer_few(a, L.router, bank, L.ld, y=store.view(T, 2688))
             assert torch.equal(store.view(T, 2688), want[torch.float32])
+
+
+def _bank_of(fmt, dims, device="meta"):
+    """A bank's tensors as quantize_experts lays them out, without data."""
+    E, F, H = dims.n_experts, dims.ffn, dims.hidden
+    e = lambda *shape, dtype=torch.uint8: torch.empty(shape, dtype=dtype, device=device)
+    if fmt == "bf16":
+        return moe.ExpertBank(fmt, e(E, F, H, dtype=torch.bfloat16), e(E, H, F, dtype=torch.bfloat16))
+    s = lambda *shape: e(E, *shape, dtype=torch.float32)
+    if fmt == "fp8":
+        return moe.ExpertBank(fmt, e(E, F, H), e(E, H * F), None, None, s(), s())
+    if fmt == "nvfp4":
+        return moe.ExpertBank(fmt, e(E, F * H // 2), e(E, H * F // 2), e(E, F * H // 16), e(E, H * F // 16), s(), s())
+    kh, kf = -(-H // 128), -(-F // 128)
+    return moe.ExpertBank(fmt, e(E, moe.block_packed_size(F, H)), e(E, moe.block_packed_size(H, F)), None, None,
+                          s(kf, kh), s(kh, kf))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4", "fp8_block"])
+def test_bank_of_other_dims_is_refused(fmt):
+    """Every tensor of a bank is looked at: its size against the dims, its type where
+    it is fixed, its device and layout.  (On the meta device: nothing is read.)"""
+    dims, dev = moe.LayerDims(192, 320, 16, 2), torch.device("meta")
+    good = _bank_of(fmt, dims)
+    moe._check_bank(good, dims, dev)
+    moe._check_bank(_bank_of(fmt, moe.LayerDims(192, 320, 32, 2)), dims, dev)  # its first experts
+    names = [n for n in ("up", "down", "up_bs", "down_bs", "up_s", "down_s") if getattr(good, n) is not None]
+    assert len(names) == {"bf16": 2, "fp8": 4, "nvfp4": 6, "fp8_block": 4}[fmt]
+    for n in names:
+        t = getattr(good, n)
+        bad = [t[:15], None, torch.empty_like(t, device="cpu"), torch.empty((2,) + t.shape, dtype=t.dtype, device=dev)[:, :8]]
+        if t.dtype != torch.uint8:
+            bad += [t.to(torch.float64)]
+        for b in bad:
+            bank = _bank_of(fmt, dims)
+            setattr(bank, n, b)
+            with pytest.raises(ValueError, match=n):
+                moe._check_bank(bank, dims, dev)
+    for other in (moe.LayerDims(256, 320, 16, 2), moe.LayerDims(192, 384, 16, 2), moe.LayerDims(192, 320, 32, 2)):
+        with pytest.raises(ValueError):
+            moe._check_bank(good, other, dev)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4", "fp8_block"])
+def test_wrong_banks_and_biases_are_refused(fmt):
+    """The call itself: refused on the host, nothing is launched."""
+    L = layer(SMALL)
+    x = synth.make_tokens(3, SMALL).cuda()
+    small = _bank_of(fmt, moe.LayerDims(256, 192, 16, 4), "cuda")
+    with pytest.raises(ValueError, match="up"):
+        moe.layer_few(x, L.router, small, L.ld)
+    for bias in (L.router.bias[:16], L.router.bias.double(), L.router.bias.cpu()):
+        with pytest.raises(ValueError, match="bias"):
+            moe.layer_few(x, moe.PackedRouter(L.router.w_packed, bias), L.bank(fmt), L.ld)
