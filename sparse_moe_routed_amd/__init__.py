@@ -183,7 +183,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev(t: torch.Tensor, dtype, name: str, shape=None):
@@ -226,6 +226,34 @@ class ExpertBank:
                        self.down_bs.data_ptr() if self.down_bs is not None else None,
                        self.up_s.data_ptr() if self.up_s is not None else None,
                        self.down_s.data_ptr() if self.down_s is not None else None)
+
+
+@functools.lru_cache(maxsize=256)
+def _bank_parts(fmt: str, E: int, H: int, F: int):
+    """(field, dtype or None, bytes) of a bank's tensors."""
+    n, code, scale = E * H * F, None, torch.float32
+    if fmt == "bf16":
+        return ("up", torch.bfloat16, 2 * n), ("down", torch.bfloat16, 2 * n)
+    if fmt == "fp8":
+        return ("up", code, n), ("down", code, n), ("up_s", scale, 4 * E), ("down_s", scale, 4 * E)
+    if fmt == "nvfp4":
+        return (("up", code, n // 2), ("down", code, n // 2), ("up_s", scale, 4 * E), ("down_s", scale, 4 * E),
+                ("up_bs", code, n // 16), ("down_bs", code, n // 16))
+    kh, kf = -(-H // 128), -(-F // 128)
+    return (("up", code, E * -(-F // 16) * kh * 2048), ("down", code, E * -(-H // 16) * kf * 2048),
+            ("up_s", scale, 4 * E * kh * kf), ("down_s", scale, 4 * E * kh * kf))
+
+
+def _check_bank(bank: ExpertBank, dims: LayerDims, device: torch.device):
+    """The bank's tensors are on the device and hold the layer's experts: the
+    kernels read them by the dims alone."""
+    for name, dtype, n in _bank_parts(bank.fmt, dims.n_experts, dims.hidden, dims.ffn):
+        t = getattr(bank, name)
+        if not (isinstance(t, torch.Tensor) and t.nbytes >= n and t.device == device and t.is_contiguous() and
+                (dtype is None or t.dtype is dtype)):
+            what = "None" if t is None else f"{tuple(t.shape)} {t.dtype} on {t.device}"
+            raise ValueError(f"{name}: {what}; {dims} needs a contiguous {dtype or 'byte'} tensor of {n} bytes "
+                             f"or more on {device}")
 
 
 def abi_version() -> int:
@@ -281,6 +309,8 @@ def route(x: torch.Tensor, router: PackedRouter, dims: LayerDims = LayerDims(),
     T = x.shape[0]
     _dev(x, torch.bfloat16, "x", (T, dims.hidden))
     _dev(router.w_packed, torch.bfloat16, "w_packed", (3, dims.n_experts, dims.hidden))
+    if router.bias is not None:
+        _dev(router.bias, torch.float32, "bias", (dims.n_experts,))
     if ids is None:
         ids = torch.empty((T, dims.top_k), dtype=torch.int32, device=x.device)
     if gates is None:
@@ -312,6 +342,7 @@ def forward(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, experts: Ex
     if y is None:
         y = torch.empty((T, dims.hidden), dtype=y_dtype, device=x.device)
     _dev(y, y_dtype, "y", (T, dims.hidden))
+    _check_bank(experts, dims, x.device)
     yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}[y_dtype]
     d = dims.c()
     e = experts.c()
@@ -349,6 +380,7 @@ def shared_forward(x: torch.Tensor, expert: ExpertBank, dims: LayerDims,
     if ws is None:
         ws = shared_workspace(dims, expert.fmt, T, x.device)
     _dev(ws, torch.uint8, "ws")
+    _check_bank(expert, dims, x.device)
     yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}[y_dtype]
     d = dims.c()
     e = expert.c()
@@ -373,6 +405,7 @@ def forward_noalloc(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, exp
     if y is None:
         y = torch.empty((T, dims.hidden), dtype=y_dtype, device=x.device)
     _dev(y, y_dtype, "y", (T, dims.hidden))
+    _check_bank(experts, dims, x.device)
     yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}[y_dtype]
     d = dims.c()
     e = experts.c()
@@ -403,6 +436,7 @@ def forward_timed(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, exper
     _dev(gates, torch.float32, "gates", (T, dims.top_k))
     _dev(ws, torch.uint8, "ws")
     _dev(y, y_dtype, "y", (T, dims.hidden))
+    _check_bank(experts, dims, x.device)
     yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}[y_dtype]
     arr = (ctypes.c_void_p * len(events))(*[ctypes.c_void_p(e) for e in events])
     d = dims.c()
@@ -419,6 +453,7 @@ class ExpertCache:
     Per-expert scales stay on the device."""
 
     def __init__(self, bank: ExpertBank, n_slots: int, dims: LayerDims = LayerDims()):
+        _check_bank(bank, dims, bank.up.device)
         dev = bank.up.device
 
         def host(t):
@@ -461,6 +496,8 @@ def forward_cached(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, cach
                    ws: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
     """moe_forward_cached: (y [T, H], stats dict); y equals forward() on the
     bank the cache was built from."""
+    if dims != cache.dims:
+        raise ValueError(f"dims: {dims}, the cache was built for {cache.dims}")
     T = x.shape[0]
     _dev(x, torch.bfloat16, "x", (T, dims.hidden))
     _dev(ids, torch.int32, "ids", (T, dims.top_k))
@@ -660,39 +697,6 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor], out: Optional[torc
     return (x if y is None else x_out), out
 
 
-def _bank_part(t, name: str, device: torch.device, dtype, n_bytes: int):
-    if not (isinstance(t, torch.Tensor) and t.device == device and t.is_contiguous()):
-        raise ValueError(f"{name}: expected a contiguous tensor on {device}")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if t.numel() * t.element_size() < n_bytes:
-        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, the layer's dims need {n_bytes}")
-
-
-def _check_bank(bank: ExpertBank, dims: LayerDims, device: torch.device):
-    """The bank's tensors are on the device and hold the layer's experts: the
-    kernels read them by the dims alone."""
-    E, H, F, fmt = dims.n_experts, dims.hidden, dims.ffn, bank.fmt
-    n = E * H * F
-    if fmt == "bf16":
-        _bank_part(bank.up, "up", device, torch.bfloat16, 2 * n)
-        _bank_part(bank.down, "down", device, torch.bfloat16, 2 * n)
-        return
-    scales = 4 * E
-    up = down = n // 2 if fmt == "nvfp4" else n
-    if fmt == "fp8_block":
-        kh, kf = -(-H // 128), -(-F // 128)
-        up, down = E * (-(-F // 16) * kh) * 2048, E * (-(-H // 16) * kf) * 2048
-        scales *= kh * kf
-    _bank_part(bank.up, "up", device, None, up)
-    _bank_part(bank.down, "down", device, None, down)
-    _bank_part(bank.up_s, "up_s", device, torch.float32, scales)
-    _bank_part(bank.down_s, "down_s", device, torch.float32, scales)
-    if fmt == "nvfp4":
-        _bank_part(bank.up_bs, "up_bs", device, None, n // 16)
-        _bank_part(bank.down_bs, "down_bs", device, None, n // 16)
-
-
 FEW_TOKENS = 16  # MOE_FEW_TOKENS of include/moe.h
 
 
@@ -716,28 +720,27 @@ def layer_few(x: torch.Tensor, router: PackedRouter, experts: ExpertBank,
         raise ValueError("x: expected a [T, H] tensor")
     T, dev = x.shape[0], x.device
     _dev(x, torch.bfloat16, "x", (T, dims.hidden))
-    _dev(router.w_packed, torch.bfloat16, "w_packed", (3, dims.n_experts, dims.hidden))
+    _arg(router.w_packed, torch.bfloat16, "w_packed", (3, dims.n_experts, dims.hidden), dev)
+    if router.bias is not None:
+        _arg(router.bias, torch.float32, "bias", (dims.n_experts,), dev)
+    _check_bank(experts, dims, dev)
     if ids is None:
         ids = torch.empty((T, dims.top_k), dtype=torch.int32, device=dev)
     else:
-        _dev(ids, torch.int32, "ids", (T, dims.top_k))
+        _arg(ids, torch.int32, "ids", (T, dims.top_k), dev)
     if gates is None:
         gates = torch.empty((T, dims.top_k), dtype=torch.float32, device=dev)
     else:
-        _dev(gates, torch.float32, "gates", (T, dims.top_k))
+        _arg(gates, torch.float32, "gates", (T, dims.top_k), dev)
     if y is None:
         y = torch.empty((T, dims.hidden), dtype=y_dtype, device=dev)
     else:
-        _dev(y, y_dtype, "y", (T, dims.hidden))
+        _arg(y, y_dtype, "y", (T, dims.hidden), dev)
     if ws is None:
         ws = layer_few_workspace(dims, experts.fmt, min(T, FEW_TOKENS), dev)
     else:
-        _dev(ws, torch.uint8, "ws")
-    if router.bias is not None:
-        _dev(router.bias, torch.float32, "bias", (dims.n_experts,))
-    _check_bank(experts, dims, dev)
-    _same_device(dev, w_packed=router.w_packed, bias=router.bias, ids=ids, gates=gates, y=y, ws=ws)
-    yd = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}[y_dtype]
+        _arg(ws, torch.uint8, "ws", getattr(ws, "shape", None), dev)
+    yd = _Y_DTYPES[y_dtype]
     d = dims.c()
     r = Router(router.w_packed.data_ptr(),
                router.bias.data_ptr() if router.bias is not None else None)

@@ -1225,3 +1225,29 @@ def test_activation_codes_of_tiny_tensors(fmt, rows):
                                         moe.LayerDims(256, 192, 1, 1))
             q, s_o = codecs.fp8_quantize(w[0].float().numpy())
             assert np.array_equal(bank.up[0].cpu().numpy(), q) and bank.up_s.item() == s_o, amax
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4", "fp8_block"])
+def test_banks_of_other_dims_are_refused(small, fmt):
+    """Every call that takes a bank, a cache or a router's bias compares it with the
+    dims before a kernel reads it; on the host, nothing is launched."""
+    d, ld = small.dims, _ld(small.dims)
+    x = _x(3, d).cuda()
+    bank = small.bank(fmt)
+    ids, gates = moe.route(x, small.router, ld)
+    few = moe.LayerDims(ld.hidden, ld.ffn, ld.n_experts // 2, ld.top_k)
+    other = moe.quantize_experts(small.up_d[:few.n_experts].contiguous(), small.down_d[:few.n_experts].contiguous(),
+                                 fmt, few)
+    sd = moe.shared_dims(ld.hidden, 2 * ld.ffn)
+    one = moe.quantize_experts(small.up_d[:1].contiguous(), small.down_d[:1].contiguous(), fmt,
+                               moe.shared_dims(ld.hidden, ld.ffn))
+    events = [0] * (moe.N_STAGES + 1)
+    for call in (lambda: moe.forward(x, ids, gates, other, ld), lambda: moe.forward_noalloc(x, ids, gates, other, ld),
+                 lambda: moe.forward_timed(x, ids, gates, other, events, ld), lambda: moe.ExpertCache(other, 16, ld),
+                 lambda: moe.shared_forward(x, one, sd),
+                 lambda: moe.forward_cached(x, ids, gates, moe.ExpertCache(bank, 16, ld), few),
+                 lambda: moe.route(x, moe.PackedRouter(small.router.w_packed, small.router.bias[:8]), ld)):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.equal(moe.forward(x, ids, gates, bank, ld), moe.forward(x, ids, gates, bank, ld))
