@@ -649,3 +649,46 @@ def test_overlapping_buffers_are_refused():
             assert L.moe_block_linear(m, N, K, x, w, s, bad, ws, need, None) == moe.EINVAL, hex(bad)
     assert L.moe_block_linear(M, N, K, x, w, s, ws + 256, ws, need, None) == moe.EINVAL
     assert L.moe_block_linear(M, N, K, ws + 256, w, s, y, ws, need, None) == moe.EINVAL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 300, 2100])
+@pytest.mark.parametrize("H,F", [(256, 320), (384, 448), (192, 64)])
+def test_up_projection_sums_are_exact(T, H, F):
+    """Each K block holds one pair of products of 448 x 448 that cancel and small
+    ones that are left.  All products are whole numbers below 2^18 times one power
+    of two a token, and so are their sums: fp32 holds every partial sum exactly, so
+    the intermediate's codes and scales are known bit for bit.  A sum that drops
+    what lies some 13 bits below its largest product loses most of h."""
+    E, k = 16, 2
+    d = moe.LayerDims(H, F, E, k)
+    rng = np.random.default_rng(3 * T + H)
+    pair = np.concatenate([b + rng.permutation(min(128, H - b))[:2] for b in range(0, H, 128)]).reshape(-1, 2)
+    # codes: the weights' scale is 1.75 / 448 = 2^-8, a token's 2^p
+    w = rng.integers(-8, 9, (E, F, H)).astype(np.float32)
+    w[:, :, pair[:, 0]], w[:, :, pair[:, 1]] = 448.0, -448.0
+    v = rng.integers(-8, 9, (T, H)).astype(np.float32)
+    v[:, pair] = 448.0
+    p = rng.integers(-6, 3, (T, 1))
+    up = torch.from_numpy(w * 2.0 ** -8).bfloat16()
+    x = torch.from_numpy(v * 2.0 ** p).bfloat16()
+    q, s = codecs.fp8_block_quantize(x.float().numpy())
+    assert np.array_equal(codecs.e4m3_decode(q), v) and (s == 2.0 ** p).all()
+    down = torch.randn((E, H, F), generator=torch.Generator().manual_seed(2)).bfloat16()
+    bank = moe.quantize_experts(up.cuda(), down.cuda(), "fp8_block", d)
+    assert (bank.up_s == 2.0 ** -8).all()
+    ids = torch.from_numpy(np.stack([rng.permutation(E)[:k] for _ in range(T)])).int()
+    ws = moe.workspace(d, "fp8_block", T)
+    moe.forward(x.cuda(), ids.cuda(), torch.full((T, k), 0.5).cuda(), bank, d, ws=ws)
+    lay, R, kb = moe.workspace_layout(d, "fp8_block", T), T * k, -(-F // 128)
+    order = ws[lay["sorted_src"]:lay["sorted_src"] + R * 4].view(torch.int32).cpu().numpy()
+    e, t = ids.numpy().reshape(-1)[order], order // k
+    h = np.zeros((R, F))
+    for i in range(E):
+        h[e == i] = v[t[e == i]].astype(np.float64) @ w[i].T.astype(np.float64) * 2.0 ** (p[t[e == i]] - 8)
+    assert (np.abs(h) > 0).mean() > 0.9
+    want, sw = codecs.fp8_block_quantize(codecs.bf16_rne(np.maximum(h, 0) ** 2))
+    codes = ws[lay["act_q"]:lay["act_q"] + R * F].view(R, F).cpu().numpy()
+    at = lay["act_q"] + -(-R * F // 256) * 256
+    scales = ws[at:at + kb * R * 4].view(torch.float32).view(kb, R).cpu().numpy().T
+    assert np.array_equal(scales, sw) and np.array_equal(codes, want)
