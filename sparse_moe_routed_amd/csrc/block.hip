@@ -226,9 +226,14 @@ __device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
 
 // the operand of 16 weight rows and one K block: `at` is the lane's offset of the
 // rows' first block, kPastEnd for rows past N
+// ONCE: non-temporal, for weights that one workgroup reads (dense, up to 64 rows:
+// 3712 x 2688 from memory, M = 16 5.9 us, cached 6.2; with a second row tile M = 77
+// 9.6, cached 8.6), and for the experts' 32-row tiles, where the few weights that
+// several tiles of a popular expert share are cheaper to read again than to keep
+// (full layer, uneven use: T = 64 156.6 us, cached 178; T = 256 244 and 261).
 template <bool ONCE>
 __device__ __forceinline__ void load_weights(u32x4 (&w)[2], Buffer b, uint32_t at, uint32_t block_at) {
-  constexpr int kPolicy = ONCE ? 2 : 0;  // non-temporal where no other workgroup reads them
+  constexpr int kPolicy = ONCE ? 2 : 0;
   w[0] = __builtin_amdgcn_raw_buffer_load_b128(b, at, block_at, kPolicy);
   w[1] = __builtin_amdgcn_raw_buffer_load_b128(b, at + 1024u, block_at, kPolicy);
 }
@@ -243,7 +248,7 @@ __device__ __forceinline__ void load_weights(u32x4 (&w)[2], Buffer b, uint32_t a
 constexpr int kSmallWaves = 8;
 constexpr int kSmallN = 32;
 
-template <int G, bool QUANT>
+template <int G, bool QUANT, bool ONCE>
 __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockArgs g) {
   constexpr int kTurn = 4096, kJoin = G * 1024;
   constexpr int kRaw = QUANT ? 2 : 1;  // 16-byte loads per 16 values
@@ -280,7 +285,7 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
   const auto load = [&](Block& b, int kb) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      load_weights<true>(b.w[i], wb, wat[i], kb * 2048);
+      load_weights<ONCE>(b.w[i], wb, wat[i], kb * 2048);
     const bool in = kb * 128 + ch * 16 < K;  // a last block may be short
     const int at = (in ? kb * 128 : -ch * 16) * kRaw;  // the row's first chunk, then made zero
     const float sw = ws[kb];
@@ -786,9 +791,9 @@ hipError_t dispatch(const void* kernel, long long blocks, int threads, const Blo
   return hipLaunchKernel(kernel, grid, block, args, 0, stream);
 }
 
-template <int G, bool QUANT>
+template <int G, bool QUANT, bool ONCE = true>
 hipError_t launch_small(const BlockArgs& g, hipStream_t stream) {
-  return dispatch(reinterpret_cast<const void*>(&block_small_kernel<G, QUANT>),
+  return dispatch(reinterpret_cast<const void*>(&block_small_kernel<G, QUANT, ONCE>),
                   tiles_of(g, kBlockDense, 16 * G, kSmallN), kSmallWaves * kWave, g, stream, KernelEvents{});
 }
 
@@ -841,7 +846,8 @@ constexpr int kFill = 200;
 hipError_t launch_block_dense(const BlockArgs& g, hipStream_t stream) {
   if (g.M <= 16) return launch_small<1, false>(g, stream);
   if (g.M <= 32) return launch_small<2, false>(g, stream);
-  if (g.M <= 128) return launch_small<4, false>(g, stream);
+  if (g.M <= 64) return launch_small<4, false>(g, stream);
+  if (g.M <= 128) return launch_small<4, false, false>(g, stream);  // two row tiles
   const auto fills = [&](int bm, int bn) { return tiles_of(g, kBlockDense, bm, bn) >= kFill; };
   if (fills(256, 256)) return launch_large<kBlockDense, 256, 256, 2, 4, 4, 2>(g, stream);
   if (fills(128, 256)) return launch_large<kBlockDense, 128, 256, 1, 8, 4, 2>(g, stream);
