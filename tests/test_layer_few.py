@@ -412,3 +412,12 @@ def test_wrong_banks_and_biases_are_refused(fmt):
     for bias in (L.router.bias[:16], L.router.bias.double(), L.router.bias.cpu()):
         with pytest.raises(ValueError, match="bias"):
             moe.layer_few(x, moe.PackedRouter(L.router.w_packed, bias), L.bank(fmt), L.ld)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("T", [1, 6])
+def test_more_column_tiles_than_workgroups(fmt, T):
+    """H = 8192: 512 tiles of the down projection for 256 workgroups, two each."""
+    d = synth.Dims(hidden=8192, ffn=192, n_experts=16, top_k=3)
+    check(layer(d), fmt, synth.make_tokens(T, d))
