@@ -692,3 +692,18 @@ def test_up_projection_sums_are_exact(T, H, F):
     at = lay["act_q"] + -(-R * F // 256) * 256
     scales = ws[at:at + kb * R * 4].view(torch.float32).view(kb, R).cpu().numpy().T
     assert np.array_equal(scales, sw) and np.array_equal(codes, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [9, 300])
+def test_tokens_of_nan_leave_the_others_in_the_experts(T):
+    """ReLU takes the NaN of such a token's sums for 0: its y is 0, and the others
+    keep their bits."""
+    L = layer(SMALL)
+    x = synth.make_tokens(T, SMALL).cuda()
+    ids, gates = moe.route(x, L.router, L.ld)
+    want = moe.forward(x, ids, gates, L.bank, L.ld)
+    x[3, 7], x[4, 200], x[5] = float("nan"), float("inf"), float("-inf")
+    y = moe.forward(x, ids, gates, L.bank, L.ld)
+    keep = [t for t in range(T) if t not in (3, 4, 5)]
+    assert torch.equal(y[keep], want[keep]) and not y[3:6].any()
