@@ -174,8 +174,12 @@ int32_t moe_route(const moe_dims* dims, int32_t T, const void* x,
  *   y_t = sum_{j<k} gates[t,j] * W_down,e . a~,   a = bf16(relu(W_up,e . x~_t)^2)
  * with e = ids[t, j], x~ / a~ the activations as the weight format quantises
  * them (identity for BF16; per-tensor E4M3 for FP8; NVFP4 blocks for 4-bit;
- * E4M3 with a scale for every 128 values of a row for FP8_BLOCK), fp32
- * accumulation, slots summed in order j = 0..k-1.
+ * E4M3 with a scale for every 128 values of a row for FP8_BLOCK), slots summed
+ * in order j = 0..k-1 in fp32.  Products are summed in fp32, except those of the
+ * FP8 and FP8_BLOCK down projections: they run on the FP8 matrix instruction,
+ * which sums 64 or 128 products at a time and drops what lies some 13 bits below
+ * the largest of them; the instruction's results are summed in fp32.  FP8_BLOCK
+ * takes fewer than 0xf0000000 values of x (T * H; MOE_EUNSUPPORTED).
  *   x     [dev] bf16 [T, H]        ids [dev] int32 [T, k]    gates [dev] fp32 [T, k]
  *   y     [dev] [T, H], bf16 (MOE_Y_BF16) or fp32 (MOE_Y_F32), written in full
  *   ws    [dev] workspace of ws_bytes >= moe_workspace_size(dims, fmt, T)
@@ -392,8 +396,9 @@ int32_t moe_residual_prenorm(int32_t T, int32_t H, void* x, const float* y, void
  * where a block is 128 values of K (the last one may be shorter), its amax
  * gives s = f32(amax / 448) and codes E4M3(f32(v * f32(448 / amax))); a block
  * with amax below 2^-100 becomes zero.  Products of a block are summed by the
- * FP8 matrix instruction (relative error of a block's sum about 2e-5), blocks
- * in fp32.
+ * FP8 matrix instruction, which drops what lies some 13 bits below the largest of
+ * them (2e-5 of a block's sum on ordinary data, at most 2^-6 of its largest
+ * product), blocks in fp32.
  *   x        [dev] bf16 [M, K]          codes [dev] u8 E4M3 [M, K], row-major
  *   scales   [dev] fp32 [ceil(K/128), M]: block by block, tokens contiguous
  *   w        [dev] bf16 [N, K]

@@ -11,7 +11,9 @@
 // its 128 products with a short significand: against exact sums of E4M3 data
 // its result is off by 1.5e-5 of its own size (rms; 6e-5 where one value of a
 // row is 100 times the others), far below the bf16 rounding of y (1.7e-3), and
-// sums across blocks are fp32.
+// sums across blocks are fp32.  What it drops lies some 13 bits below the block's
+// largest product, at most 128 times: 2^-6 of that product where products cancel,
+// below the half step (2^-4) by which its own codes may be off.
 //
 // The experts' up projection is the exception: its sums become codes again, and
 // there a sum that is cut short moves a whole E4M3 step, or a block's scale.  Its
@@ -19,7 +21,7 @@
 // 16x16x32 products in fp32 take the place of the one.  Against exact sums the
 // layer's bf16 output is then off by 1.7e-3, its own rounding (with the short sums
 // 2.0e-3 to 2.9e-3).  Batches that read weights from memory do not notice (T = 5
-// 52 us, T = 64 160); at T = 4096 the up projection takes 327 us instead of 226.
+// 54 us, T = 64 157); at T = 4096 the up projection takes 341 us instead of 226.
 //
 // Weight codes are packed in operand order: for each group of 16 rows and each
 // K block 2 KB, [half h][lane l][16 bytes] = row l % 16, values 32 (l / 16) + 16 h
@@ -398,10 +400,12 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
 // banks.  The weights go straight into registers (WBUF operands per wave and
 // group, WBUF - 1 steps under way): a weight is read by the WM waves of a column
 // and no other, so LDS would only add a way, while a row serves all WN waves.
-// Where weights come from memory once (decode) the bound is HBM, 7.3 TB/s at 64
-// tokens; where they are shared, no unit is busy for more than half the time
-// (8192 x 8192 x 4096: 2.06 PFLOP/s, matrix units about 45 %), and what is left is
-// the waves' own order of LDS reads, products and multiply-adds between barriers.
+// Where weights come from memory once (decode) the bound is HBM: 64 tokens of
+// uneven use read 92 experts, 0.92 GB, in 154 us of both products, 6.0 TB/s (a plain
+// stream of reads reaches 7.1); where they are shared, no unit is busy for more than
+// half the time (8192 x 8192 x 4096: 2.06 PFLOP/s, matrix units about 45 %), and what
+// is left is the waves' own order of LDS reads, products and multiply-adds between
+// barriers.
 __device__ __forceinline__ void load16_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, at, step_at, 0, 0);
 }
@@ -813,19 +817,21 @@ hipError_t launch_large(const BlockArgs& g, hipStream_t stream, const KernelEven
 // experts, whose 128-row tiles are too few for the chip.
 int block_tile_rows(int R, int E) { return R < (16 * E > 256 ? 16 * E : 256) ? 32 : 128; }
 
-// Full layer (128 experts, 2688 -> 1856 -> 2688), whole forward, graph replay:
-// decode tiles 32 x 64 (32 x 128 where the tile makes the codes) with the weights
-// 3 steps ahead, since each is read once and from memory: T = 5 52-58 us, T = 64
-// 158.  Prefill tiles 128 x 128 in 4 waves, two workgroups or more to a CU:
-// T = 4096 573 us, T = 1024 335 (128 x 256 in 8 waves 581 and 345, 128 x 128 in 8
-// waves 607 and 344, 64 x 128 620 and 338, 256 x 256 631 and 378; column tiles
-// dealt round the XCDs 605 and 340).  There matrix unit, LDS and vector unit are
-// each busy a quarter to a third of the time and HBM runs at 3.4 TB/s: the steps'
-// latencies are what is left.
-// (These are of E4M3 products in both projections.  The up projection's in fp16
-// are bound by the matrix unit: 128 x 128 in 2 x 2 waves T = 4096 669 us, in a row of
-// 4 waves 684, 128 x 256 in 8 waves 677, 2 x 4 waves 709; tokens handed over in fp16
-// instead of codes, which is half the conversions and twice the LDS reads, 688.)
+// Full layer (128 experts, 2688 -> 1856 -> 2688), whole forward, graph replay.
+// Decode tiles 32 x 64 (32 x 128 where the tile makes the codes) with the weights
+// 3 steps ahead, since nearly each is read once and from memory: T = 5 54 us, T = 64
+// 157.  Prefill tiles 128 x 128 in 4 waves, two workgroups or more to a CU, were the
+// best with E4M3 products in both projections (T = 4096 573 us; 128 x 256 in 8 waves
+// 581, 128 x 128 in 8 607, 64 x 128 620, 256 x 256 631; column tiles dealt round the
+// XCDs 605), and still are for the down projection.  With the up projection in fp16:
+// 128 x 128 in 2 x 2 waves 669, in a row of 4 waves 684, 128 x 256 in 8 waves 677,
+// 2 x 4 waves 709; tokens handed over in fp16 instead of codes, which is half the
+// conversions and twice the LDS reads, 688.  Counters at T = 4096 say what is left:
+// the up projection (331 us, 740 TFLOP/s) has the matrix unit busy for 33 % of the
+// time and the vector unit, with the conversions of both operands in every wave,
+// for 42, at 1.7 waves per SIMD, so the two hardly overlap; LDS is busy for 10 %, HBM
+// reads 2.7 TB/s.  The down projection (255 us): matrix unit 23, vector unit 30, LDS
+// 26 %, HBM 3.2 TB/s of reads and 264 MB of rows written.
 hipError_t launch_block_experts(int stage, const BlockArgs& g, hipStream_t stream, const KernelEvents& ev) {
   if (block_tile_rows(g.M, g.E) == 32)
     return stage == 0 ? launch_large<kBlockUp, 32, 128, 1, 4, 4, 4, true>(g, stream, ev)

@@ -8,8 +8,9 @@
 // per expert at the full width) and computes next to nothing, so the bound is
 // HBM, and below it the latency of the chain router -> selection -> up ->
 // (tensor scale of a) -> down, which as separate launches costs more than the
-// weights of one token.  Full layer, T = 1 and T = 4: BF16 37 and 82 us, FP8 28
-// and 54, NVFP4 28 and 49 (as separate launches 55 and 81, 47 and 65, 43 and 54).
+// weights of one token.  Full layer, T = 1 and T = 4: BF16 36 and 81 us, FP8 28
+// and 53, NVFP4 28 and 48 (as separate launches 54 and 81, 46 and 64, 42 and 53);
+// from 4 tokens on BF16 has enough weights to read that the launches hardly count.
 // Of NVFP4's 28 us the router's kernel takes 5, the start of 256 workgroups 3, the
 // selection 4, the up projection 7, the wait for it 2, fetching a 2 and the down
 // projection 2.5; with more tokens the products stream at 5 to 5.7 TB/s.
@@ -871,9 +872,12 @@ hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
 // kernels are not slower than moe_route and moe_forward.  What they save is
 // launches, about 20 us; what they cost grows with the rows of a that every
 // workgroup stages, and for NVFP4 quantises, T k F values.  Full layer (k F =
-// 11136), us of these against the two calls: BF16 T = 1 37 (55), 8 122 (126), 12
-// 158 (160), 16 189 (182); NVFP4 T = 1 28 (43), 5 53 (54), 6 59 (57), 16 103 (84);
-// FP8 T = 1 28 (47), 8 78 (87), 16 113 (119).
+// 11136), us of these against the two calls: BF16 T = 1 36 (54), 4 81 (81), 8 104
+// (110), 12 154 (159), 16 189 (182); NVFP4 T = 1 28 (42), 5 52 (56), 6 59 (57), 16
+// 103 (84); FP8 T = 1 28 (46), 8 75 (86), 16 117 (130).  At 1024 -> 512, 64 experts,
+// top-4, they are ahead at every T in every format (17 to 34 us against 28 to 35).
+// At 2048 -> 768, 128 experts, top-8, NVFP4 T = 8 takes 41 (47), and BF16 12 74 (75)
+// but 16 96 (90): there the border, drawn at the full layer, comes 7 % late.
 bool few_pays(int fmt, int T, int H, int F, int k) {
   const size_t staged = static_cast<size_t>(T) * k * F;
   if (fmt == kFP8Block || (fmt == kBF16 && staged > 140000) || (fmt == kNVFP4 && staged > 60000)) return false;

@@ -9,7 +9,7 @@
 // HBM bound: 2 B (x) + 4 or 2 B (y) read and 2 + 2 B written per value.  A row
 // belongs to W waves and stays in their registers from the first load to the
 // last store, so both means cost no second pass over memory.  4096 rows of 2688
-// with fp32 y move 110 MB in 21.6 us, 5.1 TB/s (a large copy: 5.0 TB/s).
+// with fp32 y move 110 MB in 22 us, 5.0 TB/s (a large copy: 4.9 to 5.0 TB/s).
 #include "moe_common.h"
 #include "moe_internal.h"
 
@@ -62,7 +62,8 @@ __device__ __forceinline__ void store_chunk(uint16_t* p, int n, const uint16_t (
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = b[2 * i] | (static_cast<uint32_t>(b[2 * i + 1]) << 16);
     // streamed: the next reader is another kernel, mostly on another XCD's L2
-    // (4096 x 2688: 26.7 us, through the caches 30.8; loads gain nothing by it)
+    // (4096 x 2688, graph replay: 26.7 us, through the caches 30.8; loads gain
+    // nothing by it)
     typedef u32x4 Out __attribute__((aligned(2)));
     __builtin_nontemporal_store(o, reinterpret_cast<Out*>(p));
   } else {
@@ -191,7 +192,7 @@ hipError_t launch_rows(const ResidualNormArgs& a, hipStream_t stream) {
 // waits for one load of a kind (H = 2688, T = 1 4.2 us, 3 waves of 2 chunks 5.3,
 // one wave of 6 8.6; T = 333 7.4, 9.1, 14.4).  Many rows are bandwidth: fewer
 // waves to a row and more rows in a CU (T = 2048 13.7 us, 6 waves 17.2; T = 4096
-// 26.7 us with 4.2 of launch, 6 waves 30.3, one wave 39.2).  Wider rows alike:
+// 26.7 us by graph replay, 4.2 of them launch, 6 waves 30.3, one wave 39.2).  Wider rows alike:
 // H = 8192, T = 64 6.3 us with 16 waves (8 waves 6.9, 4 9.6), T = 4096 74 us with
 // 8 (16 waves 80.5, 4 76); H = 12288, T = 4096 106 us (6 chunks 129).
 constexpr int kFewRows = 1536;
