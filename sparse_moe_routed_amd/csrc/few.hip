@@ -22,8 +22,8 @@
 // done.  The wait ends: tickets are handed out in order, so all up rounds
 // belong to workgroups that are running, and none of those waits before its
 // round is done, however few workgroups the GPU runs at a time.  It is bounded
-// all the same: if another call wrote to the workspace meanwhile, which the header
-// forbids, tickets and done words are lost, and y is NaN instead of a hang.
+// all the same: if another call writes to the workspace meanwhile, which the header
+// forbids, done words are lost, and the columns that waited for them become NaN.
 //
 // Weights go from HBM straight into registers in MFMA operand order.  The
 // matrix instruction takes 16 weight rows x 16 tokens: with at most 16 tokens
