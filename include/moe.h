@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 8
+#define MOE_ABI_VERSION 9
 
 typedef enum {
   MOE_OK = 0,
@@ -72,8 +72,10 @@ typedef enum {
   MOE_WFMT_NVFP4 = 2, /* E2M1 codes in 16-element blocks along K, one E4M3
                          scale per block, one fp32 scale per expert
                          projection; activations quantised the same way    */
-  MOE_WFMT_FP8_BLOCK = 3 /* E4M3 codes, one fp32 scale per 128 x 128 block of
+  MOE_WFMT_FP8_BLOCK = 3, /* E4M3 codes, one fp32 scale per 128 x 128 block of
                          a weight and per 128 values of an activation row   */
+  MOE_WFMT_INT8 = 4   /* 8-bit integers, one fp32 scale per output channel (row)
+                         of a weight and per activation row; H, F <= 65536  */
 } moe_wfmt;
 
 typedef enum { MOE_Y_BF16 = 0, MOE_Y_F32 = 1 } moe_ydtype;
@@ -121,6 +123,9 @@ typedef struct {
  *          [E, ceil(F/128), ceil(H/128)], down_s fp32 [E, ceil(H/128),
  *          ceil(F/128)], a scale for each 128 x 128 block (the last ones of a
  *          row or column of blocks may be smaller)
+ *   INT8: up, down i8, each expert's [F, H] / [H, F] matrix packed as by
+ *          moe_channel_pack (moe_channel_packed_size bytes an expert); up_s fp32
+ *          [E, F], down_s fp32 [E, H], a scale for each output channel
  * Unused pointers may be NULL. */
 typedef struct {
   int32_t fmt; /* moe_wfmt */
@@ -174,12 +179,14 @@ int32_t moe_route(const moe_dims* dims, int32_t T, const void* x,
  *   y_t = sum_{j<k} gates[t,j] * W_down,e . a~,   a = bf16(relu(W_up,e . x~_t)^2)
  * with e = ids[t, j], x~ / a~ the activations as the weight format quantises
  * them (identity for BF16; per-tensor E4M3 for FP8; NVFP4 blocks for 4-bit;
- * E4M3 with a scale for every 128 values of a row for FP8_BLOCK), slots summed
- * in order j = 0..k-1 in fp32.  Products are summed in fp32, except those of the
+ * E4M3 with a scale for every 128 values of a row for FP8_BLOCK; 8-bit integers
+ * with a scale for a row for INT8), slots summed
+ * in order j = 0..k-1 in fp32.  Products are summed in fp32 (INT8: in int32,
+ * exactly), except those of the
  * FP8 and FP8_BLOCK down projections: they run on the FP8 matrix instruction,
  * which sums 64 or 128 products at a time and drops what lies some 13 bits below
  * the largest of them; the instruction's results are summed in fp32.  FP8_BLOCK
- * takes fewer than 0xf0000000 values of x (T * H; MOE_EUNSUPPORTED).
+ * and INT8 take fewer than 0xf0000000 values of x (T * H; MOE_EUNSUPPORTED).
  *   x     [dev] bf16 [T, H]        ids [dev] int32 [T, k]    gates [dev] fp32 [T, k]
  *   y     [dev] [T, H], bf16 (MOE_Y_BF16) or fp32 (MOE_Y_F32), written in full
  *   ws    [dev] workspace of ws_bytes >= moe_workspace_size(dims, fmt, T)
@@ -196,7 +203,7 @@ int32_t moe_forward(const moe_dims* dims, int32_t T, const void* x,
  * last one.  Stages: 0 permutation (histogram, prefix sum, scatter), 1 token
  * quantisation (FP8/NVFP4), 2 up projection + ReLU^2, 3 intermediate
  * quantisation (FP8/NVFP4), 4 down projection, 5 combine; FP8_BLOCK quantises
- * the tokens in stage 0 and the intermediate in stage 2.
+ * the tokens in stage 0 and the intermediate in stage 2, INT8 in 0 and 3.
  * With n_events >= 11, events[7], events[8] take the start and end of the up
  * projection kernel itself and events[9], events[10] those of the down
  * projection kernel (stamped from the kernels' dispatch packets through
@@ -266,7 +273,7 @@ int32_t moe_forward_noalloc(const moe_dims* dims, int32_t T, const void* x,
  *   host      the whole bank in host memory, layouts as moe_experts (fmt, up,
  *             down, up_bs, down_bs; pinned memory lets the uploads run as
  *             asynchronous DMA); its scale pointers are not used
- *   up_s, down_s  [dev] fp32 [E] per-expert scales (FP8/NVFP4), resident
+ *   up_s, down_s  [dev] the bank's scales (all formats but BF16), resident
  *   slot_up, slot_down        [dev] n_slots experts of codes, same
  *             per-expert layout and size as the bank
  *   slot_up_bs, slot_down_bs  [dev] NVFP4 block scales of the slots
@@ -331,10 +338,12 @@ typedef struct {
   int64_t x_q;        /* [T, H] dequantised token values without the tensor
                          scale: FP8 bf16 dec(q); NVFP4 fp16 dec(q)*dec(sb);
                          FP8_BLOCK u8 codes, fp32 scales [ceil(H/128), T]
-                         behind them at the next multiple of 256 bytes       */
+                         behind them at the next multiple of 256 bytes;
+                         INT8 i8 codes, fp32 scales [T] behind them likewise */
   int64_t act_q;      /* FP8: u8 [T*k, F] codes; NVFP4: fp16 dec(q)*dec(sb)
                          in place over act; FP8_BLOCK: u8 [T*k, F] codes,
-                         scales [ceil(F/128), T*k] behind them as for x_q    */
+                         scales [ceil(F/128), T*k] behind them as for x_q;
+                         INT8: i8 [T*k, F], scales [T*k] behind them         */
   int64_t scales;     /* fp32 [2]: x scale, act scale (FP8, NVFP4)           */
   int64_t total;      /* bytes                                               */
 } moe_ws_layout;
@@ -342,16 +351,17 @@ typedef struct {
 int32_t moe_workspace_layout(const moe_dims* dims, int32_t fmt, int32_t T,
                              moe_ws_layout* out /* [host] */);
 
-/* Pack a bf16 expert bank into FP8 or NVFP4 on the device (any expert count
+/* Pack a bf16 expert bank into FP8, NVFP4, FP8_BLOCK or INT8 on the device (any expert count
  * 1 <= E <= 256, e.g. a shared expert's one-expert bank; top_k is not used),
  * one fp32 scale per expert projection (recipes: s = f32(amax/448), code = E4M3(f32(w*f32(448/amax)))
  * for FP8 and, over each 128 x 128 block, FP8_BLOCK (scales as in moe_experts;
  * a block whose amax is below 2^-100 becomes zero); S = f32(amax/2688), block scale sb = E4M3(f32(amax_b/f32(6S))),
  * code = E2M1(f32(w*f32(1/f32(sb*S)))) for NVFP4; amax == 0 -> zero codes and
- * scale; 448/amax or 1/(sb*S) past the range of fp32 counts as 0: zero codes).  Layouts as in moe_experts.
+ * scale; 448/amax or 1/(sb*S) past the range of fp32 counts as 0: zero codes);
+ * INT8 as moe_channel_pack, over each output channel.  Layouts as in moe_experts.
  *   up_bf16 [dev] [E, F, H], down_bf16 [dev] [E, H, F]
  *   up_q, down_q [dev] out; up_bs, down_bs [dev] out (NVFP4 only, else NULL);
- *   up_s, down_s [dev] fp32 [E] out. */
+ *   up_s, down_s [dev] fp32 out, [E] or as in moe_experts. */
 int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt,
                              const void* up_bf16, const void* down_bf16,
                              void* up_q, void* down_q, uint8_t* up_bs,
@@ -361,12 +371,12 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt,
 /* Per-tensor activation quantiser of moe_forward as a standalone call (same
  * recipes as moe_quantize_experts, amax over the whole [rows, cols] tensor;
  * FP8_BLOCK: over every 128 values of a row, the last ones of a row may be
- * fewer).
+ * fewer; INT8: over every row).
  *   x [dev] bf16 [rows, cols]; codes [dev] u8 [rows, cols] (FP8) or
  *   [rows, cols/2] (NVFP4: two codes per byte as in the weights, row-major);
  *   bs [dev] u8 [rows, cols/16] (NVFP4 only, row-major); scale [dev] fp32 [1] out
- *   (FP8_BLOCK: [ceil(cols/128), rows], block by block);
- *   ws [dev] >= 256 bytes of scratch (FP8_BLOCK: not used, may be NULL). */
+ *   (FP8_BLOCK: [ceil(cols/128), rows], block by block; INT8: [rows]);
+ *   ws [dev] >= 256 bytes of scratch (FP8_BLOCK, INT8: not used, may be NULL). */
 int32_t moe_quantize_activation(int32_t fmt, int32_t rows, int32_t cols,
                                 const void* x, void* codes, uint8_t* bs,
                                 float* scale, void* ws, size_t ws_bytes,
@@ -435,10 +445,100 @@ size_t moe_block_linear_workspace_size(int32_t max_rows, int32_t K);
 int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const void* w_codes,
                          const float* w_scales, void* y, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- products in 8-bit integers with a scale per token and channel
+ * Dense products of the decoder's projections in the format of INT8 banks:
+ *   y[m, n] = round( f32( sum_k q_x[m, k] q_w[n, k] ) * s_x[m] * s_w[n] )
+ * where a row (a token of x, an output channel of w) with amax = max |v| has
+ * s = f32(amax / 127) and codes q = RNE(v * f32(127 / amax)) of the exact product
+ * (ties to even, |q| <= 127); a row with amax below 2^-100 becomes zero.  The sum is
+ * exact; the two multiplies are fp32, in the order written.
+ *   x        [dev] bf16 [M, K]          codes [dev] i8 [M, K], row-major
+ *   scales   [dev] fp32 [M]
+ *   w        [dev] bf16 [N, K]
+ *   w_codes  [dev] i8, moe_channel_packed_size(N, K) = ceil(N/16) * ceil(K/128) *
+ *            2048 bytes: the code of w[n, k] at
+ *              (n / 16 * ceil(K/128) + k / 128) * 2048 + k % 128 / 64 * 1024 +
+ *              (k % 64 / 16 * 16 + n % 16) * 16 + k % 16
+ *            and zeros past N and K: the order in which the matrix instruction
+ *            takes them, so that weights are read in contiguous runs
+ *   w_scales [dev] fp32 [N]
+ *   y        [dev] [M, N], bf16 (MOE_Y_BF16) or fp32 (MOE_Y_F32), written in full
+ * moe_channel_pack quantises and packs a weight (once), moe_channel_pack_codes packs
+ * the row-major codes [N, K] of a checkpoint (any i8 values) whose channel scales are
+ * used as they are; moe_channel_quantize quantises activations; moe_channel_linear is
+ * moe_channel_quantize followed by moe_channel_matmul, bit for bit: in one kernel up
+ * to MOE_CHANNEL_FEW_ROWS rows, where no workspace is used and ws may be NULL, with the
+ * codes in the workspace past that.  K % 16 == 0 and K <= 65536 (MOE_EUNSUPPORTED
+ * otherwise), any N up to 1 << 20, M from 0 (a no-op) to 1 << 20; x, y, w and codes
+ * 16-byte aligned, scales 4-byte; ws 256-byte aligned, ws_bytes >=
+ * moe_channel_linear_workspace_size(M, K).  A row with a NaN or an infinity has scale
+ * NaN and codes 0: its row or column of y is NaN and no other is touched.  (Experts:
+ * ReLU takes a NaN for 0, so a weight channel or token like that counts as 0 in the up
+ * projection.)  No output, and not the workspace, may lie over another buffer of the
+ * call (MOE_EINVAL). */
+#define MOE_CHANNEL_FEW_ROWS 32
+int32_t moe_channel_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales, void* stream);
+size_t moe_channel_packed_size(int32_t N, int32_t K);
+int32_t moe_channel_pack_codes(int32_t N, int32_t K, const void* codes, void* packed, void* stream);
+int32_t moe_channel_quantize(int32_t M, int32_t K, const void* x, void* codes, float* scales,
+                             void* stream);
+int32_t moe_channel_matmul(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,
+                           const void* w_codes, const float* w_scales, void* y, int32_t y_dtype,
+                           void* stream);
+size_t moe_channel_linear_workspace_size(int32_t max_rows, int32_t K);
+int32_t moe_channel_linear(int32_t M, int32_t N, int32_t K, const void* x, const void* w_codes,
+                           const float* w_scales, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* ---- products grouped by expert
+ * One projection of the experts by itself, in bf16, for rows that are sorted by
+ * expert: for experts with another activation than moe_forward's, and for training.
+ *   moe_grouped_matmul       y[r, n]      = sum_k x[r, k] w[e, n, k]
+ *   moe_grouped_input_grad   dx[r, k]     = sum_n dy[r, n] w[e, n, k]
+ *   moe_grouped_weight_grad  dw[e, n, k]  = sum_{r of e} dy[r, n] x[r, k]   (+= with
+ *                            accumulate = 1, fp32 only)
+ *   x [dev] bf16 [R, K], dy [dev] bf16 [R, N], w [dev] bf16 [E, N, K]
+ *   offsets [dev] int32 [E + 1]: rows offsets[e] .. offsets[e + 1] - 1 belong to
+ *           expert e; 0 <= offsets[0] <= ... <= offsets[E] <= R.  They are read on
+ *           the device; whatever they hold, no access leaves the buffers (bounds
+ *           outside [0, R] are taken as the nearest of them, an expert that ends
+ *           before it starts has no rows)
+ *   y [dev] [R, N], dx [dev] [R, K]: rows of an expert are written; rows of none
+ *           are left as they were (zero_rest = 0), or those from offsets[E] on set to
+ *           zero (zero_rest = 1)
+ *   dw [dev] [E, N, K]: written in full (an expert without rows gets zeros, or with
+ *           accumulate keeps its values)
+ *   *_dtype MOE_Y_BF16 or MOE_Y_F32
+ * Products are exact and summed in fp32, in an order that depends on the sizes alone:
+ * a call repeats bit for bit.  A row's result depends on that row and its expert's
+ * weights alone, an expert's dw on its rows alone: NaN and infinities spread no
+ * further.  N % 8 == K % 8 == 0, N, K <= 65536, E <= 256, R <= 1 << 23
+ * (MOE_EUNSUPPORTED otherwise); R == 0 is a no-op, but for dw, which becomes zero.
+ * Pointers 16-byte aligned, offsets 4-byte; no output may lie over an input
+ * (MOE_EINVAL).
+ * moe_group_rows sorts the rows: ids [dev] int32 [R] (the flat [T, k] of moe_route)
+ * gives offsets [dev] int32 [E + 1], sorted_src [dev] int32 [R]: the flat index of
+ * each sorted row, and inv [dev] int32 [R]: the sorted row of each flat index.  The
+ * order is stable.  An id outside [0, E) is dropped: its inv is -1, and the last rows of
+ * sorted_src (from offsets[E] on) are left as they were.  ws 256-byte aligned,
+ * ws_bytes >= moe_group_rows_workspace_size(E, R); nothing may overlap. */
+int32_t moe_grouped_matmul(int32_t R, int32_t E, int32_t N, int32_t K, const void* x, const void* w,
+                           const int32_t* offsets, void* y, int32_t y_dtype, int32_t zero_rest,
+                           void* stream);
+int32_t moe_grouped_input_grad(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy, const void* w,
+                               const int32_t* offsets, void* dx, int32_t dx_dtype, int32_t zero_rest,
+                               void* stream);
+int32_t moe_grouped_weight_grad(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy, const void* x,
+                                const int32_t* offsets, void* dw, int32_t dw_dtype, int32_t accumulate,
+                                void* stream);
+size_t moe_group_rows_workspace_size(int32_t E, int32_t max_rows);
+int32_t moe_group_rows(int32_t R, int32_t E, const int32_t* ids, int32_t* offsets, int32_t* sorted_src,
+                       int32_t* inv, void* ws, size_t ws_bytes, void* stream);
+
 /* The whole layer for a few tokens: moe_route and moe_forward of at most
  * MOE_FEW_TOKENS tokens in two kernels (decode, where the six to nine launches
  * of the two calls cost more than the weights of one token), or as the two calls
- * where those are faster or the two kernels do not apply: FP8_BLOCK banks; more
+ * where those are faster or the two kernels do not apply: FP8_BLOCK and INT8 banks; more
  * than 140000 (BF16) or 60000 (NVFP4) values in the T*k rows of the
  * intermediate; T rows of H or F + 8 bf16 values, H and F rounded up to 128,
  * beyond 120 KiB; expert matrices of 2^30 values and more.  Formulas, routing

@@ -210,6 +210,31 @@ def fp8_block_dequantize(codes, scales, rows: int = 1) -> np.ndarray:
     return e4m3_decode(codes) * s
 
 
+def int8_row_quantize(v):
+    """8-bit integer codes of rows [N, K] with one float32 scale each: s = amax / 127
+    and the integer nearest to v * float32(127 / amax), the product exact (float64
+    holds it for v of bf16), ties to even.  A row of amax below 2^-100 is zero; one
+    with a NaN or infinity has scale NaN and codes 0."""
+    v32 = np.asarray(v, dtype=np.float32)
+    codes = np.zeros(v32.shape, np.int8)
+    scales = np.zeros(v32.shape[0], np.float32)
+    for i, row in enumerate(v32):
+        if not np.isfinite(row).all():
+            scales[i] = np.nan
+            continue
+        amax = np.float32(np.abs(row).max())
+        if amax < np.float32(2.0 ** -100):
+            continue
+        inv = np.float32(np.float32(127) / amax)
+        codes[i] = np.rint(row.astype(np.float64) * np.float64(inv)).astype(np.int8)
+        scales[i] = np.float32(amax / np.float32(127))
+    return codes, scales
+
+
+def int8_row_dequantize(codes, scales) -> np.ndarray:
+    return codes.astype(np.float64) * scales.astype(np.float64)[:, None]
+
+
 def nvfp4_quantize(v, amax=None):
     """Per-tensor NVFP4 quantisation along the last axis (16-element blocks).
 

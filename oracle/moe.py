@@ -83,7 +83,7 @@ class ExpertBank:
     quantises each expert projection itself (oracle.codecs recipes)."""
 
     def __init__(self, up_bf16, down_bf16, fmt: str = "bf16"):
-        if fmt not in ("bf16", "fp8", "nvfp4", "fp8_block"):
+        if fmt not in ("bf16", "fp8", "nvfp4", "fp8_block", "int8"):
             raise ValueError(fmt)
         self.fmt = fmt
         self._up = up_bf16
@@ -105,6 +105,8 @@ class ExpertBank:
             return codecs.fp8_dequantize(q, s)
         if self.fmt == "fp8_block":
             return codecs.fp8_block_dequantize(*codecs.fp8_block_quantize(w, 128), 128)
+        if self.fmt == "int8":
+            return codecs.int8_row_dequantize(*codecs.int8_row_quantize(w))
         q, sb, S = codecs.nvfp4_quantize(w)
         return codecs.nvfp4_dequantize(q, sb, S)
 
@@ -140,7 +142,7 @@ class ExpertBank:
 def quantise_activation(v, fmt: str) -> np.ndarray:
     """The activation a projection consumes: identity for bf16, per-tensor
     fake quantisation (quantise then dequantise) for fp8 / nvfp4, by blocks of
-    128 values of a row for fp8_block."""
+    128 values of a row for fp8_block, by rows for int8."""
     v = np.asarray(v, dtype=np.float64)
     if fmt == "bf16":
         return v
@@ -152,6 +154,8 @@ def quantise_activation(v, fmt: str) -> np.ndarray:
         return codecs.nvfp4_dequantize(q, sb, S)
     if fmt == "fp8_block":
         return codecs.fp8_block_dequantize(*codecs.fp8_block_quantize(v))
+    if fmt == "int8":
+        return codecs.int8_row_dequantize(*codecs.int8_row_quantize(v))
     raise ValueError(fmt)
 
 

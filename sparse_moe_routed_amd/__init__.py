@@ -24,7 +24,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MOE_LIB") or os.path.join(_PKG, "libmoe.so")
 
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP = 0, 1, 2, 3, 4
-WFMT = {"bf16": 0, "fp8": 1, "nvfp4": 2, "fp8_block": 3}
+WFMT = {"bf16": 0, "fp8": 1, "nvfp4": 2, "fp8_block": 3, "int8": 4}
 Y_BF16, Y_F32 = 0, 1
 
 
@@ -132,6 +132,24 @@ _SIGS = {
     "moe_block_linear_workspace_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "moe_block_linear": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
                          + [ctypes.c_void_p] * 5 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_channel_pack": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32] + [ctypes.c_void_p] * 4),
+    "moe_channel_packed_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "moe_channel_pack_codes": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32] + [ctypes.c_void_p] * 3),
+    "moe_channel_quantize": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32] + [ctypes.c_void_p] * 4),
+    "moe_channel_matmul": (ctypes.c_int32, [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 5
+                           + [ctypes.c_int32, ctypes.c_void_p]),
+    "moe_channel_linear_workspace_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "moe_channel_linear": (ctypes.c_int32, [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 4
+                           + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_grouped_matmul": (ctypes.c_int32, [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4
+                           + [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "moe_grouped_input_grad": (ctypes.c_int32, [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4
+                               + [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "moe_grouped_weight_grad": (ctypes.c_int32, [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4
+                                + [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "moe_group_rows_workspace_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "moe_group_rows": (ctypes.c_int32, [ctypes.c_int32] * 2 + [ctypes.c_void_p] * 5
+                       + [ctypes.c_size_t, ctypes.c_void_p]),
     "moe_layer_few_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims), ctypes.c_int32,
                                                        ctypes.c_int32]),
     "moe_layer_few": (ctypes.c_int32, [ctypes.POINTER(Dims), ctypes.c_int32, ctypes.c_void_p,
@@ -147,7 +165,7 @@ _SIGS = {
 }
 
 _lib = None
-ABI_VERSION = 8  # MOE_ABI_VERSION of include/moe.h this binding describes
+ABI_VERSION = 9  # MOE_ABI_VERSION of include/moe.h this binding describes
 
 
 def lib():
@@ -240,6 +258,9 @@ def _bank_parts(fmt: str, E: int, H: int, F: int):
         return (("up", code, n // 2), ("down", code, n // 2), ("up_s", scale, 4 * E), ("down_s", scale, 4 * E),
                 ("up_bs", code, n // 16), ("down_bs", code, n // 16))
     kh, kf = -(-H // 128), -(-F // 128)
+    if fmt == "int8":
+        return (("up", code, E * -(-F // 16) * kh * 2048), ("down", code, E * -(-H // 16) * kf * 2048),
+                ("up_s", scale, 4 * E * F), ("down_s", scale, 4 * E * H))
     return (("up", code, E * -(-F // 16) * kh * 2048), ("down", code, E * -(-H // 16) * kf * 2048),
             ("up_s", scale, 4 * E * kh * kf), ("down_s", scale, 4 * E * kh * kf))
 
@@ -521,8 +542,8 @@ def forward_cached(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, cach
 
 def quantize_experts(up: torch.Tensor, down: torch.Tensor, fmt: str,
                      dims: LayerDims = LayerDims()) -> ExpertBank:
-    """moe_quantize_experts: pack a bf16 bank [E,F,H] / [E,H,F] into fp8, nvfp4 or
-    fp8_block."""
+    """moe_quantize_experts: pack a bf16 bank [E,F,H] / [E,H,F] into fp8, nvfp4,
+    fp8_block or int8."""
     if fmt == "bf16":
         return ExpertBank("bf16", up, down)
     E, F, H = dims.n_experts, dims.ffn, dims.hidden
@@ -544,11 +565,17 @@ def quantize_experts(up: torch.Tensor, down: torch.Tensor, fmt: str,
         up_q = torch.empty((E, block_packed_size(F, H)), dtype=torch.uint8, device=dev)
         down_q = torch.empty((E, block_packed_size(H, F)), dtype=torch.uint8, device=dev)
         up_bs = down_bs = None
+    elif fmt == "int8":
+        up_q = torch.empty((E, channel_packed_size(F, H)), dtype=torch.int8, device=dev)
+        down_q = torch.empty((E, channel_packed_size(H, F)), dtype=torch.int8, device=dev)
+        up_bs = down_bs = None
     else:
         raise ValueError(fmt)
     nf, nh = (-(-F // 128), -(-H // 128))
-    up_s = torch.empty((E, nf, nh) if fmt == "fp8_block" else E, dtype=torch.float32, device=dev)
-    down_s = torch.empty((E, nh, nf) if fmt == "fp8_block" else E, dtype=torch.float32, device=dev)
+    up_shape = {"fp8_block": (E, nf, nh), "int8": (E, F)}.get(fmt, (E,))
+    down_shape = {"fp8_block": (E, nh, nf), "int8": (E, H)}.get(fmt, (E,))
+    up_s = torch.empty(up_shape, dtype=torch.float32, device=dev)
+    down_s = torch.empty(down_shape, dtype=torch.float32, device=dev)
     d = dims.c()
     _check("moe_quantize_experts", lib().moe_quantize_experts(
         ctypes.byref(d), WFMT[fmt], _ptr(up), _ptr(down), _ptr(up_q), _ptr(down_q),
@@ -558,20 +585,20 @@ def quantize_experts(up: torch.Tensor, down: torch.Tensor, fmt: str,
 
 def quantize_activation(x: torch.Tensor, fmt: str):
     """moe_quantize_activation: (codes, block scales or None, scale fp32[1]; fp8_block:
-    [ceil(cols / 128), rows])."""
+    [ceil(cols / 128), rows]; int8: [rows])."""
     rows, cols = x.shape
     _dev(x, torch.bfloat16, "x")
     dev = x.device
-    if fmt in ("fp8", "fp8_block"):
-        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    if fmt in ("fp8", "fp8_block", "int8"):
+        codes = torch.empty((rows, cols), dtype=torch.int8 if fmt == "int8" else torch.uint8, device=dev)
         bs = None
     elif fmt == "nvfp4":
         codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
         bs = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev)
     else:
         raise ValueError(fmt)
-    scale = torch.empty((-(-cols // 128), rows) if fmt == "fp8_block" else 1, dtype=torch.float32,
-                        device=dev)
+    shape = {"fp8_block": (-(-cols // 128), rows), "int8": (rows,)}.get(fmt, (1,))
+    scale = torch.empty(shape, dtype=torch.float32, device=dev)
     ws = torch.empty(256, dtype=torch.uint8, device=dev)
     _check("moe_quantize_activation", lib().moe_quantize_activation(
         WFMT[fmt], rows, cols, _ptr(x), _ptr(codes), _ptr(bs), _ptr(scale), _ptr(ws), 256, _stream()))
@@ -867,3 +894,227 @@ def block_linear(x: torch.Tensor, weight: BlockWeight, y: Optional[torch.Tensor]
             M, N, K, x.data_ptr(), weight.codes.data_ptr(), weight.scales.data_ptr(), y.data_ptr(),
             _p(ws), 0 if ws is None else ws.numel())
     return y
+
+
+CHANNEL_FEW_ROWS = 32  # MOE_CHANNEL_FEW_ROWS of include/moe.h
+
+
+@dataclass
+class ChannelWeight:
+    """A weight of `shape` (N, K) packed by moe_channel_pack: 8-bit integer codes
+    [channel_packed_size(N, K)] and one fp32 scale per output channel, [N]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    shape: tuple
+
+
+def channel_packed_size(N: int, K: int) -> int:
+    n = int(lib().moe_channel_packed_size(int(N), int(K)))
+    if n == 0:
+        raise ValueError(f"moe_channel_packed_size: invalid N {N} or K {K} (K % 16 == 0, K <= 65536)")
+    return n
+
+
+def channel_pack(w: torch.Tensor) -> ChannelWeight:
+    """moe_channel_pack: bf16 [N, K] -> 8-bit integer codes with a scale per row."""
+    N, K = _matrix(w, torch.bfloat16, "w").shape
+    codes = torch.empty(channel_packed_size(N, K), dtype=torch.int8, device=w.device)
+    scales = torch.empty(N, dtype=torch.float32, device=w.device)
+    _launch("moe_channel_pack", lib().moe_channel_pack, w.device.index,
+            N, K, w.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return ChannelWeight(codes, scales, (N, K))
+
+
+def channel_pack_codes(codes: torch.Tensor, scales: torch.Tensor) -> ChannelWeight:
+    """moe_channel_pack_codes: row-major int8 codes [N, K] and their channel scales
+    fp32 [N], as a checkpoint holds them."""
+    N, K = _matrix(codes, torch.int8, "codes").shape
+    _arg(scales, torch.float32, "scales", (N,), codes.device)
+    packed = torch.empty(channel_packed_size(N, K), dtype=torch.int8, device=codes.device)
+    _launch("moe_channel_pack_codes", lib().moe_channel_pack_codes, codes.device.index,
+            N, K, codes.data_ptr(), packed.data_ptr())
+    return ChannelWeight(packed, scales, (N, K))
+
+
+def channel_quantize(x: torch.Tensor):
+    """moe_channel_quantize: bf16 [M, K] -> (codes int8 [M, K], scales fp32 [M])."""
+    M, K = _matrix(x, torch.bfloat16, "x").shape
+    codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    _launch("moe_channel_quantize", lib().moe_channel_quantize, x.device.index,
+            M, K, x.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def _out(out: Optional[torch.Tensor], dtype: Optional[torch.dtype], name: str, shape, like: torch.Tensor):
+    """(output tensor, its MOE_Y_*): `out` as given, whose dtype must be `dtype` unless
+    that is None, or a new one (bf16 for None)."""
+    if out is None:
+        out = like.new_empty(shape, dtype=torch.bfloat16 if dtype is None else dtype)
+        yd = _Y_DTYPES.get(out.dtype)
+    else:
+        yd = _Y_DTYPES.get(out.dtype) if isinstance(out, torch.Tensor) else None
+        if yd is not None:
+            _arg(out, out.dtype if dtype is None else dtype, name, shape, like.device)
+    if yd is None:
+        raise ValueError(f"{name}: expected float32 or bfloat16")
+    return out, yd
+
+
+def _channel_operands(rows: torch.Tensor, weight: ChannelWeight, y, y_dtype):
+    M, K = rows.shape
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError(f"weight: K is {weight.shape[1]}, the rows have {K}")
+    dev = rows.device
+    _arg(weight.codes, torch.int8, "weight.codes", ((N + 15) // 16 * -(-K // 128) * 2048,), dev)
+    _arg(weight.scales, torch.float32, "weight.scales", (N,), dev)
+    y, yd = _out(y, y_dtype, "y", (M, N), rows)
+    return M, N, K, y, yd
+
+
+def channel_matmul(codes: torch.Tensor, scales: torch.Tensor, weight: ChannelWeight,
+                   y: Optional[torch.Tensor] = None, y_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """moe_channel_matmul: [M, N] in bf16 (or y_dtype) from codes and scales of
+    channel_quantize."""
+    _matrix(codes, torch.int8, "codes")
+    M, N, K, y, yd = _channel_operands(codes, weight, y, y_dtype)
+    _arg(scales, torch.float32, "scales", (M,), codes.device)
+    _launch("moe_channel_matmul", lib().moe_channel_matmul, codes.device.index,
+            M, N, K, codes.data_ptr(), scales.data_ptr(), weight.codes.data_ptr(),
+            weight.scales.data_ptr(), y.data_ptr(), yd)
+    return y
+
+
+@functools.lru_cache(maxsize=256)
+def _channel_linear_bytes(max_rows: int, K: int) -> int:
+    return int(lib().moe_channel_linear_workspace_size(max_rows, K))
+
+
+def channel_linear_workspace(max_rows: int, K: int, device="cuda") -> torch.Tensor:
+    n = _channel_linear_bytes(int(max_rows), int(K))
+    if n == 0:
+        raise ValueError(f"moe_channel_linear_workspace_size: invalid rows {max_rows} or K {K}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def channel_linear(x: torch.Tensor, weight: ChannelWeight, y: Optional[torch.Tensor] = None,
+                   y_dtype: Optional[torch.dtype] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_channel_linear: [M, N] in bf16 (or y_dtype) = x [M, K] quantised by rows,
+    times the weight."""
+    _matrix(x, torch.bfloat16, "x")
+    M, N, K, y, yd = _channel_operands(x, weight, y, y_dtype)
+    if ws is not None:
+        _arg(ws, torch.uint8, "ws", getattr(ws, "shape", None), x.device)
+    elif M > CHANNEL_FEW_ROWS:
+        ws = channel_linear_workspace(M, K, x.device)
+    _launch("moe_channel_linear", lib().moe_channel_linear, x.device.index,
+            M, N, K, x.data_ptr(), weight.codes.data_ptr(), weight.scales.data_ptr(), y.data_ptr(), yd,
+            _p(ws), 0 if ws is None else ws.numel())
+    return y
+
+
+# ---- products grouped by expert
+def group_rows(ids: torch.Tensor, n_experts: int):
+    """moe_group_rows: (offsets int32 [n_experts + 1], src int32 [R], inv int32 of ids'
+    shape) of the R = ids.numel() rows that ids int32 (e.g. [T, k] of route) name:
+    row i of the sorted rows is flat entry src[i], entry j is sorted row inv[j]
+    (-1: an id outside [0, n_experts); src is 0 behind the last row there is)."""
+    if not isinstance(ids, torch.Tensor):
+        raise ValueError("ids: expected a tensor")
+    _dev(ids, torch.int32, "ids")
+    R, dev = ids.numel(), ids.device
+    n = int(lib().moe_group_rows_workspace_size(int(n_experts), R))
+    if n == 0:
+        raise ValueError(f"moe_group_rows_workspace_size: invalid n_experts {n_experts} or rows {R}")
+    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
+    src = torch.zeros(R, dtype=torch.int32, device=dev)
+    inv = torch.empty(ids.shape, dtype=torch.int32, device=dev)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _launch("moe_group_rows", lib().moe_group_rows, dev.index,
+            R, n_experts, ids.data_ptr(), offsets.data_ptr(), src.data_ptr(), inv.data_ptr(), ws.data_ptr(), n)
+    return offsets, src, inv
+
+
+def _grouped_operands(rows: torch.Tensor, name: str, w: torch.Tensor, offsets: torch.Tensor, axis: int):
+    """(R, E, N, K) of rows [R, w.shape[axis]] and w [E, N, K]."""
+    R, width = _matrix(rows, torch.bfloat16, name).shape
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w: expected a [E, N, K] tensor")
+    E, N, K = shape = w.shape
+    _arg(w, torch.bfloat16, "w", shape, rows.device)
+    if shape[axis] != width:
+        raise ValueError(f"{name}: {width} columns, w is {tuple(shape)}")
+    _arg(offsets, torch.int32, "offsets", (E + 1,), rows.device)
+    return R, E, N, K
+
+
+def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: Optional[torch.Tensor] = None,
+                   y_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """moe_grouped_matmul: y [R, N] with y[r] = w[e] x[r] for the rows offsets[e] to
+    offsets[e + 1] of expert e; x bf16 [R, K], w bf16 [E, N, K].  Rows behind
+    offsets[E] stay as they are in a y that is given and are zero in a new one."""
+    R, E, N, K = _grouped_operands(x, "x", w, offsets, 2)
+    fresh = y is None
+    y, yd = _out(y, y_dtype, "y", (R, N), x)
+    _launch("moe_grouped_matmul", lib().moe_grouped_matmul, x.device.index,
+            R, E, N, K, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(), yd, 1 if fresh else 0)
+    return y
+
+
+def grouped_input_grad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                       dx: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """moe_grouped_input_grad: dx [R, K] with dx[r] = dy[r] w[e]; dy bf16 [R, N], w bf16
+    [E, N, K].  Rows behind offsets[E] as in grouped_matmul."""
+    R, E, N, K = _grouped_operands(dy, "dy", w, offsets, 1)
+    fresh = dx is None
+    dx, yd = _out(dx, dx_dtype, "dx", (R, K), dy)
+    _launch("moe_grouped_input_grad", lib().moe_grouped_input_grad, dy.device.index,
+            R, E, N, K, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), dx.data_ptr(), yd, 1 if fresh else 0)
+    return dx
+
+
+def grouped_weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                        dw: Optional[torch.Tensor] = None, dw_dtype: Optional[torch.dtype] = None,
+                        accumulate: bool = False) -> torch.Tensor:
+    """moe_grouped_weight_grad: dw [E, N, K] with dw[e] = dy[rows of e]^T x[rows of e],
+    in bf16 (or dw_dtype); with accumulate added to the fp32 dw given.  dy bf16
+    [R, N], x bf16 [R, K]."""
+    R, N = _matrix(dy, torch.bfloat16, "dy").shape
+    dev = dy.device
+    _arg(x, torch.bfloat16, "x", (R, _matrix(x, torch.bfloat16, "x").shape[1]), dev)
+    K = x.shape[1]
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets: expected an int32 [E + 1] tensor")
+    E = offsets.numel() - 1
+    _arg(offsets, torch.int32, "offsets", (E + 1,), dev)
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs the dw to add to")
+    dw, yd = _out(dw, dw_dtype, "dw", (E, N, K), dy)
+    _launch("moe_grouped_weight_grad", lib().moe_grouped_weight_grad, dev.index,
+            R, E, N, K, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), dw.data_ptr(), yd, 1 if accumulate else 0)
+    return dw
+
+
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return grouped_matmul(x, w, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = grouped_input_grad(dy, w, offsets) if ctx.needs_input_grad[0] else None
+        dw = grouped_weight_grad(dy, x, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dw, None
+
+
+def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+    """grouped_matmul with gradients (torch autograd): bf16 y [R, N] of x bf16 [R, K] and
+    w bf16 [E, N, K], dx and dw in bf16.  The forward can be captured in a graph; a
+    captured backward is to call grouped_input_grad and grouped_weight_grad themselves,
+    since autograd's own bookkeeping of leaves does not belong in one."""
+    return _GroupedLinear.apply(x, w, offsets)

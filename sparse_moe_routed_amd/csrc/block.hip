@@ -37,6 +37,7 @@
 #include "block_quant.h"
 #include "moe_common.h"
 #include "moe_internal.h"
+#include "tile.h"
 
 namespace moe {
 
@@ -211,19 +212,6 @@ __device__ __forceinline__ void store4(const BlockArgs& g, int row, int n, f32x4
         if (n + i < g.N) o[i] = b[i];
     }
   }
-}
-
-// Buffer descriptors: raw 32-bit data; a load past num_records reads zero and
-// touches no memory, so loads past the last K block are issued all the same, and
-// every wave has the same number of loads under way.  What lies past the end is
-// past it by the lane's own offset (kPastEnd, or a descriptor of no records with
-// a scalar offset of 0), whether or not the range check counts the scalar offset.
-constexpr int kRawBuffer = 0x00027000;
-constexpr uint32_t kPastEnd = kBlockMaxBytes;  // and 4 KB on: beyond every buffer
-typedef __amdgpu_buffer_rsrc_t Buffer;
-
-__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), kRawBuffer);
 }
 
 // the operand of 16 weight rows and one K block: `at` is the lane's offset of the
@@ -406,18 +394,6 @@ __global__ __launch_bounds__(kSmallWaves * kWave) void block_small_kernel(BlockA
 // half the time (8192 x 8192 x 4096: 2.06 PFLOP/s, matrix units about 45 %), and what
 // is left is the waves' own order of LDS reads, products and multiply-adds between
 // barriers.
-__device__ __forceinline__ void load16_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, at, step_at, 0, 0);
-}
-__device__ __forceinline__ void load4_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 4, at, step_at, 0, 0);
-}
-
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
-
-// s_waitcnt immediate: at most n vector memory operations outstanding
-constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
-
 template <int MODE, int BM, int BN, int WM, int WN, int NBUF, int WBUF, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64) void block_gemm_kernel(BlockArgs g) {
   constexpr int NW = WM * WN;
@@ -872,7 +848,7 @@ hipError_t launch_block_few_linear(const BlockArgs& g, hipStream_t stream) {
 
 hipError_t launch_block_quant(const BlockQuantArgs& q, hipStream_t stream) {
   if (q.rows <= 0) return hipSuccess;
-  hipLaunchKernelGGL(block_quant_kernel, dim3(block_quant_groups(q)), dim3(kQThreads), 0, stream, q);
+  hipLaunchKernelGGL(block_quant_kernel, dim3(quant_groups(q)), dim3(kQThreads), 0, stream, q);
   return hipGetLastError();
 }
 

@@ -77,9 +77,10 @@ __device__ __forceinline__ void block_quantise(const BlockQuantArgs& q, int grou
 }
 
 // workgroups for q's rows
-inline int block_quant_groups(const BlockQuantArgs& q) {
-  const int64_t n = static_cast<int64_t>(q.rows) * ((q.cols + 127) / 128);
-  const int64_t g = (n + kQThreads / 16 - 1) / (kQThreads / 16);
+inline int quant_groups(const BlockQuantArgs& q) {
+  const int64_t n = static_cast<int64_t>(q.rows) * (q.int8 ? 1 : (q.cols + 127) / 128);
+  const int64_t per = kQThreads / (q.int8 ? 64 : 16);  // rows, or blocks of a row
+  const int64_t g = (n + per - 1) / per;
   return static_cast<int>(g < 8192 ? g : 8192);
 }
 

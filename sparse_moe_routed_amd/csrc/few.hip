@@ -880,7 +880,7 @@ hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
 // but 16 96 (90): there the border, drawn at the full layer, comes 7 % late.
 bool few_pays(int fmt, int T, int H, int F, int k) {
   const size_t staged = static_cast<size_t>(T) * k * F;
-  if (fmt == kFP8Block || (fmt == kBF16 && staged > 140000) || (fmt == kNVFP4 && staged > 60000)) return false;
+  if (fmt == kFP8Block || fmt == kInt8 || (fmt == kBF16 && staged > 140000) || (fmt == kNVFP4 && staged > 60000)) return false;
   return stage_need(T, H, F) <= kMaxStage &&
          static_cast<size_t>(H) * F * 2 < (static_cast<size_t>(1) << 31);
 }

@@ -19,6 +19,7 @@ namespace {
 using moe::kBF16;
 using moe::kFP8;
 using moe::kFP8Block;
+using moe::kInt8;
 using moe::kNVFP4;
 
 constexpr int32_t kMaxTokens = 1 << 20;
@@ -56,7 +57,12 @@ moe_status bank_dims_check(const moe_dims* d) {
 }
 
 bool fmt_ok(int32_t fmt) {
-  return fmt == kBF16 || fmt == kFP8 || fmt == kNVFP4 || fmt == kFP8Block;
+  return fmt == kBF16 || fmt == kFP8 || fmt == kNVFP4 || fmt == kFP8Block || fmt == kInt8;
+}
+
+// whether a format's products cover the widths: sums of 8-bit integers stay in int32
+bool fmt_covers(int32_t fmt, const moe_dims* d) {
+  return fmt != kInt8 || (d->hidden <= moe::kChannelMaxK && d->ffn <= moe::kChannelMaxK);
 }
 
 // blocks of 128 values along a width
@@ -129,7 +135,12 @@ Layout make_layout(const moe_dims* d, int32_t fmt, int32_t T) {
   L.has_xq = fmt != kBF16;
   L.has_actq = fmt != kBF16;
   L.actq_inplace = fmt == kNVFP4;
-  if (fmt == kFP8Block) {  // codes and block scales
+  if (fmt == kInt8) {  // codes and row scales
+    L.x_q = alloc(static_cast<size_t>(T) * H);
+    L.x_s = alloc(static_cast<size_t>(T) * 4);
+    L.act_q = alloc(R * F);
+    L.act_s = alloc(R * 4);
+  } else if (fmt == kFP8Block) {  // codes and block scales
     L.x_q = alloc(static_cast<size_t>(T) * H);
     L.x_s = alloc(kblocks(H) * T * 4);
     L.act_q = alloc(R * F);
@@ -161,6 +172,52 @@ BlockLinearLayout block_linear_layout(int32_t M, int32_t K) {
   BlockLinearLayout L{};
   L.scales = up(static_cast<size_t>(M) * K);
   L.total = L.scales + up(kblocks(K) * M * 4) + kAlign;
+  return L;
+}
+
+// operands of the 8-bit integer product
+moe_status channel_dims_check(int32_t M, int32_t N, int32_t K) {
+  if (M < 0 || M > kMaxTokens || N <= 0 || K <= 0) return MOE_EINVAL;
+  if (K % 16 || N > (1 << 20) || K > moe::kChannelMaxK) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// workspace of moe_channel_linear: codes, then scales
+BlockLinearLayout channel_linear_layout(int32_t M, int32_t K) {
+  const auto up = [](size_t n) { return (n + kAlign - 1) / kAlign * kAlign; };
+  BlockLinearLayout L{};
+  L.scales = up(static_cast<size_t>(M) * K);
+  L.total = L.scales + up(static_cast<size_t>(M) * 4) + kAlign;
+  return L;
+}
+
+// rows grouped by expert: 16-byte chunks along both widths, and the experts that a
+// wave can look through
+constexpr int32_t kMaxGroupRows = 1 << 23;
+constexpr int32_t kMaxGroups = 256;
+moe_status grouped_dims_check(int32_t R, int32_t E, int32_t N, int32_t K) {
+  if (R < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_EINVAL;
+  if (R > kMaxGroupRows || E > kMaxGroups || N % 8 || K % 8 || N > (1 << 16) || K > (1 << 16))
+    return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// workspace of moe_group_rows
+struct GroupRowsLayout {
+  size_t chunk_counts, chunk_base, counts, tile_off0, tile_off1, total;
+};
+
+GroupRowsLayout group_rows_layout(int32_t E, int64_t R) {
+  const auto up = [](size_t n) { return (n + kAlign - 1) / kAlign * kAlign; };
+  const size_t list = up((static_cast<size_t>(E) + 1) * 4);
+  const size_t chunks = up(static_cast<size_t>((R + moe::kChunk - 1) / moe::kChunk) * E * 4);
+  GroupRowsLayout L{};
+  L.counts = 0;
+  L.tile_off0 = list;
+  L.tile_off1 = 2 * list;
+  L.chunk_counts = 3 * list;
+  L.chunk_base = L.chunk_counts + chunks;
+  L.total = L.chunk_base + chunks;
   return L;
 }
 
@@ -234,7 +291,7 @@ CacheView cache_view(void* state, int E, int n_slots) {
 // bytes of one expert's codes and (NVFP4) block scales in a projection N x K
 size_t expert_code_bytes(int fmt, int N, int K) {
   const size_t n = static_cast<size_t>(N) * K;
-  if (fmt == kFP8Block) return (static_cast<size_t>(N) + 15) / 16 * kblocks(K) * 2048;
+  if (fmt == kFP8Block || fmt == kInt8) return (static_cast<size_t>(N) + 15) / 16 * kblocks(K) * 2048;
   return fmt == kBF16 ? 2 * n : (fmt == kNVFP4 ? n / 2 : n);
 }
 size_t expert_scale_bytes(int fmt, int N, int K) {
@@ -303,12 +360,13 @@ const char* moe_status_str(int32_t s) {
 }
 
 size_t moe_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens) {
-  if (!dims_ok(dims) || !fmt_ok(fmt) || max_tokens < 0 || max_tokens > kMaxTokens) return 0;
+  if (!dims_ok(dims) || !fmt_ok(fmt) || !fmt_covers(fmt, dims) || max_tokens < 0 || max_tokens > kMaxTokens) return 0;
   return make_layout(dims, fmt, max_tokens).total;
 }
 
 int32_t moe_workspace_layout(const moe_dims* dims, int32_t fmt, int32_t T, moe_ws_layout* out) {
   if (!out || !dims_ok(dims) || !fmt_ok(fmt) || T < 0 || T > kMaxTokens) return MOE_EINVAL;
+  if (!fmt_covers(fmt, dims)) return MOE_EUNSUPPORTED;
   const Layout L = make_layout(dims, fmt, T);
   out->counts = static_cast<int64_t>(L.counts);
   out->offsets = static_cast<int64_t>(L.offsets);
@@ -462,6 +520,49 @@ hipError_t block_stages(const moe_dims* dims, int32_t T, const moe_experts* ex,
   return moe::launch_block_experts(1, g, st, marks.gemm(1));
 }
 
+// the same with an "int8" bank: the intermediate takes one scale a row, so it waits
+// for the row's whole maximum and is quantised by a kernel of its own
+hipError_t channel_stages(const moe_dims* dims, int32_t T, const moe_experts* ex,
+                          const moe::PermBufs& p, const int32_t* w_slot, const Layout& L, void* ws,
+                          const StageMarks& marks) {
+  const int H = dims->hidden, F = dims->ffn, E = dims->n_experts, R = T * dims->top_k;
+  const hipStream_t st = marks.st;
+  marks.mark(1);  // the permutation has quantised the tokens beside its own work
+  marks.mark(2);
+  moe::NtArgs g{};
+  g.M = R;
+  g.N = F;
+  g.K = H;
+  g.a = at<uint8_t>(ws, L.x_q);
+  g.a_s = at<float>(ws, L.x_s);
+  g.a_rows = T;
+  g.w = static_cast<const uint8_t*>(ex->up);
+  g.w_s = ex->up_s;
+  g.out = at<uint16_t>(ws, L.act);
+  g.E = E;
+  g.offsets = p.offsets;
+  g.sorted_src = p.sorted_src;
+  g.top_k = dims->top_k;
+  g.w_slot = w_slot;
+  hipError_t err = moe::launch_channel_experts(0, g, st, marks.gemm(0));
+  if (err != hipSuccess) return err;
+  marks.mark(3);
+  err = moe::launch_channel_quant({at<uint16_t>(ws, L.act), R, F, at<uint8_t>(ws, L.act_q), at<float>(ws, L.act_s), 1},
+                                  p.offsets + E, st);
+  if (err != hipSuccess) return err;
+  marks.mark(4);
+  g.N = H;
+  g.K = F;
+  g.a = at<uint8_t>(ws, L.act_q);
+  g.a_s = at<float>(ws, L.act_s);
+  g.a_rows = R;
+  g.w = static_cast<const uint8_t*>(ex->down);
+  g.w_s = ex->down_s;
+  g.out = at<float>(ws, L.out_rows);
+  g.row_gate = p.row_gate;
+  return moe::launch_channel_experts(1, g, st, marks.gemm(1));
+}
+
 // The forward pass.  With `cc` set, the expert weights come from the cache:
 // after the permutation the row counts go to the host, the missing experts
 // are uploaded into slots, and the GEMMs read the slots through slot_of.
@@ -497,6 +598,7 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   if (!ex) return MOE_EINVAL;
   if (T < 0 || T > kMaxTokens) return MOE_EINVAL;
   if (!fmt_ok(ex->fmt)) return MOE_EINVAL;
+  if (!fmt_covers(ex->fmt, dims)) return MOE_EUNSUPPORTED;
   if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
   if (accumulate && y_dtype != MOE_Y_F32) return MOE_EINVAL;
   if (T == 0) return MOE_OK;  // nothing is read or written; pointers may be null
@@ -507,8 +609,8 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(ids, 4) || !aligned(gates, 4) ||
       !bank_aligned(ex))
     return MOE_EINVAL;
-  // the block-scaled products address the tokens' codes by 32 bits
-  if (ex->fmt == kFP8Block && static_cast<size_t>(T) * dims->hidden >= moe::kBlockMaxBytes)
+  // these products address the tokens' codes by 32 bits
+  if ((ex->fmt == kFP8Block || ex->fmt == kInt8) && static_cast<size_t>(T) * dims->hidden >= moe::kBlockMaxBytes)
     return MOE_EUNSUPPORTED;
   const Layout L = make_layout(dims, ex->fmt, T);
   if (!ws || ws_bytes < L.total) return MOE_EWORKSPACE;
@@ -533,14 +635,15 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
   p.sorted_src = at<int32_t>(ws, L.sorted_src);
   p.inv = at<int32_t>(ws, L.inv);
   p.row_gate = at<float>(ws, L.row_gate);
-  p.bm0 = fmt == kFP8Block ? moe::block_tile_rows(R, E) : moe::gemm_shape(fmt, 0, T).bm;
+  const bool by_rows = fmt == kFP8Block || fmt == kInt8;  // scales of rows or parts of them
+  p.bm0 = by_rows ? moe::block_tile_rows(R, E) : moe::gemm_shape(fmt, 0, T).bm;
   p.tile_off0 = at<int32_t>(ws, L.tile_off0);
-  p.bm1 = fmt == kFP8Block ? p.bm0 : moe::gemm_shape(fmt, 1, T).bm;
+  p.bm1 = by_rows ? p.bm0 : moe::gemm_shape(fmt, 1, T).bm;
   p.tile_off1 = at<int32_t>(ws, L.tile_off1);
   p.zero_words = amax_x;  // amax slots of x and of the intermediate
   p.n_zero = 2 * moe::kAmaxSlots;
-  if (fmt == kFP8Block)
-    p.quant = {static_cast<const uint16_t*>(x), T, H, at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s)};
+  if (by_rows)
+    p.quant = {static_cast<const uint16_t*>(x), T, H, at<uint8_t>(ws, L.x_q), at<float>(ws, L.x_s), fmt == kInt8};
   marks.mark(0);
   hipError_t err = shared ? moe::launch_permute_identity(R, p, st)
                           : moe::launch_permute(ids, gates, T, E, k, p, st);
@@ -620,8 +723,9 @@ int32_t forward_impl(const moe_dims* dims, int32_t T, const void* x, const int32
     if (cc->stats) *cc->stats = moe_cache_stats{touched, hits, misses, bytes};
   }
 
-  if (fmt == kFP8Block) {
-    const hipError_t be = block_stages(dims, T, ex, p, w_slot, L, ws, marks);
+  if (by_rows) {
+    const hipError_t be = fmt == kInt8 ? channel_stages(dims, T, ex, p, w_slot, L, ws, marks)
+                                       : block_stages(dims, T, ex, p, w_slot, L, ws, marks);
     if (be != hipSuccess) return MOE_EHIP;
     marks.mark(5);
     const int mode = accumulate ? moe::kYF32Add : (y_dtype == MOE_Y_F32 ? moe::kYF32 : moe::kYBF16);
@@ -722,7 +826,7 @@ int32_t moe_forward_timed(const moe_dims* dims, int32_t T, const void* x, const 
 }
 
 size_t moe_shared_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens) {
-  if (shared_dims_check(dims) != MOE_OK || !fmt_ok(fmt) || max_tokens < 0 ||
+  if (shared_dims_check(dims) != MOE_OK || !fmt_ok(fmt) || !fmt_covers(fmt, dims) || max_tokens < 0 ||
       max_tokens > kMaxTokens)
     return 0;
   return make_layout(dims, fmt, max_tokens).total;
@@ -770,7 +874,8 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt, const void* up_b
                              const void* down_bf16, void* up_q, void* down_q, uint8_t* up_bs,
                              uint8_t* down_bs, float* up_s, float* down_s, void* stream) {
   if (const moe_status ds = bank_dims_check(dims)) return ds;
-  if (fmt != kFP8 && fmt != kNVFP4 && fmt != kFP8Block) return MOE_EINVAL;
+  if (fmt == kBF16 || !fmt_ok(fmt)) return MOE_EINVAL;
+  if (!fmt_covers(fmt, dims)) return MOE_EUNSUPPORTED;
   if (!up_bf16 || !down_bf16 || !up_q || !down_q || !up_s || !down_s) return MOE_EINVAL;
   if (fmt == kNVFP4 && (!up_bs || !down_bs)) return MOE_EINVAL;
   if (!aligned(up_bf16, 16) || !aligned(down_bf16, 16) || !aligned(up_q, 16) ||
@@ -787,6 +892,14 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt, const void* up_b
                                   static_cast<uint8_t*>(down_q), down_s, st);
     return hip_status(be);
   }
+  if (fmt == kInt8) {
+    hipError_t be = moe::launch_channel_pack(static_cast<const uint16_t*>(up_bf16), E, F, H,
+                                             static_cast<uint8_t*>(up_q), up_s, st);
+    if (be == hipSuccess)
+      be = moe::launch_channel_pack(static_cast<const uint16_t*>(down_bf16), E, H, F,
+                                    static_cast<uint8_t*>(down_q), down_s, st);
+    return hip_status(be);
+  }
   hipError_t err = moe::launch_quant_weights(fmt, static_cast<const uint16_t*>(up_bf16), E, F, H,
                                              static_cast<uint8_t*>(up_q), up_bs, up_s, 0, st);
   if (err == hipSuccess)
@@ -798,17 +911,18 @@ int32_t moe_quantize_experts(const moe_dims* dims, int32_t fmt, const void* up_b
 int32_t moe_quantize_activation(int32_t fmt, int32_t rows, int32_t cols, const void* x,
                                 void* codes, uint8_t* bs, float* scale, void* ws,
                                 size_t ws_bytes, void* stream) {
-  if (fmt != kFP8 && fmt != kNVFP4 && fmt != kFP8Block) return MOE_EINVAL;
+  if (fmt == kBF16 || !fmt_ok(fmt)) return MOE_EINVAL;
   if (rows < 0 || cols <= 0 || cols % 64) return MOE_EINVAL;
   if (static_cast<long long>(rows) * cols > (1ll << 31)) return MOE_EUNSUPPORTED;
   if (!x || !codes || !scale || (fmt == kNVFP4 && !bs)) return MOE_EINVAL;
   if (!aligned(x, 16) || !aligned(codes, 8) || !aligned(scale, 4)) return MOE_EINVAL;
-  if (fmt != kFP8Block && (!ws || ws_bytes < kAlign || !aligned(ws, 4))) return MOE_EWORKSPACE;
+  const bool by_rows = fmt == kFP8Block || fmt == kInt8;
+  if (!by_rows && (!ws || ws_bytes < kAlign || !aligned(ws, 4))) return MOE_EWORKSPACE;
   if (rows == 0) return MOE_OK;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (fmt == kFP8Block)
-    return hip_status(moe::launch_block_quant({static_cast<const uint16_t*>(x), rows, cols,
-                                               static_cast<uint8_t*>(codes), scale}, st));
+  const moe::BlockQuantArgs q{static_cast<const uint16_t*>(x), rows, cols, static_cast<uint8_t*>(codes), scale,
+                              fmt == kInt8};
+  if (by_rows) return hip_status(fmt == kInt8 ? moe::launch_channel_quant(q, nullptr, st) : moe::launch_block_quant(q, st));
   uint32_t* amax = static_cast<uint32_t*>(ws);  // kAmaxSlots words
   hipError_t err = moe::launch_zero_u32(amax, moe::kAmaxSlots, st);
   if (err == hipSuccess)
@@ -901,7 +1015,7 @@ int32_t moe_residual_norm(int32_t T, int32_t H, const void* x, const void* y, in
 }
 
 size_t moe_layer_few_workspace_size(const moe_dims* dims, int32_t fmt, int32_t max_tokens) {
-  if (!dims_ok(dims) || !fmt_ok(fmt) || max_tokens < 0 || max_tokens > moe::kFewTokens) return 0;
+  if (!dims_ok(dims) || !fmt_ok(fmt) || !fmt_covers(fmt, dims) || max_tokens < 0 || max_tokens > moe::kFewTokens) return 0;
   // if the most tokens take the two kernels, fewer do so too
   const size_t two = few_layout(dims, max_tokens).total;
   if (moe::few_pays(fmt, max_tokens, dims->hidden, dims->ffn, dims->top_k)) return two;
@@ -914,6 +1028,7 @@ int32_t moe_layer_few(const moe_dims* dims, int32_t T, const void* x, const moe_
   if (const moe_status ds = dims_check(dims)) return ds;
   if (!experts || T < 0 || T > kMaxTokens) return MOE_EINVAL;
   if (!fmt_ok(experts->fmt)) return MOE_EINVAL;
+  if (!fmt_covers(experts->fmt, dims)) return MOE_EUNSUPPORTED;
   if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
   if (T > moe::kFewTokens) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;  // nothing is read or written; pointers may be null
@@ -1065,6 +1180,216 @@ int32_t moe_block_linear(int32_t M, int32_t N, int32_t K, const void* x, const v
   const int32_t qs = moe_block_quantize(M, K, x, codes, scales, stream);
   if (qs != MOE_OK) return qs;
   return moe_block_matmul(M, N, K, codes, scales, w_codes, w_scales, y, stream);
+}
+
+int32_t moe_channel_pack(int32_t N, int32_t K, const void* w, void* codes, float* scales, void* stream) {
+  if (const moe_status cs = channel_dims_check(0, N, K)) return cs;
+  if (!w || !codes || !scales) return MOE_EINVAL;
+  if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
+  const Bytes from{w, static_cast<size_t>(N) * K * 2}, to{codes, expert_code_bytes(kInt8, N, K)};
+  if (overlap(to, from) || overlaps_any({scales, static_cast<size_t>(N) * 4}, {from, to})) return MOE_EINVAL;
+  return hip_status(moe::launch_channel_pack(static_cast<const uint16_t*>(w), 1, N, K, static_cast<uint8_t*>(codes),
+                                             scales, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_channel_packed_size(int32_t N, int32_t K) {
+  if (channel_dims_check(0, N, K) != MOE_OK) return 0;
+  return expert_code_bytes(kInt8, N, K);
+}
+
+int32_t moe_channel_pack_codes(int32_t N, int32_t K, const void* codes, void* packed, void* stream) {
+  if (const moe_status cs = channel_dims_check(0, N, K)) return cs;
+  if (!codes || !packed) return MOE_EINVAL;
+  if (!aligned(codes, 16) || !aligned(packed, 16)) return MOE_EINVAL;
+  if (overlap({codes, static_cast<size_t>(N) * K}, {packed, expert_code_bytes(kInt8, N, K)})) return MOE_EINVAL;
+  return hip_status(moe::launch_channel_pack_codes(static_cast<const uint8_t*>(codes), N, K,
+                                                   static_cast<uint8_t*>(packed), static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_channel_quantize(int32_t M, int32_t K, const void* x, void* codes, float* scales, void* stream) {
+  if (const moe_status cs = channel_dims_check(M, 1, K)) return cs;
+  if (M == 0) return MOE_OK;
+  if (!x || !codes || !scales) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_EINVAL;
+  const size_t values = static_cast<size_t>(M) * K;
+  const Bytes from{x, values * 2}, to{codes, values};
+  if (overlap(to, from) || overlaps_any({scales, static_cast<size_t>(M) * 4}, {from, to})) return MOE_EINVAL;
+  return hip_status(moe::launch_channel_quant({static_cast<const uint16_t*>(x), M, K, static_cast<uint8_t*>(codes),
+                                               scales, 1},
+                                              nullptr, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_channel_matmul(int32_t M, int32_t N, int32_t K, const void* codes, const float* scales,
+                           const void* w_codes, const float* w_scales, void* y, int32_t y_dtype, void* stream) {
+  if (const moe_status cs = channel_dims_check(M, N, K)) return cs;
+  if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (!codes || !scales || !w_codes || !w_scales || !y) return MOE_EINVAL;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(w_codes, 16) || !aligned(w_scales, 4) ||
+      !aligned(y, 16))
+    return MOE_EINVAL;
+  if (overlaps_any({y, static_cast<size_t>(M) * N * (y_dtype == MOE_Y_F32 ? 4 : 2)},
+                   {{codes, static_cast<size_t>(M) * K}, {scales, static_cast<size_t>(M) * 4},
+                    {w_codes, expert_code_bytes(kInt8, N, K)}, {w_scales, static_cast<size_t>(N) * 4}}))
+    return MOE_EINVAL;
+  moe::NtArgs g{};
+  g.M = g.a_rows = M;
+  g.N = N;
+  g.K = K;
+  g.a = static_cast<const uint8_t*>(codes);
+  g.a_s = scales;
+  g.w = static_cast<const uint8_t*>(w_codes);
+  g.w_s = w_scales;
+  g.out = y;
+  g.out_f32 = y_dtype == MOE_Y_F32;
+  return hip_status(moe::launch_channel_dense(g, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_channel_linear_workspace_size(int32_t max_rows, int32_t K) {
+  if (channel_dims_check(max_rows, 1, K) != MOE_OK) return 0;
+  return channel_linear_layout(max_rows, K).total;
+}
+
+int32_t moe_channel_linear(int32_t M, int32_t N, int32_t K, const void* x, const void* w_codes,
+                           const float* w_scales, void* y, int32_t y_dtype, void* ws, size_t ws_bytes,
+                           void* stream) {
+  if (const moe_status cs = channel_dims_check(M, N, K)) return cs;
+  if (y_dtype != MOE_Y_BF16 && y_dtype != MOE_Y_F32) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (!x || !w_codes || !w_scales || !y) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(y, 16)) return MOE_EINVAL;
+  static_assert(moe::kChannelFewRows == MOE_CHANNEL_FEW_ROWS, "the header's limit");
+  const size_t values = static_cast<size_t>(M) * N;
+  const Bytes bx{x, static_cast<size_t>(M) * K * 2}, by{y, values * (y_dtype == MOE_Y_F32 ? 4 : 2)};
+  const Bytes bw{w_codes, expert_code_bytes(kInt8, N, K)}, bs{w_scales, static_cast<size_t>(N) * 4};
+  if (overlaps_any(by, {bx, bw, bs})) return MOE_EINVAL;
+  if (M <= moe::kChannelFewRows) {
+    moe::NtArgs g{};
+    g.M = g.a_rows = M;
+    g.N = N;
+    g.K = K;
+    g.a = static_cast<const uint8_t*>(x);
+    g.w = static_cast<const uint8_t*>(w_codes);
+    g.w_s = w_scales;
+    g.out = y;
+    g.out_f32 = y_dtype == MOE_Y_F32;
+    return hip_status(moe::launch_channel_few_linear(g, static_cast<hipStream_t>(stream)));
+  }
+  const BlockLinearLayout L = channel_linear_layout(M, K);
+  if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
+  if (overlaps_any({ws, L.total}, {bx, by, bw, bs})) return MOE_EINVAL;
+  uint8_t* codes = at<uint8_t>(ws, 0);
+  float* scales = at<float>(ws, L.scales);
+  const int32_t qs = moe_channel_quantize(M, K, x, codes, scales, stream);
+  if (qs != MOE_OK) return qs;
+  return moe_channel_matmul(M, N, K, codes, scales, w_codes, w_scales, y, y_dtype, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// rows times their expert's weight, or with `grad` times its transpose
+int32_t grouped_rows_call(int32_t R, int32_t E, int32_t N, int32_t K, const void* a, const void* w,
+                          const int32_t* offsets, void* out, int32_t out_dtype, int32_t zero_rest, void* stream,
+                          bool grad) {
+  if (const moe_status cs = grouped_dims_check(R, E, N, K)) return cs;
+  if (out_dtype != MOE_Y_BF16 && out_dtype != MOE_Y_F32) return MOE_EINVAL;
+  if (zero_rest != 0 && zero_rest != 1) return MOE_EINVAL;
+  if (R == 0) return MOE_OK;  // nothing is read or written; pointers may be null
+  if (!a || !w || !offsets || !out) return MOE_EINVAL;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(offsets, 4)) return MOE_EINVAL;
+  const size_t rows = static_cast<size_t>(R);
+  if (overlaps_any({out, rows * (grad ? K : N) * (out_dtype == MOE_Y_F32 ? 4 : 2)},
+                   {{a, rows * (grad ? N : K) * 2}, {w, static_cast<size_t>(E) * N * K * 2},
+                    {offsets, (static_cast<size_t>(E) + 1) * 4}}))
+    return MOE_EINVAL;
+  moe::GroupedArgs g{};
+  g.R = R;
+  g.E = E;
+  g.N = N;
+  g.K = K;
+  (grad ? g.dy : g.x) = a;
+  g.w = w;
+  g.offsets = offsets;
+  g.out = out;
+  g.out_f32 = out_dtype == MOE_Y_F32;
+  g.zero_rest = zero_rest;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  return hip_status(grad ? moe::launch_grouped_input_grad(g, st) : moe::launch_grouped_matmul(g, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_group_rows_workspace_size(int32_t E, int32_t max_rows) {
+  if (E <= 0 || E > kMaxGroups || max_rows < 0 || max_rows > kMaxGroupRows) return 0;
+  return group_rows_layout(E, max_rows).total;
+}
+
+int32_t moe_group_rows(int32_t R, int32_t E, const int32_t* ids, int32_t* offsets, int32_t* sorted_src,
+                       int32_t* inv, void* ws, size_t ws_bytes, void* stream) {
+  if (R < 0 || E <= 0) return MOE_EINVAL;
+  if (R > kMaxGroupRows || E > kMaxGroups) return MOE_EUNSUPPORTED;
+  if (!offsets || (R > 0 && (!ids || !sorted_src || !inv))) return MOE_EINVAL;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(sorted_src, 4) || !aligned(inv, 4)) return MOE_EINVAL;
+  const GroupRowsLayout L = group_rows_layout(E, R);
+  if (!ws || ws_bytes < L.total || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
+  const size_t rows = static_cast<size_t>(R) * 4;
+  const Bytes bi{ids, rows}, bo{offsets, (static_cast<size_t>(E) + 1) * 4}, bs{sorted_src, rows}, bv{inv, rows};
+  if (overlaps_any(bo, {bi, bs, bv}) || overlaps_any(bs, {bi, bv}) || overlap(bv, bi) ||
+      overlaps_any({ws, L.total}, {bi, bo, bs, bv}))
+    return MOE_EINVAL;
+  moe::PermBufs p{};
+  p.chunk_counts = at<int32_t>(ws, L.chunk_counts);
+  p.chunk_base = at<int32_t>(ws, L.chunk_base);
+  p.counts = at<int32_t>(ws, L.counts);
+  p.offsets = offsets;
+  p.sorted_src = sorted_src;
+  p.inv = inv;
+  p.bm0 = p.bm1 = 1;
+  p.tile_off0 = at<int32_t>(ws, L.tile_off0);
+  p.tile_off1 = at<int32_t>(ws, L.tile_off1);
+  return hip_status(moe::launch_permute(ids, nullptr, R, E, 1, p, static_cast<hipStream_t>(stream)));
+}
+
+int32_t moe_grouped_matmul(int32_t R, int32_t E, int32_t N, int32_t K, const void* x, const void* w,
+                           const int32_t* offsets, void* y, int32_t y_dtype, int32_t zero_rest, void* stream) {
+  return grouped_rows_call(R, E, N, K, x, w, offsets, y, y_dtype, zero_rest, stream, false);
+}
+
+int32_t moe_grouped_input_grad(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy, const void* w,
+                               const int32_t* offsets, void* dx, int32_t dx_dtype, int32_t zero_rest,
+                               void* stream) {
+  return grouped_rows_call(R, E, N, K, dy, w, offsets, dx, dx_dtype, zero_rest, stream, true);
+}
+
+int32_t moe_grouped_weight_grad(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy, const void* x,
+                                const int32_t* offsets, void* dw, int32_t dw_dtype, int32_t accumulate,
+                                void* stream) {
+  if (const moe_status cs = grouped_dims_check(R, E, N, K)) return cs;
+  if (dw_dtype != MOE_Y_BF16 && dw_dtype != MOE_Y_F32) return MOE_EINVAL;
+  if ((accumulate != 0 && accumulate != 1) || (accumulate && dw_dtype != MOE_Y_F32)) return MOE_EINVAL;
+  if (!offsets || !dw || (R > 0 && (!dy || !x))) return MOE_EINVAL;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(offsets, 4)) return MOE_EINVAL;
+  const size_t rows = static_cast<size_t>(R);
+  if (overlaps_any({dw, static_cast<size_t>(E) * N * K * (dw_dtype == MOE_Y_F32 ? 4 : 2)},
+                   {{dy, rows * N * 2}, {x, rows * K * 2}, {offsets, (static_cast<size_t>(E) + 1) * 4}}))
+    return MOE_EINVAL;
+  if (R == 0 && accumulate) return MOE_OK;
+  moe::GroupedArgs g{};
+  g.R = R;
+  g.E = E;
+  g.N = N;
+  g.K = K;
+  g.dy = dy;
+  g.x = x;
+  g.offsets = offsets;
+  g.out = dw;
+  g.out_f32 = dw_dtype == MOE_Y_F32;
+  g.accumulate = accumulate;
+  return hip_status(moe::launch_grouped_weight_grad(g, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -6,7 +6,7 @@
 
 namespace moe {
 
-enum Fmt { kBF16 = 0, kFP8 = 1, kNVFP4 = 2, kFP8Block = 3 };
+enum Fmt { kBF16 = 0, kFP8 = 1, kNVFP4 = 2, kFP8Block = 3, kInt8 = 4 };
 // GEMM operand modes: kFP8 runs the FP8 MFMA on E4M3 codes; kFP8X expands
 // E4M3 weight codes to bf16 (exact) in LDS and runs the BF16 MFMA.
 constexpr int kFP8X = 16;
@@ -33,12 +33,14 @@ __host__ __device__ __forceinline__ int nv_panel_rows(int N, int p) {
   return left < kNvPanel ? left : kNvPanel;
 }
 
-// codes [rows, cols] and scales [ceil(cols / 128), rows] of bf16 rows
+// codes [rows, cols] of bf16 rows: E4M3 with scales [ceil(cols / 128), rows], or
+// 8-bit integers with scales [rows]
 struct BlockQuantArgs {
   const uint16_t* x;
   int rows, cols;
   uint8_t* codes;
   float* scales;
+  int int8;
 };
 
 struct PermBufs {
@@ -238,5 +240,50 @@ hipError_t launch_block_quant(const BlockQuantArgs& q, hipStream_t stream);
 hipError_t launch_block_pack_codes(const uint8_t* q, int N, int K, uint8_t* codes, hipStream_t stream);
 hipError_t launch_block_pack(const uint16_t* w, int E, int N, int K, uint8_t* codes, float* scales,
                              hipStream_t stream);
+
+// 8-bit integers with a scale per token and channel (moe_channel_*, "int8" banks)
+// operands of nt.h's kernel
+struct NtArgs {
+  int M, N, K;  // rows (of all groups), weight rows, values of K
+  const uint8_t* a;
+  int a_rows;  // rows of a
+  const uint8_t* w;
+  const float *a_s, *w_s;  // 8-bit integers: [a_rows], [E, N]
+  void* out;
+  int out_f32;
+  // groups
+  int E;
+  const int32_t* offsets;  // [E + 1]
+  const int32_t* sorted_src;
+  int top_k;
+  const int32_t* w_slot;
+  const float* row_gate;
+};
+constexpr int kChannelMaxK = 1 << 16;  // sums of 127 * 127 (128 * 128 of foreign codes) fit int32
+constexpr int kChannelFewRows = 32;
+hipError_t launch_channel_experts(int stage, const NtArgs& g, hipStream_t stream,
+                                  const KernelEvents& ev = KernelEvents{});
+hipError_t launch_channel_dense(const NtArgs& g, hipStream_t stream);
+hipError_t launch_channel_few_linear(const NtArgs& g, hipStream_t stream);
+// n_rows [dev]: the rows there are of q.rows, or null: all
+hipError_t launch_channel_quant(const BlockQuantArgs& q, const int32_t* n_rows, hipStream_t stream);
+hipError_t launch_channel_pack_codes(const uint8_t* q, int N, int K, uint8_t* codes, hipStream_t stream);
+hipError_t launch_channel_pack(const uint16_t* w, int E, int N, int K, uint8_t* codes, float* scales,
+                               hipStream_t stream);
+
+// products grouped by expert in bf16 (moe_grouped_*): rows offsets[e] to
+// offsets[e + 1] belong to expert e
+struct GroupedArgs {
+  int R, E, N, K;
+  const void *x, *dy, *w;  // [R, K], [R, N], [E, N, K]; the ones the product takes
+  const int32_t* offsets;  // [E + 1]
+  void* out;               // [R, N], [R, K] or [E, N, K]
+  int out_f32;
+  int zero_rest;   // rows of no expert become zero (matmul, input_grad)
+  int accumulate;  // add to out (weight_grad, fp32)
+};
+hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t stream);
+hipError_t launch_grouped_input_grad(const GroupedArgs& g, hipStream_t stream);
+hipError_t launch_grouped_weight_grad(const GroupedArgs& g, hipStream_t stream);
 
 }  // namespace moe

@@ -15,10 +15,10 @@
 // ballots.  When all ids fit one chunk (decode batches) perm_single does the
 // three steps in one workgroup.  No host sync.
 //
-// For an "fp8_block" bank the tokens' codes are made beside it: the first kernel
+// For an "fp8_block" or "int8" bank the tokens' codes are made beside it: the first kernel
 // gets workgroups of its own for them, which saves a launch (full layer, T = 1
 // 28.0 -> 26.0 us, T = 64 157.8 -> 156.3).
-#include "block_quant.h"
+#include "channel_quant.h"
 #include "moe_common.h"
 #include "moe_internal.h"
 
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kPermThreads) void perm_count_kernel(
     BlockQuantArgs quant) {
   __shared__ int32_t cnt[256];
   if (static_cast<int>(blockIdx.x) >= n_chunks)
-    return block_quantise(quant, blockIdx.x - n_chunks, gridDim.x - n_chunks);
+    return quantise_tokens(quant, blockIdx.x - n_chunks, gridDim.x - n_chunks);
   int ev[kRounds];
   load_chunk(ids, R, E, blockIdx.x, ev);
   for (int e = threadIdx.x; e < E; e += kPermThreads) cnt[e] = 0;
@@ -147,7 +147,7 @@ __device__ void scatter_chunk(const int (&ev)[kRounds], const float* __restrict_
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
     const int i = base + r * kPermThreads + threadIdx.x;
-    gv[r] = ev[r] >= 0 ? gates[i] : 0.f;
+    gv[r] = ev[r] >= 0 && gates ? gates[i] : 0.f;
   }
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
@@ -170,7 +170,7 @@ __device__ void scatter_chunk(const int (&ev)[kRounds], const float* __restrict_
       for (int w = 0; w < wave; ++w) pos += wcnt[w][e];
       sorted_src[pos] = i;
       inv[i] = pos;
-      row_gate[pos] = gv[r];
+      if (row_gate) row_gate[pos] = gv[r];
     }
     __syncthreads();
     for (int ee = threadIdx.x; ee < E; ee += kPermThreads) {
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(kPermThreads) void perm_single_kernel(
     int32_t* __restrict__ tile_off0, int bm1, int32_t* __restrict__ tile_off1,
     uint32_t* __restrict__ zero_words, int n_zero, int32_t* __restrict__ sorted_src,
     int32_t* __restrict__ inv, float* __restrict__ row_gate, BlockQuantArgs quant) {
-  if (blockIdx.x > 0) return block_quantise(quant, blockIdx.x - 1, gridDim.x - 1);
+  if (blockIdx.x > 0) return quantise_tokens(quant, blockIdx.x - 1, gridDim.x - 1);
   __shared__ int32_t cnt[256];
   __shared__ int32_t wcnt[kPermThreads / 64][256];
   __shared__ int tmp[kPermThreads / 64];
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kPermThreads) void perm_identity_kernel(
     uint32_t* __restrict__ zero_words, int n_zero, int32_t* __restrict__ sorted_src,
     int32_t* __restrict__ inv, float* __restrict__ row_gate, int groups, BlockQuantArgs quant) {
   if (static_cast<int>(blockIdx.x) >= groups)
-    return block_quantise(quant, blockIdx.x - groups, gridDim.x - groups);
+    return quantise_tokens(quant, blockIdx.x - groups, gridDim.x - groups);
   for (int i = blockIdx.x * kPermThreads + threadIdx.x; i < R; i += groups * kPermThreads) {
     sorted_src[i] = i;
     inv[i] = i;
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(kPermThreads) void perm_identity_kernel(
 hipError_t launch_permute_identity(int R, const PermBufs& p, hipStream_t stream) {
   int g = (R + kPermThreads - 1) / kPermThreads;
   g = g < 1 ? 1 : (g > 1024 ? 1024 : g);
-  hipLaunchKernelGGL(perm_identity_kernel, dim3(g + block_quant_groups(p.quant)), dim3(kPermThreads), 0,
+  hipLaunchKernelGGL(perm_identity_kernel, dim3(g + quant_groups(p.quant)), dim3(kPermThreads), 0,
                      stream, R, p.counts, p.offsets, p.bm0, p.tile_off0, p.bm1, p.tile_off1,
                      p.zero_words, p.n_zero, p.sorted_src, p.inv, p.row_gate, g, p.quant);
   return hipGetLastError();
@@ -277,7 +277,7 @@ hipError_t launch_permute(const int32_t* ids, const float* gates, int T, int E, 
                           const PermBufs& p, hipStream_t stream) {
   const int R = T * k;
   const int n_chunks = (R + kChunk - 1) / kChunk;
-  const int quant = block_quant_groups(p.quant);
+  const int quant = quant_groups(p.quant);
   if (n_chunks <= 1) {
     hipLaunchKernelGGL(perm_single_kernel, dim3(1 + quant), dim3(kPermThreads), 0, stream, ids, gates,
                        R, E, p.counts, p.offsets, p.bm0, p.tile_off0, p.bm1, p.tile_off1,
