@@ -30,6 +30,12 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return static_cast<uint16_t>(u >> 16);
 }
 
+// the same of two values, the first in the low half (hardware convert; a NaN stays one)
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
 // round a binary64 value directly to bf16 (nearest, ties to even), so that a
 // value computed exactly in double is rounded once.  Values below the bf16
 // normal range go through fp32 (they do not occur on the layer's data).

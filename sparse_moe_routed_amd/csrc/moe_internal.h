@@ -242,7 +242,7 @@ hipError_t launch_block_pack(const uint16_t* w, int E, int N, int K, uint8_t* co
                              hipStream_t stream);
 
 // 8-bit integers with a scale per token and channel (moe_channel_*, "int8" banks)
-// operands of nt.h's kernel
+// operands of the products of products.h
 struct NtArgs {
   int M, N, K;  // rows (of all groups), weight rows, values of K
   const uint8_t* a;
@@ -258,6 +258,7 @@ struct NtArgs {
   int top_k;
   const int32_t* w_slot;
   const float* row_gate;
+  int accumulate;  // kGradWeights: out += (fp32)
 };
 constexpr int kChannelMaxK = 1 << 16;  // sums of 127 * 127 (128 * 128 of foreign codes) fit int32
 constexpr int kChannelFewRows = 32;

@@ -26,6 +26,10 @@ __device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
 __device__ __forceinline__ void load16_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, at, step_at, 0, 0);
 }
+__device__ __forceinline__ void load16_to_lds(Buffer b, uint32_t at, uint32_t step_at,
+                                              __attribute__((address_space(3))) uint8_t* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, at, step_at, 0, 0);
+}
 __device__ __forceinline__ void load4_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 4, at, step_at, 0, 0);
 }
