@@ -508,6 +508,9 @@ int32_t moe_channel_linear(int32_t M, int32_t N, int32_t K, const void* x, const
  *           zero (zero_rest = 1)
  *   dw [dev] [E, N, K]: written in full (an expert without rows gets zeros, or with
  *           accumulate keeps its values)
+ *   ws [dev] 256-byte aligned, ws_bytes >= moe_grouped_weight_grad_workspace_size(R, E,
+ *           N, K); NULL will do where that is 256: sums are taken in parts only where the
+ *           experts' matrices are too small to fill the chip and the rows many
  *   *_dtype MOE_Y_BF16 or MOE_Y_F32
  * Products are exact and summed in fp32, in an order that depends on the sizes alone:
  * a call repeats bit for bit.  A row's result depends on that row and its expert's
@@ -530,7 +533,8 @@ int32_t moe_grouped_input_grad(int32_t R, int32_t E, int32_t N, int32_t K, const
                                void* stream);
 int32_t moe_grouped_weight_grad(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy, const void* x,
                                 const int32_t* offsets, void* dw, int32_t dw_dtype, int32_t accumulate,
-                                void* stream);
+                                void* ws, size_t ws_bytes, void* stream);
+size_t moe_grouped_weight_grad_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K);
 size_t moe_group_rows_workspace_size(int32_t E, int32_t max_rows);
 int32_t moe_group_rows(int32_t R, int32_t E, const int32_t* ids, int32_t* offsets, int32_t* sorted_src,
                        int32_t* inv, void* ws, size_t ws_bytes, void* stream);

@@ -145,8 +145,10 @@ _SIGS = {
                            + [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
     "moe_grouped_input_grad": (ctypes.c_int32, [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4
                                + [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "moe_grouped_weight_grad_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 4),
     "moe_grouped_weight_grad": (ctypes.c_int32, [ctypes.c_int32] * 4 + [ctypes.c_void_p] * 4
-                                + [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+                                + [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                                   ctypes.c_void_p]),
     "moe_group_rows_workspace_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "moe_group_rows": (ctypes.c_int32, [ctypes.c_int32] * 2 + [ctypes.c_void_p] * 5
                        + [ctypes.c_size_t, ctypes.c_void_p]),
@@ -1074,12 +1076,18 @@ def grouped_input_grad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     return dx
 
 
+@functools.lru_cache(maxsize=256)
+def _weight_grad_bytes(R: int, E: int, N: int, K: int) -> int:
+    return int(lib().moe_grouped_weight_grad_workspace_size(R, E, N, K))
+
+
 def grouped_weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
                         dw: Optional[torch.Tensor] = None, dw_dtype: Optional[torch.dtype] = None,
-                        accumulate: bool = False) -> torch.Tensor:
+                        accumulate: bool = False, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_grouped_weight_grad: dw [E, N, K] with dw[e] = dy[rows of e]^T x[rows of e],
     in bf16 (or dw_dtype); with accumulate added to the fp32 dw given.  dy bf16
-    [R, N], x bf16 [R, K]."""
+    [R, N], x bf16 [R, K].  ws: a uint8 workspace, allocated here where the sizes need
+    one and none is given."""
     R, N = _matrix(dy, torch.bfloat16, "dy").shape
     dev = dy.device
     _arg(x, torch.bfloat16, "x", (R, _matrix(x, torch.bfloat16, "x").shape[1]), dev)
@@ -1091,8 +1099,15 @@ def grouped_weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
     if accumulate and dw is None:
         raise ValueError("accumulate needs the dw to add to")
     dw, yd = _out(dw, dw_dtype, "dw", (E, N, K), dy)
+    if ws is not None:
+        _arg(ws, torch.uint8, "ws", getattr(ws, "shape", None), dev)
+    else:
+        n = _weight_grad_bytes(R, E, N, K)
+        if n > 256:
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
     _launch("moe_grouped_weight_grad", lib().moe_grouped_weight_grad, dev.index,
-            R, E, N, K, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), dw.data_ptr(), yd, 1 if accumulate else 0)
+            R, E, N, K, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), dw.data_ptr(), yd, 1 if accumulate else 0,
+            _p(ws), 0 if ws is None else ws.numel())
     return dw
 
 

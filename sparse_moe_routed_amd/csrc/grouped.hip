@@ -8,6 +8,7 @@
 // sum; in the others the sum runs over the rows of a matrix: of w for dx, of dy and x
 // for dw.
 #include "products.h"
+#include "small.h"
 #include "tile_gemm.h"
 
 namespace moe {
@@ -23,6 +24,23 @@ __global__ __launch_bounds__(256) void zero_rest_kernel(const int32_t* __restric
   for (size_t i = static_cast<size_t>(from) * row_bytes + (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
        i < end; i += static_cast<size_t>(gridDim.x) * 256 * 16)
     *reinterpret_cast<u32x4*>(out + i) = zero;
+}
+
+// dw of its parts [splits, n], added up in their order
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ parts, int splits, size_t n,
+                                                   void* __restrict__ out, int out_f32, int accumulate) {
+  for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+       i += static_cast<size_t>(gridDim.x) * 1024) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(parts + s * n + i);
+    if (out_f32) {
+      f32x4* const o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + i);
+      *o = accumulate ? v + *o : v;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + i) =
+          make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+    }
+  }
 }
 
 hipError_t launch_zero_rest(const GroupedArgs& g, int width, hipStream_t stream) {
@@ -48,26 +66,67 @@ NtArgs product_args(const GroupedArgs& g, const void* rows, const void* cols) {
 
 }  // namespace
 
-// Tiles of 256 rows read each weight once where an expert has no more rows; tiles of 64
-// are three or four to a CU and keep more bytes under way.
+// tiles of 256 x 256 that full rows would make: fewer leave CUs idle
+constexpr int kFillLarge = 128;
+long long large_tiles(int R, int width) {
+  return static_cast<long long>((R + 255) / 256) * ((width + 255) / 256);
+}
+
+// Few rows, whose tiles of 64 x 128 would leave most CUs without one: 32 columns a
+// workgroup and the sum dealt to its waves.  Then tiles of 64 rows, three to a CU, which
+// keep more bytes of weights under way, until experts have more rows than such a tile
+// often enough; tiles of 256 rows read each weight once.
 hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t stream) {
   const NtArgs a = product_args(g, g.x, g.w);
-  const hipError_t err = g.R < 96 * g.E ? launch_tile<NtBf16, kNtGroups, 64, 128, 1, 4, 2, 2>(a, stream)
-                                        : launch_tile<NtBf16, kNtGroups, 256, 256, 2, 4, 2, 2>(a, stream);
+  const int experts = g.R < g.E ? g.R : g.E;  // at most, with rows
+  hipError_t err;
+  if (g.R <= 256 && ((g.R + 63) / 64 + experts) * ((g.N + 127) / 128) < 128)
+    err = g.R <= 16 ? launch_small<NtBf16, kNtGroups, 1, false>(a, stream)
+                    : launch_small<NtBf16, kNtGroups, 4, false>(a, stream);
+  else if (g.R < 96 * g.E || large_tiles(g.R, g.N) < kFillLarge)
+    err = launch_tile<NtBf16, kNtGroups, 64, 128, 1, 4, 2, 2>(a, stream);
+  else err = launch_tile<NtBf16, kNtGroups, 256, 256, 2, 4, 2, 2>(a, stream);
   return err == hipSuccess && g.zero_rest ? launch_zero_rest(g, g.N, stream) : err;
 }
 
 hipError_t launch_grouped_input_grad(const GroupedArgs& g, hipStream_t stream) {
   const NtArgs a = product_args(g, g.dy, g.w);
   hipError_t err;
-  if (g.R < 16 * g.E) err = launch_tile<NtBf16, kGradRows, 64, 128, 1, 4, 1, 4>(a, stream);
+  if (g.R < 16 * g.E || large_tiles(g.R, g.K) < kFillLarge)
+    err = launch_tile<NtBf16, kGradRows, 64, 128, 1, 4, 1, 4>(a, stream);
   else if (g.R < 320 * g.E) err = launch_tile<NtBf16, kGradRows, 256, 256, 2, 4, 1, 4>(a, stream);
   else err = launch_tile<NtBf16, kGradRows, 256, 256, 2, 4, 2, 2>(a, stream);
   return err == hipSuccess && g.zero_rest ? launch_zero_rest(g, g.K, stream) : err;
 }
 
+// dw: parts of an expert's rows side by side where the experts' tiles are too few for the
+// chip and the rows many (128 rows a part at least), each a sum of its own, joined in order
+constexpr int kDwRows = 128, kDwCols = 256;
+int weight_grad_splits(int R, int E, int N, int K) {
+  const long long tiles = static_cast<long long>(E) * ((N + kDwRows - 1) / kDwRows) * ((K + kDwCols - 1) / kDwCols);
+  const long long by_tiles = 256 / tiles, by_rows = R / (128ll * E);
+  const long long s = by_tiles < by_rows ? by_tiles : by_rows;
+  return s < 2 ? 1 : static_cast<int>(s < 64 ? s : 64);
+}
+
 hipError_t launch_grouped_weight_grad(const GroupedArgs& g, hipStream_t stream) {
-  return launch_tile<NtBf16, kGradWeights, 128, 256, 1, 4, 1, 3>(product_args(g, g.dy, g.x), stream);
+  NtArgs a = product_args(g, g.dy, g.x);
+  a.splits = weight_grad_splits(g.R, g.E, g.N, g.K);
+  // rows worth reading ahead, and that the last-level cache (256 MB) can hold
+  const size_t bytes = static_cast<size_t>(g.R) * (g.N + g.K) * 2;
+  a.warm = bytes >= (32u << 20) && bytes <= (240u << 20) ? 32 : 0;
+  if (a.splits > 1) {
+    a.out = g.partial;
+    a.out_f32 = 1;
+    a.accumulate = 0;
+  }
+  const hipError_t err = launch_tile<NtBf16, kGradWeights, kDwRows, kDwCols, 1, 4, 1, 3>(a, stream);
+  if (err != hipSuccess || a.splits == 1) return err;
+  const size_t n = static_cast<size_t>(g.E) * g.N * g.K;
+  const size_t groups = (n / 4 + 255) / 256;
+  hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(groups < 4096 ? groups : 4096)), dim3(256), 0, stream,
+                     g.partial, a.splits, n, g.out, g.out_f32, g.accumulate);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -1365,18 +1365,30 @@ int32_t moe_grouped_input_grad(int32_t R, int32_t E, int32_t N, int32_t K, const
   return grouped_rows_call(R, E, N, K, dy, w, offsets, dx, dx_dtype, zero_rest, stream, true);
 }
 
+size_t moe_grouped_weight_grad_workspace_size(int32_t R, int32_t E, int32_t N, int32_t K) {
+  if (grouped_dims_check(R, E, N, K) != MOE_OK) return 0;
+  const int splits = moe::weight_grad_splits(R, E, N, K);
+  return kAlign + (splits > 1 ? static_cast<size_t>(splits) * E * N * K * 4 : 0);
+}
+
 int32_t moe_grouped_weight_grad(int32_t R, int32_t E, int32_t N, int32_t K, const void* dy, const void* x,
                                 const int32_t* offsets, void* dw, int32_t dw_dtype, int32_t accumulate,
-                                void* stream) {
+                                void* ws, size_t ws_bytes, void* stream) {
   if (const moe_status cs = grouped_dims_check(R, E, N, K)) return cs;
   if (dw_dtype != MOE_Y_BF16 && dw_dtype != MOE_Y_F32) return MOE_EINVAL;
   if ((accumulate != 0 && accumulate != 1) || (accumulate && dw_dtype != MOE_Y_F32)) return MOE_EINVAL;
   if (!offsets || !dw || (R > 0 && (!dy || !x))) return MOE_EINVAL;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16) || !aligned(offsets, 4)) return MOE_EINVAL;
   const size_t rows = static_cast<size_t>(R);
-  if (overlaps_any({dw, static_cast<size_t>(E) * N * K * (dw_dtype == MOE_Y_F32 ? 4 : 2)},
-                   {{dy, rows * N * 2}, {x, rows * K * 2}, {offsets, (static_cast<size_t>(E) + 1) * 4}}))
-    return MOE_EINVAL;
+  const Bytes bd{dy, rows * N * 2}, bx{x, rows * K * 2}, bo{offsets, (static_cast<size_t>(E) + 1) * 4};
+  const Bytes bw{dw, static_cast<size_t>(E) * N * K * (dw_dtype == MOE_Y_F32 ? 4 : 2)};
+  if (overlaps_any(bw, {bd, bx, bo})) return MOE_EINVAL;
+  const bool parts = moe::weight_grad_splits(R, E, N, K) > 1;
+  if (parts) {
+    const size_t need = moe_grouped_weight_grad_workspace_size(R, E, N, K);
+    if (!ws || ws_bytes < need || !aligned(ws, kAlign)) return MOE_EWORKSPACE;
+    if (overlaps_any({ws, need}, {bd, bx, bo, bw})) return MOE_EINVAL;
+  }
   if (R == 0 && accumulate) return MOE_OK;
   moe::GroupedArgs g{};
   g.R = R;
@@ -1389,6 +1401,7 @@ int32_t moe_grouped_weight_grad(int32_t R, int32_t E, int32_t N, int32_t K, cons
   g.out = dw;
   g.out_f32 = dw_dtype == MOE_Y_F32;
   g.accumulate = accumulate;
+  g.partial = parts ? static_cast<float*>(ws) : nullptr;
   return hip_status(moe::launch_grouped_weight_grad(g, static_cast<hipStream_t>(stream)));
 }
 

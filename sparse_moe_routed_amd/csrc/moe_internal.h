@@ -259,6 +259,8 @@ struct NtArgs {
   const int32_t* w_slot;
   const float* row_gate;
   int accumulate;  // kGradWeights: out += (fp32)
+  int warm;        // kGradWeights: workgroups that read the rows ahead
+  int splits;      // kGradWeights: parts of an expert's rows, a result of each in out
 };
 constexpr int kChannelMaxK = 1 << 16;  // sums of 127 * 127 (128 * 128 of foreign codes) fit int32
 constexpr int kChannelFewRows = 32;
@@ -282,7 +284,9 @@ struct GroupedArgs {
   int out_f32;
   int zero_rest;   // rows of no expert become zero (matmul, input_grad)
   int accumulate;  // add to out (weight_grad, fp32)
+  float* partial;  // weight_grad: [splits, E, N, K] of weight_grad_splits
 };
+int weight_grad_splits(int R, int E, int N, int K);
 hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t stream);
 hipError_t launch_grouped_input_grad(const GroupedArgs& g, hipStream_t stream);
 hipError_t launch_grouped_weight_grad(const GroupedArgs& g, hipStream_t stream);

@@ -315,6 +315,13 @@ __device__ __forceinline__ void store_tile(const NtArgs& g, const StoreAt& t, Bu
   }
 }
 
+template <int MODE, int BM, int BN>
+long long row_tiles(const NtArgs& g) {
+  const long long n_nt = (g.N + BN - 1) / BN;
+  if (MODE != kNtDense) return group_tiles(g.M, g.E, BM, n_nt);
+  return (n_nt * ((g.M + BM - 1) / BM) + 7) / 8 * 8;
+}
+
 // with timing events the kernel's own start and end are stamped
 template <typename Args>
 hipError_t launch_tiles(const void* kernel, long long blocks, int threads, const Args& g, hipStream_t stream,

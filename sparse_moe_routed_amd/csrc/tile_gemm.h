@@ -58,10 +58,16 @@ __device__ __forceinline__ bool tile_find(const NtArgs& g, TileAt2& t) {
     // a row of tiles of one expert is one XCD's, the rows of tiles go round: experts
     // of many rows are then shared by all
     const int n_rt = (g.N + BM - 1) / BM, n_ct = (g.K + BN - 1) / BN;
-    const int l = blockIdx.x >> 3, panel = l / n_ct * 8 + (blockIdx.x & 7), ct = l % n_ct;
-    if (panel >= g.E * n_rt) return false;
-    const int e = panel / n_rt, rt = panel - e * n_rt;
-    const int lo = min(max(g.offsets[e], 0), g.M), hi = min(max(g.offsets[e + 1], 0), g.M);
+    const int b = blockIdx.x - g.warm, l = b >> 3, panel = l / n_ct * 8 + (b & 7), ct = l % n_ct;
+    if (panel >= g.E * g.splits * n_rt) return false;
+    const int es = panel / n_rt, rt = panel - es * n_rt, e = es / g.splits, split = es - e * g.splits;
+    int lo = min(max(g.offsets[e], 0), g.M), hi = min(max(g.offsets[e + 1], 0), g.M);
+    if (g.splits > 1) {  // a part of the expert's rows, whole stages of them
+      const int part = (max(hi - lo, 0) + g.splits * 32 - 1) / (g.splits * 32) * 32;
+      const int from = min(lo + split * part, hi);
+      hi = min(from + part, hi);
+      lo = from;
+    }
     const int first = __builtin_amdgcn_readfirstlane(lo);
     t.length = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
     if (t.length == 0 && g.accumulate) return false;
@@ -74,7 +80,7 @@ __device__ __forceinline__ bool tile_find(const NtArgs& g, TileAt2& t) {
     t.a = g.a + static_cast<size_t>(first) * t.a_stride + t.row0 * 2;
     t.b = g.w + static_cast<size_t>(first) * t.b_stride + t.n0 * 2;
     t.ldo = g.K;
-    t.out = (static_cast<size_t>(e) * g.N + t.row0) * g.K + t.n0;
+    t.out = ((static_cast<size_t>(split) * g.E + e) * g.N + t.row0) * g.K + t.n0;
   } else {
     const int width = MODE == kGradRows ? g.K : g.N;  // of the output
     t.length = MODE == kGradRows ? g.N : g.K;
@@ -148,6 +154,35 @@ __device__ __forceinline__ i32x4 descriptor(const uint8_t* p, uint32_t bytes) {
                uniform(static_cast<int>(bytes)), kRawBuffer};
 }
 
+// Reads all rows of dy and x once, expert after expert, g.warm workgroups side by side,
+// and drops them: they are in the last-level cache then, where the tiles find them.
+// A tile's own loads are a few stages ahead of its products, which is too little for
+// memory that is busy with the writes of dw.
+__device__ __forceinline__ void warm_rows(const NtArgs& g, Lds to, int waves) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t mine = (blockIdx.x * waves + wave) * 1024u + lane * 16u, all = g.warm * waves * 1024u;
+  const Lds at = to + wave * 1024;
+  const auto read = [&](const uint8_t* p, size_t bytes) __attribute__((always_inline)) {
+    constexpr uint32_t kPart = 1u << 30;  // of a descriptor
+    for (size_t base = 0; base < bytes; base += kPart) {
+      const uint32_t n = static_cast<uint32_t>(bytes - base < kPart ? bytes - base : kPart);
+      const i32x4 d = descriptor(p + base, n);
+      for (uint32_t o = 0; o < n; o += all) {
+        dma16(d, mine, o, at);
+        __asm__ volatile("s_waitcnt vmcnt(24)" ::: "memory");
+      }
+    }
+  };
+  const int E = g.E;
+  for (int e = 0; e < E; ++e) {
+    const int lo = uniform(min(max(g.offsets[e], 0), g.M)), hi = uniform(min(max(g.offsets[e + 1], 0), g.M));
+    if (hi <= lo) continue;
+    read(g.w + static_cast<size_t>(lo) * g.K * 2, static_cast<size_t>(hi - lo) * g.K * 2);
+    read(g.a + static_cast<size_t>(lo) * g.N * 2, static_cast<size_t>(hi - lo) * g.N * 2);
+  }
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 // chunk x of row r of a contiguous operand lies at x ^ row_swz(r): 16 rows of an operand
 // read fall on distinct banks
 template <int KH>
@@ -170,6 +205,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
   static_assert((AF != kTurned || BM >= 128) && (BF != kTurned || BN >= 128), "a turned row covers the banks");
   static_assert((KH == 1 || KH == 2) && NBUF >= 2 && NBUF * BUF <= 160 * 1024 && (NBUF - 1) * kLoads < 64, "buffers");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * BUF];
+  if (MODE == kGradWeights && static_cast<int>(blockIdx.x) < g.warm) {
+    warm_rows(g, (Lds)lds, NW);
+    return;
+  }
   TileAt2 t;
   if (!tile_find<T, MODE, BM, BN>(g, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -362,7 +401,7 @@ template <typename T, int MODE, int BM, int BN, int WM, int WN, int KH, int NBUF
 hipError_t launch_tile(const NtArgs& g, hipStream_t stream, const KernelEvents& ev = KernelEvents{}) {
   const long long width = MODE >= kGradRows ? g.K : g.N, n_ct = (width + BN - 1) / BN;
   long long blocks;
-  if (MODE == kGradWeights) blocks = (g.E * static_cast<long long>((g.N + BM - 1) / BM) + 7) / 8 * 8 * n_ct;
+  if (MODE == kGradWeights) blocks = (g.E * static_cast<long long>(g.splits) * ((g.N + BM - 1) / BM) + 7) / 8 * 8 * n_ct + g.warm;
   else if (MODE == kNtDense) blocks = (n_ct * ((g.M + BM - 1) / BM) + 7) / 8 * 8;
   else blocks = group_tiles(g.M, g.E, BM, n_ct);
   return launch_tiles(reinterpret_cast<const void*>(&tile_kernel<T, MODE, BM, BN, WM, WN, KH, NBUF>), blocks, WM * WN * 64, g,

@@ -29,8 +29,8 @@ def test_validation():
             for bad in (a, a + 40 * rows * 2 - 16, w + 4 * 64 * 128 * 2 - 16, o - 40 * out * size + 16, o):
                 assert call(y=bad, yd=yd) == moe.EINVAL, hex(bad)
 
-    def dw(R=40, E=4, N=64, K=128, dy=a, x=w, o=o, dw=y, d=0, acc=0):
-        return L.moe_grouped_weight_grad(R, E, N, K, dy, x, o, dw, d, acc, None)
+    def dw(R=40, E=4, N=64, K=128, dy=a, x=w, o=o, dw=y, d=0, acc=0, ws=None, nb=0):
+        return L.moe_grouped_weight_grad(R, E, N, K, dy, x, o, dw, d, acc, ws, nb, None)
 
     for bad in (dict(R=-1), dict(E=0), dict(dy=None), dict(x=None), dict(o=None), dict(dw=None), dict(dy=a + 8),
                 dict(x=w + 8), dict(o=o + 1), dict(dw=y + 8), dict(d=2), dict(acc=2), dict(acc=1),
@@ -39,6 +39,16 @@ def test_validation():
     for bad in (dict(E=257), dict(N=60), dict(K=130), dict(R=(1 << 23) + 1)):
         assert dw(**bad) == moe.EUNSUPPORTED, bad
     assert dw(R=0, dy=None, x=None, d=1, acc=1) == moe.OK  # nothing to add
+    # parts of the rows where the matrices are few and small
+    size = L.moe_grouped_weight_grad_workspace_size
+    assert size(40, 4, 64, 128) == 256 and size(24576, 128, 1856, 2688) == 256 and size(40, 4, 60, 128) == 0
+    need = size(8192, 1, 64, 128)
+    assert need > 256 and (need - 256) % (64 * 128 * 4) == 0
+    big, ws = dict(R=8192, E=1), FAKE + (5 << 24)
+    for bad in (dict(), dict(ws=ws, nb=need - 1), dict(ws=ws + 16, nb=need)):
+        assert dw(**big, **bad) == moe.EWORKSPACE, bad
+    for bad in (a, a + 8192 * 128 - 256, w, y, o - need + 256):
+        assert dw(**big, ws=bad, nb=need) == moe.EINVAL, hex(bad)
 
 
 def test_validation_of_group_rows():
@@ -133,7 +143,9 @@ SHAPES = [
     ("skew", 100, 16, 136, 72, 20), ("skew", 300, 7, 200, 264, 300), ("one", 257, 3, 128, 128, 1),
     ("even", 511, 1, 1000, 200, 0), ("skew", 700, 256, 64, 96, 5), ("even", 1000, 4, 512, 1024, 0),
     ("skew", 2500, 16, 320, 192, 77), ("one", 1300, 256, 256, 384, 0), ("skew", 4000, 3, 1856, 88, 0),
-    ("skew", 6000, 8, 264, 1352, 130),
+    ("skew", 6000, 8, 264, 1352, 130), ("skew", 5, 16, 1000, 392, 0), ("skew", 40, 3, 200, 1352, 9),
+    ("even", 64, 1, 72, 2688, 0), ("one", 8000, 1, 64, 72, 0), ("skew", 9001, 2, 136, 264, 5),
+    ("one", 5000, 3, 256, 128, 0),
 ]
 
 
