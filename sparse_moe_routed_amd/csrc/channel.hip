@@ -286,20 +286,39 @@ hipError_t launch_channel_tile(const NtArgs& g, hipStream_t stream, const Kernel
 
 }  // namespace
 
+// Rows of a tile near what an expert has: the fewer, the more workgroups share the
+// streaming of the weights, the more the fewer times each is read.  The layer of 128
+// experts, 2688 x 1856, 6 a token, us with tiles of 32 x 64, 64 x 128 and 128 x 128: 384
+// rows 199, 222 and 257; 2400 rows 263, 283 and 298; 6000 rows 539, 330 and 345; 9000
+// rows 626, 390 and 381; 24576 rows 1157, 661 and 656.
 hipError_t launch_channel_experts(int stage, const NtArgs& g, hipStream_t stream, const KernelEvents& ev) {
-  if (g.M < (16 * g.E > 256 ? 16 * g.E : 256))
+  if (g.M < (24 * g.E > 256 ? 24 * g.E : 256))
     return stage == 0 ? launch_channel_tile<kNtUp, 32, 64, 1, 4, 4, 4, true>(g, stream, ev)
                       : launch_channel_tile<kNtDown, 32, 64, 1, 4, 4, 4, true>(g, stream, ev);
+  if (g.M < 56 * g.E)
+    return stage == 0 ? launch_channel_tile<kNtUp, 64, 128, 1, 4, 4, 4>(g, stream, ev)
+                      : launch_channel_tile<kNtDown, 64, 128, 1, 4, 4, 4>(g, stream, ev);
   return stage == 0 ? launch_channel_tile<kNtUp, 128, 128, 1, 4, 4, 4>(g, stream, ev)
                     : launch_channel_tile<kNtDown, 128, 128, 1, 4, 4, 4>(g, stream, ev);
 }
 
-constexpr int kFill = 200;  // tiles that fill the chip
+// Tiles by size, us measured at N x K:
+//   - few rows: 32 columns a workgroup and the sum dealt to its waves, for up to 32 rows
+//     (14336 x 4096, 1 row 10.1, in tiles of 64 x 64 11.7) and, while one round of
+//     workgroups covers the columns, up to 128 (3712 x 2688, 100 rows 7.3 and 8.6; but
+//     14336 x 4096 32 and 18);
+//   - then the largest tile of which there are kFill, which reads least from the caches
+//     for each product.  2688 x 1856: 1024 rows 10.6 in the 168 tiles of 128 x 128, 15.6
+//     in 64 x 128; 1500 rows 11.7 in 128 x 128, 15.7 in the 132 of 128 x 256; 2048 rows
+//     16.3 in 176 of those and 19.2; 4096 rows 28.5 in 176 of 256 x 256, 32 in 128 x 256.
+constexpr int kFill = 140;
 hipError_t launch_channel_dense(const NtArgs& g, hipStream_t stream) {
   if (g.M <= 16) return launch_small<NtInt8, kNtDense, 1, false>(g, stream);
   if (g.M <= 32) return launch_small<NtInt8, kNtDense, 2, false>(g, stream);
-  if (g.M <= 64) return launch_small<NtInt8, kNtDense, 4, false>(g, stream);
-  if (g.M <= 128) return launch_small<NtInt8, kNtDense, 4, false, false>(g, stream);  // two row tiles
+  if (g.N <= 256 * kSmallN) {
+    if (g.M <= 64) return launch_small<NtInt8, kNtDense, 4, false>(g, stream);
+    if (g.M <= 128) return launch_small<NtInt8, kNtDense, 4, false, false>(g, stream);  // two row tiles
+  }
   const auto fills = [&](long long bm, long long bn) {
     return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn) >= kFill;
   };

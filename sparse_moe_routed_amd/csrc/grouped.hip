@@ -66,33 +66,49 @@ NtArgs product_args(const GroupedArgs& g, const void* rows, const void* cols) {
 
 }  // namespace
 
-// tiles of 256 x 256 that full rows would make: fewer leave CUs idle
-constexpr int kFillLarge = 128;
+// tiles of 256 x 256 that full rows would make
 long long large_tiles(int R, int width) {
   return static_cast<long long>((R + 255) / 256) * ((width + 255) / 256);
 }
 
-// Few rows, whose tiles of 64 x 128 would leave most CUs without one: 32 columns a
-// workgroup and the sum dealt to its waves.  Then tiles of 64 rows, three to a CU, which
-// keep more bytes of weights under way, until experts have more rows than such a tile
-// often enough; tiles of 256 rows read each weight once.
+// Tiles by size, measured at N = 1856 and K = 2688:
+//   - few rows, whose tiles of 64 x 128 would leave many CUs without one: 32 columns a
+//     workgroup and the sum dealt to its waves (1 row 8.7 us, in tiles 15.5; 64 rows of 8
+//     experts 20 and 25; but 24 rows of 128 experts 53 and 41);
+//   - 256 x 256, which read least from the caches for each product, where the experts have
+//     rows for them and the chip enough of them (192 rows an expert of 128: 315 us, 393 in
+//     128 x 128; 8192 rows of one 68 and 81; but 128 rows an expert 289 and 279, and 4096
+//     rows of one expert, 128 tiles, 56 and 42);
+//   - 128 x 128 where there are enough of those (1500 rows of 128 experts 225 us, 230 in
+//     64 x 128; 4096 of one 42 and 66);
+//   - 64 x 128 for the rest, three workgroups to a CU (1500 rows of one expert 28 us, 31
+//     in 128 x 128; 24 rows of 128 experts 41 and 44).
 hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t stream) {
   const NtArgs a = product_args(g, g.x, g.w);
   const int experts = g.R < g.E ? g.R : g.E;  // at most, with rows
+  const long long cols = (g.N + 127) / 128;
   hipError_t err;
-  if (g.R <= 256 && ((g.R + 63) / 64 + experts) * ((g.N + 127) / 128) < 128)
-    err = g.R <= 16 ? launch_small<NtBf16, kNtGroups, 1, false>(a, stream)
+  if (g.R <= 256 && ((g.R + 63) / 64 + experts) * cols < 160)
+    err = g.R <= 64 ? launch_small<NtBf16, kNtGroups, 1, false>(a, stream)
                     : launch_small<NtBf16, kNtGroups, 4, false>(a, stream);
-  else if (g.R < 96 * g.E || large_tiles(g.R, g.N) < kFillLarge)
-    err = launch_tile<NtBf16, kNtGroups, 64, 128, 1, 4, 2, 2>(a, stream);
-  else err = launch_tile<NtBf16, kNtGroups, 256, 256, 2, 4, 2, 2>(a, stream);
+  else if (g.R >= 144 * g.E && large_tiles(g.R, g.N) >= 160)
+    err = launch_tile<NtBf16, kNtGroups, 256, 256, 2, 4, 2, 2>(a, stream);
+  else if (g.R >= 4 * g.E && (g.R / 128 + experts) * cols >= 320)
+    err = launch_tile<NtBf16, kNtGroups, 128, 128, 2, 2, 2, 2>(a, stream);
+  else err = launch_tile<NtBf16, kNtGroups, 64, 128, 1, 4, 2, 2>(a, stream);
   return err == hipSuccess && g.zero_rest ? launch_zero_rest(g, g.N, stream) : err;
 }
 
+// As above, but w's tile is read turned, a stage of 32 of its rows: four of them in LDS
+// beat two of 64 until the matrix instructions bind (192 rows an expert of 128 317 us and
+// 322, 512 rows 638 and 618; 8192 rows of 8 experts 97 and 89).  64 x 128 for few rows:
+// 1500 rows of 128 experts 221 us, 228 in 256 x 256; 12288 rows 334 and 270; 1000 rows of
+// one expert 23 us, 2048 rows 34, where 256 x 256 have too few tiles.  128 x 128 beat
+// neither (12288 rows 267 us, 1500 rows 236).
 hipError_t launch_grouped_input_grad(const GroupedArgs& g, hipStream_t stream) {
   const NtArgs a = product_args(g, g.dy, g.w);
   hipError_t err;
-  if (g.R < 16 * g.E || large_tiles(g.R, g.K) < kFillLarge)
+  if (g.R < 16 * g.E || large_tiles(g.R, g.K) < 128)
     err = launch_tile<NtBf16, kGradRows, 64, 128, 1, 4, 1, 4>(a, stream);
   else if (g.R < 320 * g.E) err = launch_tile<NtBf16, kGradRows, 256, 256, 2, 4, 1, 4>(a, stream);
   else err = launch_tile<NtBf16, kGradRows, 256, 256, 2, 4, 2, 2>(a, stream);

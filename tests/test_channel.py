@@ -227,7 +227,8 @@ def _same(got, want):
 SHAPES = [(1, 1, 16), (1, 3712, 2688), (3, 37, 64), (7, 130, 144), (16, 64, 128), (17, 33, 1856),
           (32, 200, 400), (33, 64, 2688), (77, 301, 336), (128, 129, 256), (129, 130, 144), (200, 1, 128),
           (300, 515, 1856), (513, 768, 208), (2900, 3000, 80), (4096, 1856, 320), (150, 1000, 2688),
-          (500, 3700, 2000), (1000, 3700, 1840), (1500, 9000, 400), (2, 40, 8192), (40, 40, 8192)]
+          (500, 3700, 2000), (1000, 3700, 1840), (1500, 9000, 400), (2, 40, 8192), (40, 40, 8192), (40, 8200, 144),
+          (100, 8200, 144), (1100, 4400, 80), (1100, 2300, 80), (600, 2300, 96)]
 
 
 @pytest.mark.gpu

@@ -145,7 +145,9 @@ SHAPES = [
     ("skew", 2500, 16, 320, 192, 77), ("one", 1300, 256, 256, 384, 0), ("skew", 4000, 3, 1856, 88, 0),
     ("skew", 6000, 8, 264, 1352, 130), ("skew", 5, 16, 1000, 392, 0), ("skew", 40, 3, 200, 1352, 9),
     ("even", 64, 1, 72, 2688, 0), ("one", 8000, 1, 64, 72, 0), ("skew", 9001, 2, 136, 264, 5),
-    ("one", 5000, 3, 256, 128, 0),
+    ("one", 5000, 3, 256, 128, 0), ("skew", 5200, 3, 2056, 72, 30), ("skew", 5200, 3, 72, 2056, 30),
+    ("skew", 5200, 20, 136, 2056, 30), ("skew", 700, 16, 2056, 104, 9), ("one", 700, 16, 1856, 136, 0),
+    ("skew", 6000, 4, 1000, 1800, 0), ("even", 24001, 1, 360, 368, 0),
 ]
 
 
