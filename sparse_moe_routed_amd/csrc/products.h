@@ -128,7 +128,6 @@ __device__ __forceinline__ void nt_store(const NtArgs& g, size_t at, int width, 
   if constexpr (F32) {
     float* const o = static_cast<float*>(g.out) + at;
     if constexpr (WHOLE) {
-      if (MODE == kGradWeights && g.accumulate) h += *reinterpret_cast<const f32x4*>(o);
       *reinterpret_cast<f32x4*>(o) = h;
     } else {
 #pragma unroll

@@ -26,10 +26,6 @@ __device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
 __device__ __forceinline__ void load16_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, at, step_at, 0, 0);
 }
-__device__ __forceinline__ void load16_to_lds(Buffer b, uint32_t at, uint32_t step_at,
-                                              __attribute__((address_space(3))) uint8_t* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, at, step_at, 0, 0);
-}
 __device__ __forceinline__ void load4_to_lds(Buffer b, uint32_t at, uint32_t step_at, uint8_t* to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 4, at, step_at, 0, 0);
 }
@@ -85,14 +81,16 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* __restrict__ offs
     upto[q] = wave_scan((count[q] + BM - 1) / BM) + total;
     total = __builtin_amdgcn_readlane(upto[q], 63);
   }
-  const int tiles = total * n_nt, per_xcd = (tiles + 7) >> 3;
+  // (groups that overlap may have more tiles than the launch: those past its bound are left)
+  const int tiles = min(total, (R + BM - 1) / BM + min(R, E)) * n_nt, per_xcd = (tiles + 7) >> 3;
   const int local = blockIdx.x >> 3;
   const int logical = (blockIdx.x & 7) * per_xcd + local;
   if (local >= per_xcd || logical >= tiles) return false;
+  const int panel = logical / n_nt;
   int e = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    if (64 * q < E) e += __popcll(__ballot(64 * q + lane < E && upto[q] * n_nt <= logical));
+    if (64 * q < E) e += __popcll(__ballot(64 * q + lane < E && upto[q] <= panel));
   e = __builtin_amdgcn_readfirstlane(e);
   int lo = 0, n = 0, last = 0;
 #pragma unroll

@@ -35,7 +35,7 @@ struct TileAt2 {
   int length;       // of the sum, in values
   const uint8_t *a, *b;
   uint32_t a_stride, b_stride;  // bytes between rows of memory
-  uint32_t a_bytes;             // contiguous rows: bytes from a on
+  uint32_t a_bytes;             // of contiguous rows
   size_t out;                   // first value of the output tile
   int ldo;                      // values between rows of the output
   const float* w_s;
@@ -106,13 +106,9 @@ __device__ __forceinline__ bool tile_find(const NtArgs& g, TileAt2& t) {
     t.n0 = nt * BN;
     t.cols = min(BN, width - t.n0);
     t.a_stride = t.length * T::kBytes;
-    // gathered rows are addressed from the first row (fewer than 2^32 bytes, checked by
-    // the caller), others from the tile's first
-    const size_t first = MODE == kNtUp ? 0 : static_cast<size_t>(t.row0);
-    t.a = g.a + first * t.a_stride;
-    t.a_bytes = static_cast<uint32_t>(static_cast<size_t>(MODE == kNtUp ? g.a_rows : t.rows) * t.a_stride);
-    const int ew = (MODE == kNtUp || MODE == kNtDown) && g.w_slot ? g.w_slot[e] : e;
-    const uint8_t* const w = g.w + static_cast<size_t>(ew) * nt_matrix_bytes<T>(g.N, g.K);
+    t.a = g.a + static_cast<size_t>(t.row0) * t.a_stride;
+    t.a_bytes = static_cast<uint32_t>(t.rows) * t.a_stride;
+    const uint8_t* const w = g.w + static_cast<size_t>(e) * nt_matrix_bytes<T>(g.N, g.K);
     if constexpr (MODE == kGradRows) {
       t.b_stride = g.K * 2u;
       t.b = w + t.n0 * 2;
@@ -122,7 +118,7 @@ __device__ __forceinline__ bool tile_find(const NtArgs& g, TileAt2& t) {
     }
     t.ldo = width;
     t.out = static_cast<size_t>(t.row0) * width + t.n0;
-    t.w_s = T::kBytes == 1 ? g.w_s + static_cast<size_t>(e) * g.N : nullptr;
+    t.w_s = g.w_s;
   }
   t.a = uniform(t.a);
   t.b = uniform(t.b);
@@ -140,9 +136,12 @@ __device__ __forceinline__ bool tile_find(const NtArgs& g, TileAt2& t) {
 // 16 bytes a lane from memory straight into LDS, 1 KB from `to` on.  In assembly because
 // the compiler, which cannot tell the two buffers apart in every form of read, would
 // wait for all of them before the next read; the waits are the step's own.  A load
-// past the descriptor's end writes zeros.
+// past the descriptor's end writes zeros.  The compiler does not look into the assembly
+// either for what the scalar operands need: five wait states between a vector
+// instruction (a readfirstlane) that writes one and the load that reads it, one
+// after m0.
 __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t at, uint32_t step_at, Lds to) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                        uniform(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)))),
                    "v"(at), "s"(rsrc), "s"(uniform(step_at))
                    : "memory");
@@ -203,6 +202,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
   constexpr int kStep = kRow / T::kBytes;  // values of the sum
   static_assert(QA * NW * 1024 == ABYTES && QB * NW * 1024 == BBYTES, "tile");
   static_assert((AF != kTurned || BM >= 128) && (BF != kTurned || BN >= 128), "a turned row covers the banks");
+  static_assert(MODE == kNtDense || MODE == kNtGroups || MODE >= kGradRows, "rows as they lie");
+  static_assert(BF != kPackedForm || KH == 2, "whole steps of packed weights");
   static_assert((KH == 1 || KH == 2) && NBUF >= 2 && NBUF * BUF <= 160 * 1024 && (NBUF - 1) * kLoads < 64, "buffers");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NBUF * BUF];
   if (MODE == kGradWeights && static_cast<int>(blockIdx.x) < g.warm) {
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
       const int col = (((ch >> 1) ^ tr_swz(k)) << 4) + ((ch & 1) << 3);  // first of 8 columns
       return col < valid ? k * stride + col * 2u : kPastEnd;
     } else if constexpr (kForm == kPackedForm) {
-      return KH == 1 ? p * stride + lane * 16u : (p >> 1) * stride + (p & 1) * 1024u + lane * 16u;
+      return (p >> 1) * stride + (p & 1) * 1024u + lane * 16u;
     } else {
       const int r = p * kRows + lane / kChunks;
       return r * stride + ((lane % kChunks) ^ row_swz<KH>(r)) * 16u;
@@ -240,20 +241,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
   static_assert(KH == 1 || NW % 2 == 0, "contiguous rows and packed groups move alike");
   const uint32_t apart_a = AF == kTurned ? NW * 512 / BM * t.a_stride : NW * kRows * t.a_stride;
   const uint32_t apart_b =
-      BF == kTurned ? NW * 512 / BN * t.b_stride : (BF == kPackedForm ? NW / KH : NW * kRows) * t.b_stride;
+      BF == kTurned ? NW * 512 / BN * t.b_stride : (BF == kPackedForm ? NW / 2 : NW * kRows) * t.b_stride;
   const int chunk = (lane % kChunks) ^ row_swz<KH>(wave * kRows + lane / kChunks);  // of a contiguous row
-  uint32_t aa[MODE == kNtUp || !kAlikeA ? QA : 1], ba[kAlikeB ? 1 : QB];
-  if constexpr (MODE == kNtUp) {  // gathered rows
+  uint32_t aa[kAlikeA ? 1 : QA], ba[kAlikeB ? 1 : QB];
 #pragma unroll
-    for (int i = 0; i < QA; ++i) {
-      const int r = (wave + NW * i) * kRows + lane / kChunks;
-      aa[i] = static_cast<uint32_t>(nt_source<MODE>(g, t.row0 + min(r, t.rows - 1))) * t.a_stride + chunk * 16u;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < (kAlikeA ? 1 : QA); ++i)
-      aa[i] = place(std::integral_constant<int, AF>{}, BM, t.a_stride, t.rows, i);
-  }
+  for (int i = 0; i < (kAlikeA ? 1 : QA); ++i)
+    aa[i] = place(std::integral_constant<int, AF>{}, BM, t.a_stride, t.rows, i);
 #pragma unroll
   for (int i = 0; i < (kAlikeB ? 1 : QB); ++i)
     ba[i] = place(std::integral_constant<int, BF>{}, BN, t.b_stride, t.cols, i);
@@ -268,12 +261,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
     const uint32_t stride = kIsA ? t.a_stride : t.b_stride;
     const Lds to = buf + (kIsA ? 0 : ABYTES) + (wave + NW * i) * 1024;
     uint32_t at;
-    if constexpr (kIsA) at = MODE == kNtUp || !kAlikeA ? aa[MODE == kNtUp || !kAlikeA ? i : 0] : aa[0] + i * apart_a;
+    if constexpr (kIsA) at = kAlikeA ? aa[0] + i * apart_a : aa[kAlikeA ? 0 : i];
     else at = kAlikeB ? ba[0] + i * apart_b : ba[kAlikeB ? 0 : i];
     if constexpr (kForm == kTurned) {
       dma16(descriptor(base + static_cast<size_t>(step) * kStep * stride, left * stride), at, 0, to);
     } else if constexpr (kForm == kPackedForm) {
-      dma16(descriptor(base, left > 0 ? b_bytes : 0u), at, step * KH * 1024, to);
+      dma16(descriptor(base, left > 0 ? b_bytes : 0u), at, step * 2048, to);
     } else {
       if (chunk * (16 / T::kBytes) >= left) at = kPastEnd;
       dma16(descriptor(base, kIsA ? t.a_bytes : b_bytes), at, step * kRow, to);

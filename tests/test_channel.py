@@ -264,6 +264,22 @@ def test_largest_sums(M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(70000, 24), (3, 70000), (150, 70000), (70000, 32768)])
+def test_past_32_bits(M, N):
+    """Codes, weights or results of more than 4 GB: the last rows and channels."""
+    K = 65536 if min(M, N) < 1000 else 64
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.empty((N, K), dtype=torch.bfloat16, device="cuda").normal_()
+    W = moe.channel_pack(w)
+    y = moe.channel_linear(x, W)
+    q, s = moe.channel_quantize(x)
+    xs, ws = x[-20:].float().cpu().numpy(), w[-40:].float().cpu().numpy()
+    want = _value(*codecs.int8_row_quantize(xs), *codecs.int8_row_quantize(ws))
+    for got in (y, moe.channel_matmul(q, s, W)):
+        assert _same(got[-20:, -40:], torch.from_numpy(want).bfloat16().float().numpy())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [5, 20, 40, 300])
 def test_rows_and_channels_are_apart(M):
     """NaN and infinities: their row of y, or their column, is NaN; no other changes."""

@@ -241,6 +241,48 @@ def test_rows_and_experts_are_apart(R):
 
 
 @pytest.mark.gpu
+def test_rows_past_32_bits():
+    """x and dx of 5 GB: the rows behind 2^31 values, and dw's sum over them."""
+    R, E, N, K = 40000, 2, 64, 65536
+    b = [0, 39000, 39900]  # 100 rows of no expert
+    x = torch.empty((R, K), dtype=torch.bfloat16, device="cuda").normal_()
+    dy = torch.empty((R, N), dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.empty((E, N, K), dtype=torch.bfloat16, device="cuda").normal_()
+    off = torch.tensor(b, dtype=torch.int32, device="cuda")
+    y, dx, dw = (moe.grouped_matmul(x, w, off), moe.grouped_input_grad(dy, w, off),
+                 moe.grouped_weight_grad(dy, x, off, dw_dtype=torch.float32))
+    for e, s in ((0, slice(38980, 39000)), (1, slice(39880, 39900))):
+        xs, ds, we = x[s].cpu().double(), dy[s].cpu().double(), w[e].cpu().double()
+        _check(y[s], xs @ we.T, xs.abs() @ we.abs().T, K)
+        _check(dx[s], ds @ we, ds.abs() @ we.abs(), N)
+    xs, ds = x[b[1]:b[2], -512:].cpu().double(), dy[b[1]:b[2]].cpu().double()
+    _check(dw[1, :, -512:], ds.T @ xs, ds.abs().T @ xs.abs(), b[2] - b[1])
+    assert not y[b[2]:].any() and not dx[b[2]:].any()
+
+
+@pytest.mark.gpu
+def test_weights_past_32_bits():
+    """Two matrices of 5 GB: the last rows and columns of either, and of its gradient."""
+    R, E, N, K = 100, 2, 65536, 40000
+    b = [0, 30, 100]
+    x = torch.empty((R, K), dtype=torch.bfloat16, device="cuda").normal_()
+    dy = torch.empty((R, N), dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.empty((E, N, K), dtype=torch.bfloat16, device="cuda").normal_()
+    off = torch.tensor(b, dtype=torch.int32, device="cuda")
+    y, dx, dw = (moe.grouped_matmul(x, w, off), moe.grouped_input_grad(dy, w, off),
+                 moe.grouped_weight_grad(dy, x, off))
+    for e in range(E):
+        s = slice(b[e], b[e + 1])
+        xs, ds = x[s].cpu().double(), dy[s].cpu().double()
+        last = w[e, -200:].cpu().double()
+        _check(y[s, -200:], xs @ last.T, xs.abs() @ last.abs().T, K)
+        last = w[e, :, -24:].cpu().double()
+        _check(dx[s, -24:], ds @ last, ds.abs() @ last.abs(), N)
+        xs, ds = xs[:, -300:], ds[:, -300:]
+        _check(dw[e, -300:, -300:], ds.T @ xs, ds.abs().T @ xs.abs(), b[e + 1] - b[e])
+
+
+@pytest.mark.gpu
 def test_no_rows():
     w = torch.randn((3, 64, 128), device="cuda").bfloat16()
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
