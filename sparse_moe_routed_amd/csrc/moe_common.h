@@ -72,6 +72,19 @@ __device__ __forceinline__ uint16_t relu_sq_bf16(float h) {
   return static_cast<uint16_t>(u >> 16);
 }
 
+// the same of two values, the first in the low half, without a branch: what lo leaves is
+// kept in hi's lowest bit, which decides on a midpoint and nowhere else (of an
+// infinity, whose lo is no number, either rounds back to it)
+__device__ __forceinline__ uint32_t relu_sq_bf16_pair(float a, float b) {
+  const auto rounded = [](float h) __attribute__((always_inline)) {
+    h = __builtin_fmaxf(h, 0.f);  // 0 for a NaN
+    const float hi = h * h, lo = __builtin_fmaf(h, h, -hi);
+    const uint32_t u = (__float_as_uint(hi) - (lo < 0.f ? 1u : 0u)) | (lo != 0.f ? 1u : 0u);
+    return u + 0x7fffu + ((u >> 16) & 1u);
+  };
+  return __builtin_amdgcn_perm(rounded(b), rounded(a), 0x07060302u);
+}
+
 // ----------------------------------------------------------------- E4M3 (OCP E4M3FN)
 // 1 sign, 4 exponent bits (bias 7), 3 mantissa bits, largest finite 448,
 // subnormals m * 2^-9.  Encode: nearest-even, finite inputs saturate to 448,

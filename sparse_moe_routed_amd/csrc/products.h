@@ -135,17 +135,18 @@ __device__ __forceinline__ void nt_store(const NtArgs& g, size_t at, int width, 
         if (n + i < width) o[i] = h[i];
     }
   } else {
-    uint16_t b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = MODE == kNtUp ? relu_sq_bf16(h[i]) : f32_to_bf16(h[i]);
     uint16_t* const o = static_cast<uint16_t*>(g.out) + at;
+    const auto pair = [&](int i) __attribute__((always_inline)) {
+      return MODE == kNtUp ? relu_sq_bf16_pair(h[i], h[i + 1]) : bf16_pair(h[i], h[i + 1]);
+    };
+    const uint2 b = make_uint2(pair(0), pair(2));
     if constexpr (WHOLE) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | (static_cast<uint32_t>(b[1]) << 16),
-                                                b[2] | (static_cast<uint32_t>(b[3]) << 16));
+      *reinterpret_cast<uint2*>(o) = b;
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < width) o[i] = b[i];
+      if (n < width) o[0] = static_cast<uint16_t>(b.x);
+      if (n + 1 < width) o[1] = static_cast<uint16_t>(b.x >> 16);
+      if (n + 2 < width) o[2] = static_cast<uint16_t>(b.y);
+      if (n + 3 < width) o[3] = static_cast<uint16_t>(b.y >> 16);
     }
   }
 }
@@ -192,28 +193,34 @@ __device__ __forceinline__ void store_tile(const NtArgs& g, const StoreAt& t, Bu
   constexpr int MS = BM / WM / 16, NS = BN / WN / 16, NW = WM * WN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN, c = lane & 15, q = lane >> 4;
+  // scales of this lane's rows and columns, all loads at once
+  float rs[MS], gate[MS];
+  f32x4 cs[NS];
+  if constexpr (T::kBytes == 1) {
+    size_t source[MS];
+#pragma unroll
+    for (int j = 0; j < MS; ++j) {
+      const int r = t.row0 + min((j * WM + wm) * 16 + c, t.rows - 1);
+      source[j] = nt_source<MODE>(g, r);
+      if constexpr (MODE == kNtDown) gate[j] = g.row_gate[r];
+    }
+#pragma unroll
+    for (int j = 0; j < MS; ++j) rs[j] = g.a_s[source[j]];
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cs[i][k] = t.w_s[min(t.n0 + (wn * NS + i) * 16 + 4 * q + k, g.N - 1)];
+  }
   // this lane's four results of column group i, row group j
-  const auto scaled = [&](int i, int j, f32x4 cs) __attribute__((always_inline)) {
-    const int r = t.row0 + min((j * WM + wm) * 16 + c, t.rows - 1);
-    float rs = 1.f;
-    if constexpr (T::kBytes == 1) rs = g.a_s[nt_source<MODE>(g, r)];
+  const auto scaled = [&](int i, int j) __attribute__((always_inline)) {
     f32x4 h;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = nt_value(acc[i][j][k], rs, cs[k]);
-    if constexpr (MODE == kNtDown) {
-      const float gate = g.row_gate[r];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] *= gate;
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (T::kBytes == 1) h[k] = nt_value(acc[i][j][k], rs[j], cs[i][k]);
+      else h[k] = acc[i][j][k];
+      if constexpr (MODE == kNtDown) h[k] *= gate[j];
     }
     return h;
-  };
-  const auto col_scales = [&](int n) __attribute__((always_inline)) {
-    f32x4 cs = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (T::kBytes == 1) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) cs[k] = t.w_s[min(t.n0 + n + k, g.N - 1)];
-    }
-    return cs;
   };
   const auto rows = [&](auto f32_c) __attribute__((always_inline)) {
     constexpr bool kF32 = decltype(f32_c)::value;
@@ -230,12 +237,11 @@ __device__ __forceinline__ void store_tile(const NtArgs& g, const StoreAt& t, Bu
       __syncthreads();  // what was there has been read
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const f32x4 cs = col_scales((wn * NS + i) * 16 + 4 * q);
 #pragma unroll
         for (int jj = 0; jj < NB * kGroups; ++jj) {
           const int j = round * NB * kGroups + jj;
           if (j >= MS) continue;
-          const f32x4 h = scaled(i, j, cs);
+          const f32x4 h = scaled(i, j);
           const int group = wn * NS + i;
           const Lds row = buffer(jj / kGroups) + ((jj % kGroups * WM + wm) * 16 + c) * kRowBytes;
           if constexpr (kF32) {
@@ -243,8 +249,7 @@ __device__ __forceinline__ void store_tile(const NtArgs& g, const StoreAt& t, Bu
           } else {
             u32x2 v;
             if constexpr (MODE == kNtUp) {
-              v = u32x2{relu_sq_bf16(h[0]) | static_cast<uint32_t>(relu_sq_bf16(h[1])) << 16,
-                        relu_sq_bf16(h[2]) | static_cast<uint32_t>(relu_sq_bf16(h[3])) << 16};
+              v = u32x2{relu_sq_bf16_pair(h[0], h[1]), relu_sq_bf16_pair(h[2], h[3])};
             } else {
               v = u32x2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
             }
@@ -280,12 +285,11 @@ __device__ __forceinline__ void store_tile(const NtArgs& g, const StoreAt& t, Bu
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int n = (wn * NS + i) * 16 + 4 * q;
-      const f32x4 cs = col_scales(n);
 #pragma unroll
       for (int j = 0; j < MS; ++j) {
         const int r = (j * WM + wm) * 16 + c;
         if (r >= t.rows) continue;
-        const f32x4 h = scaled(i, j, cs);
+        const f32x4 h = scaled(i, j);
         const size_t to = t.out + static_cast<size_t>(r) * t.ldo + n;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
