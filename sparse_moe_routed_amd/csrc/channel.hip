@@ -60,11 +60,11 @@ __global__ __launch_bounds__(kQThreads) void channel_pack_codes_kernel(const uin
 }
 
 // Tiles of BM rows x BN weight rows in WM x WN waves, 128 bytes of K a step.  The
-// rows go from memory straight into LDS (NBUF buffers, NBUF - 1 steps under way);
+// rows go from memory straight into LDS (4 buffers, 3 steps under way);
 // the weights straight into registers (WBUF operands per wave and group, WBUF - 1
 // steps under way): a weight is read by the WM waves of a column and no other, while a
 // row serves all WN.  ONCE: weights non-temporal, where one workgroup reads them.
-template <int MODE, int BM, int BN, int WM, int WN, int NBUF, int WBUF, bool ONCE>
+template <int MODE, int BM, int BN, int WM, int WN, int WBUF, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
   typedef NtInt8 T;
   typedef T::Acc Acc;
@@ -72,19 +72,19 @@ __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int MS = WTM / 16, NS = WTN / 16;  // 16 x 16 products of a wave
   constexpr int QA = BM / 8 / NW;              // loads of 8 rows per wave and step
-  constexpr int kRowsAhead = (NBUF - 2) * QA;  // loads that may be under way when a step's rows are there:
+  constexpr int kRowsAhead = 2 * QA;  // loads that may be under way when a step's rows are there:
   // of rows, and of weights those of steps from this one on issued after its rows.  Loads
   // are spread between the products where rows and weights are both ahead of time;
   // otherwise all at once, rows first.
-  constexpr bool kSpread = NBUF == 4 && !ONCE;
+  constexpr bool kSpread = !ONCE;
   constexpr int kAhead = kRowsAhead + (kSpread ? WBUF / 2 : WBUF - 1) * 2 * NS;
   constexpr int BUF = BM * 128;
   static_assert(QA * 8 * NW == BM, "tile");
-  static_assert((NBUF == 2 || NBUF == 4) && (WBUF == 2 || WBUF == 4) && kAhead < 64, "buffers");
+  static_assert((WBUF == 2 || WBUF == 4) && kAhead < 64, "buffers");
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[BUF];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[BUF];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds2[NBUF == 4 ? BUF : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds3[NBUF == 4 ? BUF : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[BUF];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds3[BUF];
   NtTile t;
   if (!nt_find<T, MODE, BM, BN>(g, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
     }
   };
   // One step: its rows have arrived (this wave's, then at the barrier everyone's),
-  // those of step + NBUF - 1 start into the buffer that everyone has read, the
+  // those of step + 3 start into the buffer that everyone has read, the
   // weights of step + WBUF - 1 into the registers of step - 1, then the products.
   // The last steps of all (TAIL, fewer than 4) wait for all that is under way.
   const auto body = [&](int step, const uint8_t* cur, uint8_t* ahead, const Weights& now, Weights& next,
@@ -187,11 +187,11 @@ __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
         for (int l = 0; l < kLoads; ++l) {
           if (l * kProducts / kLoads != u) continue;
           if (l < NS) load_w1(next, step + WBUF - 1, l);
-          else load_row(step + NBUF - 1, ahead, l - NS);
+          else load_row(step + 3, ahead, l - NS);
         }
       });
     } else {
-      if (!TAIL || NBUF == 2) load_rows(step + NBUF - 1, ahead);
+      if (!TAIL) load_rows(step + 3, ahead);
       if (!TAIL || WBUF == 2) load_w(next, step + WBUF - 1);
       compute(cur, now, live_c, [](int) {});
     }
@@ -199,10 +199,8 @@ __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
   const auto run = [&](auto live_c) __attribute__((always_inline)) {
     Weights w0, w1, w2, w3;
     load_rows(0, lds0);
-    if (NBUF == 4) {
-      load_rows(1, lds1);
-      load_rows(2, lds2);
-    }
+    load_rows(1, lds1);
+    load_rows(2, lds2);
     load_w(w0, 0);
     if (WBUF == 4) {
       load_w(w1, 1);
@@ -212,13 +210,13 @@ __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
     // compiler sees which loads each step has to wait for)
     int step = 0;
     const auto one = [&](auto k_c, auto tail_c) __attribute__((always_inline)) {
-      constexpr int k = decltype(k_c)::value, n = k % NBUF, ah = (k + NBUF - 1) % NBUF;
-      constexpr int v = k % WBUF, y = (k + WBUF - 1) % WBUF;
+      constexpr int n = decltype(k_c)::value, ah = (n + 3) % 4;
+      constexpr int v = n % WBUF, y = (n + WBUF - 1) % WBUF;
       const uint8_t* const cur = n == 0 ? lds0 : (n == 1 ? lds1 : (n == 2 ? lds2 : lds3));
       uint8_t* const ahead = ah == 0 ? lds0 : (ah == 1 ? lds1 : (ah == 2 ? lds2 : lds3));
       Weights& now = v == 0 ? w0 : (v == 1 ? w1 : (v == 2 ? w2 : w3));
       Weights& next = y == 0 ? w0 : (y == 1 ? w1 : (y == 2 ? w2 : w3));
-      body(step + k, cur, ahead, now, next, live_c, tail_c);
+      body(step + n, cur, ahead, now, next, live_c, tail_c);
     };
     constexpr std::integral_constant<int, 0> k0{};
     constexpr std::integral_constant<int, 1> k1{};
@@ -247,17 +245,22 @@ __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
   if constexpr (BN >= 128 && BUF >= 16 * WM * BN * 4) {
     const int cols = min(BN, g.N - t.n0);
     const StoreAt to{t.row0, t.rows, t.n0, cols, g.N, static_cast<size_t>(t.row0) * g.N + t.n0, t.w_s};
-    if constexpr (NBUF == 4) {
-      const auto buffers = [&](int b) __attribute__((always_inline)) {
-        return b == 0 ? (Lds)lds0 : (b == 1 ? (Lds)lds1 : (b == 2 ? (Lds)lds2 : (Lds)lds3));
-      };
-      store_tile<T, MODE, BM, BN, WM, WN, 4, BUF>(g, to, buffers, acc);
-    } else {
-      const auto buffers = [&](int b) __attribute__((always_inline)) { return b == 0 ? (Lds)lds0 : (Lds)lds1; };
-      store_tile<T, MODE, BM, BN, WM, WN, 2, BUF>(g, to, buffers, acc);
-    }
+    const auto buffers = [&](int b) __attribute__((always_inline)) {
+      return b == 0 ? (Lds)lds0 : (b == 1 ? (Lds)lds1 : (b == 2 ? (Lds)lds2 : (Lds)lds3));
+    };
+    store_tile<T, MODE, BM, BN, WM, WN, 4, BUF>(g, to, buffers, acc);
     return;
   }
+  float rs[MS], gate[MS];  // all loads at once
+  size_t source[MS];
+#pragma unroll
+  for (int j = 0; j < MS; ++j) {
+    const int r = t.row0 + min((j * WM + wm) * 16 + c, t.rows - 1);
+    source[j] = nt_source<MODE>(g, r);
+    gate[j] = MODE == kNtDown ? g.row_gate[r] : 1.f;
+  }
+#pragma unroll
+  for (int j = 0; j < MS; ++j) rs[j] = g.a_s[source[j]];
   nt_store_as<T, MODE>(g, g.N, [&](auto f32_c, auto whole_c) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -268,38 +271,32 @@ __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
       for (int j = 0; j < MS; ++j) {
         const int r = (j * WM + wm) * 16 + c;
         if (r >= t.rows) continue;
-        float rs = 1.f, gate = 1.f;
-        rs = g.a_s[nt_source<MODE>(g, t.row0 + r)];
-        if constexpr (MODE == kNtDown) gate = g.row_gate[t.row0 + r];
         nt_store<T, MODE, decltype(f32_c)::value, decltype(whole_c)::value>(
-            g, static_cast<size_t>(t.row0 + r) * g.N + n, g.N, n, acc[i][j], rs, cs, gate);
+            g, static_cast<size_t>(t.row0 + r) * g.N + n, g.N, n, acc[i][j], rs[j], cs, gate[j]);
       }
     }
   });
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, int NBUF, int WBUF, bool ONCE = false>
+template <int MODE, int BM, int BN, int WM, int WN, int WBUF, bool ONCE = false>
 hipError_t launch_channel_tile(const NtArgs& g, hipStream_t stream, const KernelEvents& ev = KernelEvents{}) {
-  return launch_tiles(reinterpret_cast<const void*>(&channel_tile_kernel<MODE, BM, BN, WM, WN, NBUF, WBUF, ONCE>),
+  return launch_tiles(reinterpret_cast<const void*>(&channel_tile_kernel<MODE, BM, BN, WM, WN, WBUF, ONCE>),
                       row_tiles<MODE, BM, BN>(g), WM * WN * 64, g, stream, ev);
 }
 
 }  // namespace
 
-// Rows of a tile near what an expert has: the fewer, the more workgroups share the
-// streaming of the weights, the more the fewer times each is read.  The layer of 128
-// experts, 2688 x 1856, 6 a token, us with tiles of 32 x 64, 64 x 128 and 128 x 128: 384
-// rows 199, 222 and 257; 2400 rows 263, 283 and 298; 6000 rows 539, 330 and 345; 9000
-// rows 626, 390 and 381; 24576 rows 1157, 661 and 656.
+// Few rows an expert: small tiles, so that many workgroups share the streaming of the
+// weights; many: larger ones, which read them fewer times.  The layer of 128 experts,
+// 2688 x 1856, 6 a token, us with tiles of 32 x 64 and of 128 x 128: 384 rows 195 and 240;
+// 2400 rows 260 and 286; 3600 rows 319 and 306; 24576 rows 1161 and 614 (64 x 128 lie
+// between: 238, 284, 303 and 648).
 hipError_t launch_channel_experts(int stage, const NtArgs& g, hipStream_t stream, const KernelEvents& ev) {
   if (g.M < (24 * g.E > 256 ? 24 * g.E : 256))
-    return stage == 0 ? launch_channel_tile<kNtUp, 32, 64, 1, 4, 4, 4, true>(g, stream, ev)
-                      : launch_channel_tile<kNtDown, 32, 64, 1, 4, 4, 4, true>(g, stream, ev);
-  if (g.M < 56 * g.E)
-    return stage == 0 ? launch_channel_tile<kNtUp, 64, 128, 1, 4, 4, 4>(g, stream, ev)
-                      : launch_channel_tile<kNtDown, 64, 128, 1, 4, 4, 4>(g, stream, ev);
-  return stage == 0 ? launch_channel_tile<kNtUp, 128, 128, 1, 4, 4, 4>(g, stream, ev)
-                    : launch_channel_tile<kNtDown, 128, 128, 1, 4, 4, 4>(g, stream, ev);
+    return stage == 0 ? launch_channel_tile<kNtUp, 32, 64, 1, 4, 4, true>(g, stream, ev)
+                      : launch_channel_tile<kNtDown, 32, 64, 1, 4, 4, true>(g, stream, ev);
+  return stage == 0 ? launch_channel_tile<kNtUp, 128, 128, 1, 4, 4>(g, stream, ev)
+                    : launch_channel_tile<kNtDown, 128, 128, 1, 4, 4>(g, stream, ev);
 }
 
 // Tiles by size, us measured at N x K:
@@ -323,10 +320,10 @@ hipError_t launch_channel_dense(const NtArgs& g, hipStream_t stream) {
     return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn) >= kFill;
   };
   if (fills(256, 256)) return launch_tile<NtInt8, kNtDense, 256, 256, 2, 4, 2, 2>(g, stream);
-  if (fills(128, 256)) return launch_channel_tile<kNtDense, 128, 256, 1, 8, 4, 2>(g, stream);
-  if (fills(128, 128)) return launch_channel_tile<kNtDense, 128, 128, 2, 4, 4, 2>(g, stream);
-  if (fills(64, 128)) return launch_channel_tile<kNtDense, 64, 128, 2, 4, 4, 2>(g, stream);
-  return launch_channel_tile<kNtDense, 64, 64, 2, 4, 4, 4>(g, stream);
+  if (fills(128, 256)) return launch_channel_tile<kNtDense, 128, 256, 1, 8, 2>(g, stream);
+  if (fills(128, 128)) return launch_channel_tile<kNtDense, 128, 128, 2, 4, 2>(g, stream);
+  if (fills(64, 128)) return launch_channel_tile<kNtDense, 64, 128, 2, 4, 2>(g, stream);
+  return launch_channel_tile<kNtDense, 64, 64, 2, 4, 4>(g, stream);
 }
 
 // at most kChannelFewRows bf16 rows, quantised by every workgroup that takes them
