@@ -182,11 +182,12 @@ __device__ __forceinline__ void warm_rows(const NtArgs& g, Lds to, int waves) {
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// chunk x of row r of a contiguous operand lies at x ^ row_swz(r): 16 rows of an operand
-// read fall on distinct banks
+// chunk x of row r of a contiguous operand lies at x ^ row_swz(r).  16 lanes at a time read
+// LDS: rows 0 to 3 and 12 to 15 of one chunk with rows 4 to 11 of its neighbour (x ^ 1), or
+// the other way round; they fall on distinct banks.
 template <int KH>
 __device__ __forceinline__ int row_swz(int r) {
-  return KH == 1 ? (r >> 2) & 3 : swz(r);
+  return KH == 1 ? -(r >> 2) & 3 : swz(r);
 }
 
 template <typename T, int MODE, int BM, int BN, int WM, int WN, int KH, int NBUF>
