@@ -512,7 +512,7 @@ int32_t moe_channel_linear(int32_t M, int32_t N, int32_t K, const void* x, const
  *           N, K); NULL will do where that is 256: sums are taken in parts only where the
  *           experts' matrices are too small to fill the chip and the rows many
  *   *_dtype MOE_Y_BF16 or MOE_Y_F32
- * Products are exact and summed in fp32, in an order that depends on the sizes alone:
+ * Products are exact and summed in fp32, in an order that depends on sizes and bounds alone:
  * a call repeats bit for bit.  A row's result depends on that row and its expert's
  * weights alone, an expert's dw on its rows alone: NaN and infinities spread no
  * further.  N % 8 == K % 8 == 0, N, K <= 65536, E <= 256, R <= 1 << 23

@@ -15,7 +15,8 @@ namespace moe {
 
 namespace {
 
-// rows of no expert, [offsets[E], R), set to zero: 16 bytes a thread
+// rows of no expert, [offsets[E], R), set to zero: 16 bytes a thread.  For the few rows
+// that pad a batch it is a launch's time
 __global__ __launch_bounds__(256) void zero_rest_kernel(const int32_t* __restrict__ offsets, int E, int R,
                                                         size_t row_bytes, uint8_t* __restrict__ out) {
   const int from = min(max(offsets[E], 0), R);
@@ -26,12 +27,14 @@ __global__ __launch_bounds__(256) void zero_rest_kernel(const int32_t* __restric
     *reinterpret_cast<u32x4*>(out + i) = zero;
 }
 
-// dw of its parts [splits, n], added up in their order
+// dw of its parts [splits, n], added up in their order, eight loads at a time (64 parts of
+// 64 x 64: 18 us with the product, 41 one by one)
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ parts, int splits, size_t n,
                                                    void* __restrict__ out, int out_f32, int accumulate) {
   for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
        i += static_cast<size_t>(gridDim.x) * 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(parts + s * n + i);
     if (out_f32) {
       f32x4* const o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + i);
@@ -115,10 +118,18 @@ hipError_t launch_grouped_input_grad(const GroupedArgs& g, hipStream_t stream) {
   return err == hipSuccess && g.zero_rest ? launch_zero_rest(g, g.K, stream) : err;
 }
 
-// dw: parts of an expert's rows side by side where the experts' tiles are too few for the
-// chip and the rows many (128 rows a part at least), each a sum of its own, joined in order
+// dw in tiles of 128 x 256, whose four waves read two operands of rows for each of columns:
+// at 128 experts of 1856 x 2688 and 24576 rows 472 us, in 256 x 256 522, in 128 x 128 542;
+// at 1500 rows, where the fill of dw binds, 237, 287 and 298.
+//
+// Parts of an expert's rows side by side, 128 rows a part at least, each a sum of its own,
+// joined in order, where the experts' tiles are too few for the chip and the experts' rows
+// many enough to pay for the second kernel: 24576 rows of one expert, 64 x 64, 18 us, in one
+// part 249; 1500 rows of each of 16, 256 x 256, 22 and 28; 1024 rows each 21 and 21; 512 rows
+// each 18 and 14.
 constexpr int kDwRows = 128, kDwCols = 256;
 int weight_grad_splits(int R, int E, int N, int K) {
+  if (R < 1024ll * E) return 1;
   const long long tiles = static_cast<long long>(E) * ((N + kDwRows - 1) / kDwRows) * ((K + kDwCols - 1) / kDwCols);
   const long long by_tiles = 256 / tiles, by_rows = R / (128ll * E);
   const long long s = by_tiles < by_rows ? by_tiles : by_rows;
@@ -128,9 +139,13 @@ int weight_grad_splits(int R, int E, int N, int K) {
 hipError_t launch_grouped_weight_grad(const GroupedArgs& g, hipStream_t stream) {
   NtArgs a = product_args(g, g.dy, g.x);
   a.splits = weight_grad_splits(g.R, g.E, g.N, g.K);
-  // rows worth reading ahead, and that the last-level cache (256 MB) can hold
+  // Rows are read ahead where there are enough of them, the last-level cache (256 MB) holds
+  // them and the writes of dw would keep memory from them: R = 24576, 1856 x 2688, bf16,
+  // 128 experts (dw 5.7 times the rows' bytes) 472 us, 520 without; 64 experts (2.9 times)
+  // 349 and 354; but 32 (1.4 times) 315 and 294.
   const size_t bytes = static_cast<size_t>(g.R) * (g.N + g.K) * 2;
-  a.warm = bytes >= (32u << 20) && bytes <= (240u << 20) ? 32 : 0;
+  const size_t dw_bytes = static_cast<size_t>(g.E) * g.N * g.K * (g.out_f32 ? 4 : 2);
+  a.warm = bytes >= (32u << 20) && bytes <= (240u << 20) && dw_bytes >= 2 * bytes ? 32 : 0;
   if (a.splits > 1) {
     a.out = g.partial;
     a.out_f32 = 1;

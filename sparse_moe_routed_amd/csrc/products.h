@@ -186,7 +186,8 @@ struct StoreAt {
 // rows, which would be a part of 16 lines.  buffer(0) to buffer(NB - 1) are parts of LDS of
 // kBytes each, which take as many rows as fit at a time; chunk x of row r lies at x ^ (r % 16), on
 // other banks than its neighbours.  Row group j of a wave is j WM + wm.  Stores are
-// non-temporal: nothing of an output is read again before it has left the caches.
+// non-temporal: nothing of an output is read again before it has left the caches (dw of
+// 1500 rows 246 us, with ordinary stores 333; of 24576 rows in fp32 561 and 724).
 template <typename T, int MODE, int BM, int BN, int WM, int WN, int NB, int kBytes, typename Buffers>
 __device__ __forceinline__ void store_tile(const NtArgs& g, const StoreAt& t, Buffers buffer,
                                            const typename T::Acc (&acc)[BN / WN / 16][BM / WM / 16]) {

