@@ -1055,7 +1055,8 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: O
                    y_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """moe_grouped_matmul: y [R, N] with y[r] = w[e] x[r] for the rows offsets[e] to
     offsets[e + 1] of expert e; x bf16 [R, K], w bf16 [E, N, K].  Rows behind
-    offsets[E] stay as they are in a y that is given and are zero in a new one."""
+    offsets[E] stay as they are in a y that is given and are zero in a new one.  (With
+    gradients: grouped_linear.)"""
     R, E, N, K = _grouped_operands(x, "x", w, offsets, 2)
     fresh = y is None
     y, yd = _out(y, y_dtype, "y", (R, N), x)
