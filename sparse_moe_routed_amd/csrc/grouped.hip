@@ -76,29 +76,32 @@ long long large_tiles(int R, int width) {
 
 // Tiles by size, measured at N = 1856 and K = 2688:
 //   - few rows, whose tiles of 64 x 128 would leave many CUs without one: 32 columns a
-//     workgroup and the sum dealt to its waves (1 row 8.7 us, in tiles 15.5; 64 rows of 8
-//     experts 20 and 25; but 24 rows of 128 experts 53 and 41);
+//     workgroup and the sum dealt to its waves (1 row 8.6 us, in tiles 13.9; 16 rows of 4
+//     experts 11.0 and 14.5; but of 8 experts 19.5 and 16.0);
 //   - 256 x 256, which read least from the caches for each product, where the experts have
 //     rows for them and the chip enough of them (192 rows an expert of 128: 315 us, 393 in
 //     128 x 128; 8192 rows of one 68 and 81; but 128 rows an expert 289 and 279, and 4096
-//     rows of one expert, 128 tiles, 56 and 42);
-//   - 128 x 128 where there are enough of those (1500 rows of 128 experts 225 us, 230 in
-//     64 x 128; 4096 of one 42 and 66);
-//   - 64 x 128 for the rest, three workgroups to a CU (1500 rows of one expert 28 us, 31
-//     in 128 x 128; 24 rows of 128 experts 41 and 44).
+//     rows of one expert, 128 tiles, 56 and 41);
+//   - 128 x 128 where there is more than one for each CU (2500 rows of one expert 36 us, 43
+//     in 64 x 128; 4096 rows 41 and 58);
+//   - 64 x 128 for the rest, two workgroups to a CU and two stages under way in each (1000
+//     rows of one expert 19 us, 31 in 128 x 128; 1000 rows of 16 experts 26 and 30).  With
+//     one stage under way in each of three workgroups 1000 rows of one expert take 26 us,
+//     and 400 rows of 128 experts with weights in memory 216, now 196.
 hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t stream) {
   const NtArgs a = product_args(g, g.x, g.w);
   const int experts = g.R < g.E ? g.R : g.E;  // at most, with rows
+  const int row_tiles = (g.R + 127) / 128;
   const long long cols = (g.N + 127) / 128;
   hipError_t err;
-  if (g.R <= 256 && ((g.R + 63) / 64 + experts) * cols < 160)
+  if (g.R <= 256 && ((g.R + 63) / 64 + experts) * cols < 128)
     err = g.R <= 64 ? launch_small<NtBf16, kNtGroups, 1, false>(a, stream)
                     : launch_small<NtBf16, kNtGroups, 4, false>(a, stream);
   else if (g.R >= 144 * g.E && large_tiles(g.R, g.N) >= 160)
     err = launch_tile<NtBf16, kNtGroups, 256, 256, 2, 4, 2, 2>(a, stream);
-  else if (g.R >= 4 * g.E && (g.R / 128 + experts) * cols >= 320)
+  else if (g.R >= 4 * g.E && (row_tiles > experts ? row_tiles : experts) * cols >= 280)
     err = launch_tile<NtBf16, kNtGroups, 128, 128, 2, 2, 2, 2>(a, stream);
-  else err = launch_tile<NtBf16, kNtGroups, 64, 128, 1, 4, 2, 2>(a, stream);
+  else err = launch_tile<NtBf16, kNtGroups, 64, 128, 1, 4, 2, 3>(a, stream);
   return err == hipSuccess && g.zero_rest ? launch_zero_rest(g, g.N, stream) : err;
 }
 

@@ -148,6 +148,7 @@ SHAPES = [
     ("one", 5000, 3, 256, 128, 0), ("skew", 5200, 3, 2056, 72, 30), ("skew", 5200, 3, 72, 2056, 30),
     ("skew", 5200, 20, 136, 2056, 30), ("skew", 700, 16, 2056, 104, 9), ("one", 700, 16, 1856, 136, 0),
     ("skew", 6000, 4, 1000, 1800, 0), ("even", 24001, 1, 360, 368, 0),
+    ("skew", 2600, 3, 1856, 104, 7),
 ]
 
 
