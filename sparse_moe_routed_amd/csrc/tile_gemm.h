@@ -35,7 +35,7 @@ enum TileForm { kContig = 0, kPackedForm = 1, kTurned = 2 };
 // 24..27, each then 4 on) lie on distinct banks
 __device__ __forceinline__ int tr_swz(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
 
-struct TileAt2 {
+struct ProductTile {
   int rows, cols;   // valid rows and columns of the tile
   int row0, n0;     // first row (of all rows) and column
   int length;       // of the sum, in values
@@ -59,7 +59,7 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 }
 
 template <typename T, int MODE, int BM, int BN>
-__device__ __forceinline__ bool tile_find(const NtArgs& g, TileAt2& t) {
+__device__ __forceinline__ bool tile_find(const NtArgs& g, ProductTile& t) {
   if constexpr (MODE == kGradWeights) {
     // a row of tiles of one expert is one XCD's, the rows of tiles go round: experts
     // of many rows are then shared by all
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
     warm_rows(g, (Lds)lds, NW);
     return;
   }
-  TileAt2 t;
+  ProductTile t;
   if (!tile_find<T, MODE, BM, BN>(g, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
