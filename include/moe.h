@@ -504,8 +504,8 @@ int32_t moe_channel_linear(int32_t M, int32_t N, int32_t K, const void* x, const
  *           outside [0, R] are taken as the nearest of them, an expert that ends
  *           before it starts has no rows)
  *   y [dev] [R, N], dx [dev] [R, K]: rows of an expert are written; rows of none
- *           are left as they were (zero_rest = 0), or those from offsets[E] on set to
- *           zero (zero_rest = 1)
+ *           are left as they were (zero_rest = 0), or those before offsets[0] and from
+ *           offsets[E] on set to zero (zero_rest = 1)
  *   dw [dev] [E, N, K]: written in full (an expert without rows gets zeros, or with
  *           accumulate keeps its values)
  *   ws [dev] 256-byte aligned, ws_bytes >= moe_grouped_weight_grad_workspace_size(R, E,

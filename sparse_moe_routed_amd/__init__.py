@@ -1054,9 +1054,9 @@ def _grouped_operands(rows: torch.Tensor, name: str, w: torch.Tensor, offsets: t
 def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: Optional[torch.Tensor] = None,
                    y_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """moe_grouped_matmul: y [R, N] with y[r] = w[e] x[r] for the rows offsets[e] to
-    offsets[e + 1] of expert e; x bf16 [R, K], w bf16 [E, N, K].  Rows behind
-    offsets[E] stay as they are in a y that is given and are zero in a new one.  (With
-    gradients: grouped_linear.)"""
+    offsets[e + 1] of expert e; x bf16 [R, K], w bf16 [E, N, K].  Rows before
+    offsets[0] and behind offsets[E] stay as they are in a y that is given and are zero
+    in a new one.  (With gradients: grouped_linear.)"""
     R, E, N, K = _grouped_operands(x, "x", w, offsets, 2)
     fresh = y is None
     y, yd = _out(y, y_dtype, "y", (R, N), x)
@@ -1068,7 +1068,7 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: O
 def grouped_input_grad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                        dx: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """moe_grouped_input_grad: dx [R, K] with dx[r] = dy[r] w[e]; dy bf16 [R, N], w bf16
-    [E, N, K].  Rows behind offsets[E] as in grouped_matmul."""
+    [E, N, K].  Rows before offsets[0] and behind offsets[E] as in grouped_matmul."""
     R, E, N, K = _grouped_operands(dy, "dy", w, offsets, 1)
     fresh = dx is None
     dx, yd = _out(dx, dx_dtype, "dx", (R, K), dy)
@@ -1130,7 +1130,8 @@ class _GroupedLinear(torch.autograd.Function):
 
 def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
     """grouped_matmul with gradients (torch autograd): bf16 y [R, N] of x bf16 [R, K] and
-    w bf16 [E, N, K], dx and dw in bf16.  The forward can be captured in a graph; a
+    w bf16 [E, N, K], dx and dw in bf16; rows of no expert have y and dx of zero, so that
+    offsets may be those of some of the experts, off[lo:hi + 1].  The forward can be captured in a graph; a
     captured backward is to call grouped_input_grad and grouped_weight_grad themselves,
     since autograd's own bookkeeping of leaves does not belong in one."""
     return _GroupedLinear.apply(x, w, offsets)

@@ -15,16 +15,16 @@ namespace moe {
 
 namespace {
 
-// rows of no expert, [offsets[E], R), set to zero: 16 bytes a thread.  For the few rows
-// that pad a batch it is a launch's time
+// rows of no expert, before offsets[0] and from offsets[E] on, set to zero: 16 bytes a
+// thread.  For the few rows that pad a batch it is a launch's time
 __global__ __launch_bounds__(256) void zero_rest_kernel(const int32_t* __restrict__ offsets, int E, int R,
                                                         size_t row_bytes, uint8_t* __restrict__ out) {
-  const int from = min(max(offsets[E], 0), R);
-  const size_t end = static_cast<size_t>(R) * row_bytes;
+  const size_t head = min(max(offsets[0], 0), R) * row_bytes, tail = min(max(offsets[E], 0), R) * row_bytes;
+  const size_t end = R * row_bytes, step = static_cast<size_t>(gridDim.x) * 256 * 16;
+  const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  for (size_t i = static_cast<size_t>(from) * row_bytes + (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 16;
-       i < end; i += static_cast<size_t>(gridDim.x) * 256 * 16)
-    *reinterpret_cast<u32x4*>(out + i) = zero;
+  for (size_t i = at; i < head; i += step) *reinterpret_cast<u32x4*>(out + i) = zero;
+  for (size_t i = tail + at; i < end; i += step) *reinterpret_cast<u32x4*>(out + i) = zero;
 }
 
 // dw of its parts [splits, n], added up in their order, eight loads at a time (64 parts of

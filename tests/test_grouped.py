@@ -502,3 +502,56 @@ def test_gradients_against_differences():
     assert torch.equal(xg, dx)
     wg, = torch.autograd.grad(moe.grouped_linear(x.detach(), w, off), (w,), dy.t().contiguous().t())
     assert torch.equal(wg, dw)
+
+
+def _stale(*shape):
+    """The allocator's next block of this size holds NaN."""
+    torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,lo,hi", [(40, 2, 5), (40, 0, 3), (40, 5, 8), (1500, 3, 4), (3000, 1, 8), (1500, 4, 4)])
+def test_rows_before_the_first_expert(R, lo, hi):
+    """Some of the experts, as a process that holds experts lo to hi has them: all rows and
+    the bounds of its own.  A new output is zero in the others' rows on both sides, one
+    that is given keeps them."""
+    c = Case("skew", R, 8, 192, 320, rest=5)
+    x, dy, w, off = c.cuda()
+    some, own = off[lo:hi + 1].contiguous(), w[lo:hi].contiguous()
+    if lo == hi:  # one expert without rows, somewhere inside
+        some, own = off[lo].repeat(2), w[lo:lo + 1].contiguous()
+    a, b = int(c.bounds[lo]), int(c.bounds[hi])
+    grads = []
+    for call, rows, width, op in ((moe.grouped_matmul, x, 192, "y"), (moe.grouped_input_grad, dy, 320, "dx")):
+        ref, size = c.ref(op)
+        _stale(c.R, width)
+        new = call(rows, own, some)
+        assert not new[:a].any() and not new[b:].any()
+        _check(new[a:b], ref[a:b], size[a:b], c.terms(op))
+        kept = call(rows, own, some, **{op: torch.full_like(new, 7.0)})
+        assert (kept[:a] == 7).all() and (kept[b:] == 7).all() and torch.equal(kept[a:b], new[a:b])
+        grads.append(new)
+    xl, wl = x.clone().requires_grad_(), own.clone().requires_grad_()
+    _stale(c.R, 192)
+    y = moe.grouped_linear(xl, wl, some)
+    assert torch.equal(y, grads[0])
+    _stale(c.R, 320)
+    dx, dw = torch.autograd.grad(y, (xl, wl), dy)
+    assert torch.equal(dx, grads[1])
+    if lo == hi:
+        assert not dw.any()
+    else:
+        ref, size = c.ref("dw")
+        _check(dw, ref[lo:hi], size[lo:hi], c.terms("dw"))
+
+
+@pytest.mark.gpu
+def test_bounds_past_the_rows_leave_nothing_stale():
+    """All bounds behind the rows, or before them: no row is an expert's."""
+    x = torch.ones((300, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((2, 64, 64), dtype=torch.bfloat16, device="cuda")
+    for bad in ([300, 300, 300], [400, 500, 600], [-5, -5, -1]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        for call in (moe.grouped_matmul, moe.grouped_input_grad):
+            _stale(300, 64)
+            assert not call(x, w, off).any()
