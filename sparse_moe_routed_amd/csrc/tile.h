@@ -5,6 +5,7 @@
 #include <stdint.h>
 #include <type_traits>
 
+#include "load_at.h"
 #include "moe_common.h"
 #include "moe_internal.h"
 
@@ -16,7 +17,7 @@ namespace moe {
 // past it by the lane's own offset (kPastEnd, or a descriptor of no records with
 // a scalar offset of 0), whether or not the range check counts the scalar offset.
 constexpr int kRawBuffer = 0x00027000;
-constexpr uint32_t kPastEnd = kBlockMaxBytes;  // and 4 KB on: beyond every buffer
+static_assert(kPastEnd == kBlockMaxBytes, "beyond every buffer");
 typedef __amdgpu_buffer_rsrc_t Buffer;
 
 __device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {

@@ -168,15 +168,10 @@ __device__ __forceinline__ void warm_rows(const NtArgs& g, Lds to, int waves) {
   const uint32_t mine = (blockIdx.x * waves + wave) * 1024u + lane * 16u, all = g.warm * waves * 1024u;
   const Lds at = to + wave * 1024;
   const auto read = [&](const uint8_t* p, size_t bytes) __attribute__((always_inline)) {
-    constexpr uint32_t kPart = 1u << 30;  // of a descriptor
-    for (size_t base = 0; base < bytes; base += kPart) {
-      const uint32_t n = static_cast<uint32_t>(bytes - base < kPart ? bytes - base : kPart);
-      const i32x4 d = descriptor(p + base, n);
-      for (uint32_t o = 0; o < n; o += all) {
-        dma16(d, mine, o, at);
-        __asm__ volatile("s_waitcnt vmcnt(24)" ::: "memory");
-      }
-    }
+    read_once(bytes, mine, all, [&](size_t base, uint32_t n, uint32_t o, uint32_t step_at) __attribute__((always_inline)) {
+      dma16(descriptor(p + base, n), o, step_at, at);
+      __asm__ volatile("s_waitcnt vmcnt(24)" ::: "memory");
+    });
   };
   const int E = g.E;
   for (int e = 0; e < E; ++e) {
