@@ -22,4 +22,25 @@ __host__ __device__ __forceinline__ void read_once(size_t bytes, uint32_t mine, 
   }
 }
 
+// Where a lane's load of a stage goes: records of the descriptor, the lane's offset and
+// the scalar one.  Stages past the sum's last are loaded all the same, as zeros: they have
+// a scalar offset of 0, since it may be more than the records and some range checks would
+// take it off them.
+struct StageLoad {
+  uint32_t records, at, step_at;
+};
+
+// contiguous rows of `bytes` in all, their stages `stage` bytes apart: `at` is the lane's
+// chunk in the first one, `left` is what the stage holds of a row's sum, `from` the chunk's
+// first of it
+__host__ __device__ __forceinline__ StageLoad load_rows(uint32_t bytes, uint32_t at, int step, int stage, int left,
+                                                       int from) {
+  return {bytes, from < left ? at : kPastEnd, left > 0 ? static_cast<uint32_t>(step * stage) : 0u};
+}
+
+// packed weights, 2 KB a stage of each group
+__host__ __device__ __forceinline__ StageLoad load_packed(uint32_t bytes, uint32_t at, int step, int left) {
+  return {left > 0 ? bytes : 0u, at, left > 0 ? static_cast<uint32_t>(step * 2048) : 0u};
+}
+
 }  // namespace moe

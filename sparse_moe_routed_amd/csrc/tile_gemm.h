@@ -253,7 +253,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
   for (int i = 0; i < (kAlikeB ? 1 : QB); ++i)
     ba[i] = place(std::integral_constant<int, BF>{}, BN, t.b_stride, t.cols, i);
   const uint32_t b_bytes = (BF == kPackedForm ? (t.cols + 15) / 16 : t.cols) * t.b_stride;
-  // load l of QA + QB of a stage
+  // load l of QA + QB of a stage (load_at.h)
   const auto load1 = [&](int step, Lds buf, auto l_c) __attribute__((always_inline)) {
     constexpr int l = decltype(l_c)::value;
     constexpr bool kIsA = l < QA;
@@ -268,10 +268,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
     if constexpr (kForm == kTurned) {
       dma16(descriptor(base + static_cast<size_t>(step) * kStep * stride, left * stride), at, 0, to);
     } else if constexpr (kForm == kPackedForm) {
-      dma16(descriptor(base, left > 0 ? b_bytes : 0u), at, step * 2048, to);
+      const StageLoad g = load_packed(b_bytes, at, step, left);
+      dma16(descriptor(base, g.records), g.at, g.step_at, to);
     } else {
-      if (chunk * (16 / T::kBytes) >= left) at = kPastEnd;
-      dma16(descriptor(base, kIsA ? t.a_bytes : b_bytes), at, step * kRow, to);
+      const StageLoad g = load_rows(kIsA ? t.a_bytes : b_bytes, at, step, kRow, left, chunk * (16 / T::kBytes));
+      dma16(descriptor(base, g.records), g.at, g.step_at, to);
     }
   };
   const auto load_part = [&](int step, Lds buf, auto from_c, auto to_c) __attribute__((always_inline)) {

@@ -67,3 +67,44 @@ int main() {
   }
 }
 """)
+
+
+@needs_compiler
+def test_stages_of_rows_and_of_packed_weights(tmp_path):
+    """Loads of all stages of a tile and of those past the last one: contiguous rows and
+    packed groups of 16 rows.  A chunk that holds values is read, no other is, and none behind the buffer."""
+    _run(tmp_path, r"""
+static void see(bool holds) {
+  for (int r = 0; r < 3; ++r)
+    if (dropped[r] == holds) {
+      std::printf("reading %d: a chunk is %s\n", r, holds ? "left out" : "read");
+      std::exit(2);
+    }
+}
+int main() {
+  for (int row_bytes : {16, 64, 80, 128, 144, 2688, 131072})
+    for (int rows : {1, 3, 16, 17})
+      for (int stage : {64, 128})
+        for (int step = 0; step < (row_bytes + stage - 1) / stage + 5; ++step) {
+          const int left = row_bytes - step * stage < stage ? row_bytes - step * stage : stage;  // bytes
+          const uint32_t bytes = rows * row_bytes;
+          for (int r = 0; r < 32; ++r)
+            for (int chunk = 0; chunk < stage / 16; ++chunk) {
+              const StageLoad l = load_rows(bytes, r * row_bytes + chunk * 16, step, stage, left, chunk * 16);
+              look(bytes, l.records, l.at, l.step_at);
+              see(r < rows && chunk * 16 < left);
+            }
+        }
+  for (int steps : {1, 2, 21})
+    for (int groups : {1, 2, 5})
+      for (int step = 0; step < steps + 5; ++step) {
+        const uint32_t bytes = groups * steps * 2048;
+        for (int g = 0; g < 8; ++g)
+          for (int at = 0; at < 2048; at += 16) {
+            const StageLoad l = load_packed(bytes, g * steps * 2048 + at, step, step < steps ? 128 : 0);
+            look(bytes, l.records, l.at, l.step_at);
+            see(g < groups && step < steps);
+          }
+      }
+}
+""")
