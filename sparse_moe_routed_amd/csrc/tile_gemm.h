@@ -142,12 +142,12 @@ __device__ __forceinline__ bool tile_find(const NtArgs& g, ProductTile& t) {
 // 16 bytes a lane from memory straight into LDS, 1 KB from `to` on.  In assembly because
 // the compiler, which cannot tell the two buffers apart in every form of read, would
 // wait for all of them before the next read; the waits are the step's own.  A load
-// past the descriptor's end writes zeros.  The compiler does not look into the assembly
-// either for what the scalar operands need: five wait states between a vector
-// instruction (a readfirstlane) that writes one and the load that reads it, one
-// after m0.
+// past the descriptor's end writes zeros.  m0, which holds `to`, is an operand, so that the
+// compiler knows what is in it.  It does not look into the assembly for what the scalar
+// operands need: five wait states between a vector instruction (a readfirstlane) that
+// writes one and the load that reads it, one after m0.
 __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t at, uint32_t step_at, Lds to) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+  __asm__ volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"{m0}"(
                        uniform(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)))),
                    "v"(at), "s"(rsrc), "s"(uniform(step_at))
                    : "memory");

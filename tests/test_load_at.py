@@ -108,3 +108,39 @@ int main() {
       }
 }
 """)
+
+
+DMA = r"""
+#include "tile_gemm.h"
+namespace moe {
+__global__ void loads(const uint8_t* p, uint8_t* out) {
+  __shared__ __attribute__((aligned(1024))) uint8_t a[1024], b[1024];
+  const Buffer d = buffer_of(p, 4096);
+  load16_to_lds(d, threadIdx.x * 16, 0, a);
+  dma16(descriptor(p, 4096), threadIdx.x * 16, 0, (Lds)b);
+  load16_to_lds(d, threadIdx.x * 16 + 1024, 0, a);
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  out[threadIdx.x] = a[threadIdx.x] + b[threadIdx.x];
+}
+}  // namespace moe
+"""
+
+
+def test_load_into_lds_and_the_compilers_own(tmp_path):
+    """dma16 between two of the compiler's loads into another buffer of LDS: m0, the
+    buffer's place, is written anew for each of the three."""
+    from sparse_moe_routed_amd import build
+
+    src, out = tmp_path / "loads.hip", tmp_path / "loads.s"
+    src.write_text(DMA)
+    subprocess.run([build.hipcc(), *build.HIPCC_FLAGS, "-I", CSRC, "--cuda-device-only", "-S", str(src), "-o", str(out)],
+                   check=True, capture_output=True)
+    places = []
+    for line in out.read_text().splitlines():
+        op = line.split()
+        if len(op) > 1 and op[1] == "m0,":
+            m0 = op[2]
+        elif op and op[0].startswith("buffer_load") and op[-1] == "lds":
+            places.append(m0)
+    assert len(places) == 3 and places[0] == places[2] != places[1]
