@@ -1123,6 +1123,8 @@ class _GroupedLinear(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
+        if dy.data_ptr() % 16:  # a part of another gradient, which may begin anywhere
+            dy = dy.clone()
         dx = grouped_input_grad(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = grouped_weight_grad(dy, x, offsets) if ctx.needs_input_grad[1] else None
         return dx, dw, None

@@ -555,3 +555,18 @@ def test_bounds_past_the_rows_leave_nothing_stale():
         for call in (moe.grouped_matmul, moe.grouped_input_grad):
             _stale(300, 64)
             assert not call(x, w, off).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R", [7, 300])
+def test_gradient_that_begins_anywhere(R):
+    """autograd hands on views: here the part of a longer gradient that begins at its
+    fourth value, six bytes in, contiguous and so not copied by contiguous()."""
+    c = Case("skew", R, 4, 64, 128)
+    x, dy, w, off = c.cuda()
+    x, w = x.requires_grad_(), w.requires_grad_()
+    head = torch.zeros(3, dtype=torch.bfloat16, device="cuda")
+    both = torch.cat([head, moe.grouped_linear(x, w, off).reshape(-1)])
+    dx, dw = torch.autograd.grad(both, (x, w), torch.cat([head, dy.reshape(-1)]))
+    want = torch.autograd.grad(moe.grouped_linear(x, w, off), (x, w), dy)
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
