@@ -573,3 +573,23 @@ def test_block_captured_and_on_two_streams(T):
                 step(x, y, p, w)
     torch.cuda.synchronize()
     assert torch.equal(both[0][0][1], want) and torch.equal(both[1][0][1], want)
+
+
+# (M, N, K) whose rows of y are no multiple of 16 bytes, in each of the larger tiles:
+# 256 x 256, 128 x 256, 128 x 128 and 64 x 128
+ODD_ROWS = [(2900, 3001, 80), (2900, 3002, 80), (2900, 3004, 80), (1100, 4399, 80), (1100, 4402, 80), (1100, 2301, 80),
+            (1100, 2302, 80), (1100, 2300, 80), (600, 2301, 96), (600, 2302, 96)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", ODD_ROWS)
+def test_odd_rows_of_large_tiles(M, N, K):
+    x, w = _rows(M, K, M + N + K), _weight(N, K, M + N)
+    W = moe.channel_pack(w.cuda())
+    q, s = moe.channel_quantize(x.cuda())
+    want = _value(*codecs.int8_row_quantize(x.float().numpy()), *codecs.int8_row_quantize(w.float().numpy()))
+    for dt in (torch.bfloat16, torch.float32):
+        store = torch.full((M * N + 1280,), 7.0, dtype=dt, device="cuda")
+        y = moe.channel_matmul(q, s, W, y=store[640:640 + M * N].view(M, N))
+        assert _same(y, torch.from_numpy(want).to(dt).float().numpy())
+        assert (store[:640] == 7.0).all() and (store[640 + M * N:] == 7.0).all()

@@ -570,3 +570,21 @@ def test_gradient_that_begins_anywhere(R):
     dx, dw = torch.autograd.grad(both, (x, w), torch.cat([head, dy.reshape(-1)]))
     want = torch.autograd.grad(moe.grouped_linear(x, w, off), (x, w), dy)
     assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.gpu
+def test_group_rows_of_the_largest_batch():
+    """2^23 rows over 256 experts, a share of them dropped."""
+    R, E = 1 << 23, 256
+    g = torch.Generator("cuda").manual_seed(1)
+    ids = torch.randint(-1, E + 1, (R // 8, 8), generator=g, device="cuda", dtype=torch.int32)
+    off, src, inv = moe.group_rows(ids, E)
+    flat = ids.reshape(-1)
+    live = (flat >= 0) & (flat < E)
+    n = int(live.sum())
+    order = torch.argsort(torch.where(live, flat, E), stable=True)[:n]
+    assert torch.equal(src[:n].long(), order) and not src[n:].any()
+    want = torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    want[order] = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert torch.equal(inv.reshape(-1), want)
+    assert off.tolist() == [0] + torch.bincount(flat[live], minlength=E).cumsum(0).tolist()
