@@ -65,10 +65,12 @@ __global__ __launch_bounds__(kQThreads) void channel_pack_codes_kernel(const uin
 // rows go from memory straight into LDS (4 buffers, 3 steps under way);
 // the weights straight into registers (WBUF operands per wave and group, WBUF - 1
 // steps under way): a weight is read by the WM waves of a column and no other, while a
-// row serves all WN.  ONCE: weights non-temporal, where one workgroup reads them.
+// row serves all WN.  ONCE: weights non-temporal, where one workgroup reads them
+// (as with experts of up to 32 rows; a single expert of 255 has them read eight times).
 // Bound by the weights: at 2688 x 1856 and 107 experts of 3.6 rows tiles of 32 x 64 read
-// them at 6.2 to 6.5 TB/s (82 and 86 us); with 192 rows an expert tiles of 128 x 128 move 4.3
-// TB/s of weights, rows and results (216 and 247 us), the matrix unit 31 and 25 % busy.
+// them at 6.2 to 6.5 TB/s (82 and 86 us).  With 192 rows an expert tiles of 128 x 128 move 4.3
+// and 4.1 TB/s of weights, rows and results (216 and 247 us), the matrix unit 31 and 25 %
+// busy: neither is full.
 template <int MODE, int BM, int BN, int WM, int WN, int WBUF, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64) void channel_tile_kernel(NtArgs g) {
   typedef NtInt8 T;
@@ -295,7 +297,9 @@ hipError_t launch_channel_tile(const NtArgs& g, hipStream_t stream, const Kernel
 // weights; many: larger ones, which read them fewer times.  The layer of 128 experts,
 // 2688 x 1856, 6 a token, us with tiles of 32 x 64 and of 128 x 128: 384 rows 195 and 240;
 // 2400 rows 260 and 286; 3600 rows 319 and 306; 24576 rows 1161 and 614 (64 x 128 lie
-// between: 238, 284, 303 and 648).
+// between: 238, 284, 303 and 648).  A single expert of every token takes the same tiles,
+// which are few for the chip: 2688 -> 3712 -> 2688 of 64 tokens 29 us, 255 39, 1024 53, 4096
+// 155; two dense products with their quantisations 27, 27, 41 and 100.
 hipError_t launch_channel_experts(int stage, const NtArgs& g, hipStream_t stream, const KernelEvents& ev) {
   if (g.M < (24 * g.E > 256 ? 24 * g.E : 256))
     return stage == 0 ? launch_channel_tile<kNtUp, 32, 64, 1, 4, 4, true>(g, stream, ev)

@@ -16,7 +16,9 @@ namespace moe {
 namespace {
 
 // rows of no expert, before offsets[0] and from offsets[E] on, set to zero: 16 bytes a
-// thread.  For the few rows that pad a batch it is a launch's time
+// thread.  For the few rows that pad a batch it is a launch's time (1 to 2 us); for those of
+// other experts their fill (24576 rows of 2688 bf16, a quarter of the experts: 124 us, without
+// 102)
 __global__ __launch_bounds__(256) void zero_rest_kernel(const int32_t* __restrict__ offsets, int E, int R,
                                                         size_t row_bytes, uint8_t* __restrict__ out) {
   const size_t head = min(max(offsets[0], 0), R) * row_bytes, tail = min(max(offsets[E], 0), R) * row_bytes;

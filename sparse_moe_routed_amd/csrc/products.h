@@ -186,8 +186,11 @@ struct StoreAt {
 // rows, which would be a part of 16 lines.  buffer(0) to buffer(NB - 1) are parts of LDS of
 // kBytes each, which take as many rows as fit at a time; chunk x of row r lies at x ^ (r % 16), on
 // other banks than its neighbours.  Row group j of a wave is j WM + wm.  Stores are
-// non-temporal: nothing of an output is read again before it has left the caches (dw of
-// 1500 rows 246 us, with ordinary stores 333; of 24576 rows in fp32 561 and 724).
+// non-temporal: of y, dx and dw nothing is read again before it has left the caches (dw of
+// 1500 rows 246 us, with ordinary stores 333; of 24576 rows in fp32 561 and 724).  What the
+// experts write is read by the next kernel, but ordinary stores gain nothing there either
+// (the layer of 640, 2048 and 4096 tokens 316, 402 and 551 us, with ordinary stores of the
+// intermediate and of the rows 317, 405 and 555).
 template <typename T, int MODE, int BM, int BN, int WM, int WN, int NB, int kBytes, typename Buffers>
 __device__ __forceinline__ void store_tile(const NtArgs& g, const StoreAt& t, Buffers buffer,
                                            const typename T::Acc (&acc)[BN / WN / 16][BM / WM / 16]) {

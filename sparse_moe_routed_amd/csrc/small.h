@@ -7,14 +7,17 @@
 namespace moe {
 
 // ---- few rows: 32 weight rows x 16 G rows per workgroup, the steps of K dealt to 8
-// waves, each one step ahead of its products; the waves' sums are joined through LDS.
-// The rows come a line at a time (8 lanes to 128 bytes) and are turned into
-// operand order in LDS that belongs to the wave.  With QUANT the rows are bf16: the
-// workgroup first takes the maxima of whole rows, while its first weights are on
-// their way, then makes the codes as the steps go.
-// Bound by latency, so 8 waves share K: a wave has 3 steps at K = 2688.  1 x 3712 x 2688
-// 7.0 us with the quantisation inside (10 MB of weights, 1.4 TB/s); 77 rows 8.2 us, their
-// quantisation 3.3 before it: past 32 rows every workgroup would repeat too much of it.
+// waves; the waves' sums are joined through LDS.  The rows come a line at a time (8 lanes
+// to 128 bytes) and are turned into operand order in LDS that belongs to the wave.  With
+// QUANT the rows are bf16: the workgroup first takes the maxima of whole rows, then makes
+// the codes as the steps go.
+// Bound by memory latencies in a row, so 8 waves share K: a wave has 3 steps at K = 2688.
+// A step's loads stand before the products of the step before it but do not run beside
+// them: chunks past K are made zero where they are loaded, which waits for the step's
+// loads, the weights' among them.  A row's maximum is a load and its wait at a time, six at
+// K = 2688, after the first step's.  1 x 3712 x 2688 7.0 us with the quantisation inside
+// (10 MB of weights, 1.4 TB/s); 77 rows 8.2 us, their quantisation 3.3 before it: past 32
+// rows every workgroup would repeat too much of it.
 constexpr int kSmallWaves = 8;
 constexpr int kSmallN = 32;
 

@@ -394,14 +394,14 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(NtArgs g) {
 }
 
 template <typename T, int MODE, int BM, int BN, int WM, int WN, int KH, int NBUF>
-hipError_t launch_tile(const NtArgs& g, hipStream_t stream, const KernelEvents& ev = KernelEvents{}) {
+hipError_t launch_tile(const NtArgs& g, hipStream_t stream) {
   const long long width = MODE >= kGradRows ? g.K : g.N, n_ct = (width + BN - 1) / BN;
   long long blocks;
   if (MODE == kGradWeights) blocks = (g.E * static_cast<long long>(g.splits) * ((g.N + BM - 1) / BM) + 7) / 8 * 8 * n_ct + g.warm;
   else if (MODE == kNtDense) blocks = (n_ct * ((g.M + BM - 1) / BM) + 7) / 8 * 8;
   else blocks = group_tiles(g.M, g.E, BM, n_ct);
   return launch_tiles(reinterpret_cast<const void*>(&tile_kernel<T, MODE, BM, BN, WM, WN, KH, NBUF>), blocks, WM * WN * 64, g,
-                      stream, ev);
+                      stream);
 }
 
 }  // namespace moe
