@@ -19,7 +19,7 @@
 //
 // What bounds it: on 8192^3, where a tile of 256 x 256 needs 64 KB of operands for each
 // 8.4 million products, the matrix unit: 1150 to 1360 TFLOP/s in bf16 in the three
-// forms (library products 1171 to 1458), and 1.95 POP/s in integers at 4096 x 3712 x 2688.
+// forms (library products 1171 to 1458), and 2.10 POP/s in integers at 4096 x 3712 x 2688.
 // Grouped by expert the weights bind, each read once: 4.1 to 4.4 TB/s with their rows and
 // results at 192 rows an expert, 5.8 TB/s at 12.
 #pragma once
